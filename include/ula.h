@@ -399,6 +399,141 @@ int ula_profile_spans_read(ula_ctx *ctx, ula_span *out, uint32_t cap, uint32_t *
 int ula_dedup_noalloc(const uint32_t *d_sel, uint32_t n, uint32_t *d_uniq,
                       int32_t *d_entry_row, uint32_t *d_n_uniq, void *stream);
 
+/* ------------------------------------------------------------ operators on rows
+ * What a model does with the cache's FP8 rows, beside the residency calls above: it
+ * packs a token's latents and rope channels into a row (the input of ula_alloc),
+ * turns its queries' rope channels, attends over the rows that a step gathered, and
+ * joins partial results over disjoint rows (TP mode's local and remote rows).  A row is
+ * ULA_ROW_BYTES bytes, 16-byte aligned: 512 e4m3 codes (the latent), 4 fp32 scales (one
+ * for each block of 128 channels: channel c stands for scale[c / 128] * code[c]), 64
+ * bf16 rope channels.
+ *
+ * These calls need no context.  Every one is asynchronous on `stream`, launches on the
+ * current device, and returns ULA_ERR_INVALID_ARG with nothing launched for bad
+ * arguments (NULL buffers with work to do, misaligned buffers or strides, sizes out of
+ * range).  They allocate nothing and keep nothing between calls.
+ */
+#define ULA_ROW_BYTES 656u
+#define ULA_ROW_LATENT 512u
+#define ULA_ROW_ROPE 64u
+#define ULA_ROW_BLOCK 128u /* latent channels that share a scale */
+#define ULA_ROPE_PAIRS 32u
+#define ULA_MAX_AXES 8u
+#define ULA_MAX_PARTS 8u
+
+enum { ULA_TYPE_BF16 = 0, ULA_TYPE_F16 = 1, ULA_TYPE_F32 = 2 };
+enum {
+  ULA_PAIR_ADJACENT = 0, /* pair j is channels (2j, 2j + 1) */
+  ULA_PAIR_HALVES = 1    /* pair j is channels (j, j + 32) */
+};
+#define ULA_ROTATE_INVERSE 1u
+
+/* Rotary positions with several axes (time, height, width for images and video; one
+ * axis for text): pair j is turned by pos[axis[j]] * freq[j] radians.  Host struct. */
+typedef struct ula_rotary {
+  uint32_t n_axes;                /* 1..ULA_MAX_AXES */
+  uint32_t pairing;               /* ULA_PAIR_* */
+  float freq[ULA_ROPE_PAIRS];     /* radians per position, finite */
+  uint8_t axis[ULA_ROPE_PAIRS];   /* < n_axes */
+} ula_rotary;
+
+/*
+ * ula_rows_rotate -- turn the rope channels of n tokens' heads.  With the angle
+ * t = pos[axis[j]][token] * freq[j], pair (a, b) becomes (a cos t - b sin t,
+ * a sin t + b cos t); ULA_ROTATE_INVERSE turns by -t (which is also the gradient:
+ * the rotation's transpose).  The angle is taken modulo one turn in 64-bit fixed
+ * point, so it is as exact at position 2^30 as at 1; the pair is turned in fp32 and
+ * rounded once.
+ *   d_pos : device int32, axis a of token t at d_pos[a * pos_axis_stride + t].
+ *   d_x   : device, channel c of head h of token t at
+ *           d_x[t * x_token_stride + h * x_head_stride + c] (strides in elements).
+ *   d_out : likewise; may be d_x itself with the same strides (in place), and must not
+ *           overlap it otherwise.
+ *   dtype : ULA_TYPE_* of d_x and d_out.
+ */
+int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const int32_t *d_pos,
+                    uint64_t pos_axis_stride, uint32_t n, uint32_t heads, uint32_t dtype,
+                    const void *d_x, uint64_t x_token_stride, uint64_t x_head_stride,
+                    void *d_out, uint64_t out_token_stride, uint64_t out_head_stride,
+                    void *stream);
+
+/*
+ * ula_rows_pack -- write n tokens' cache rows.  For each block of 128 latents
+ * scale = max(amax |x| / 448, 2^-126) and code = e4m3(x / scale), the nearest value
+ * (ties to even); the rope channels are turned as by ula_rows_rotate and stored in
+ * bf16.  A block that holds a NaN or an infinity stands for NaN throughout.
+ *   d_latent : device, channel c of token t at d_latent[t * latent_stride + c]; dtype.
+ *   d_rope   : device, d_rope[t * rope_stride + c]; dtype.
+ *   d_rows   : device-accessible, 16-byte aligned; row t at byte t * row_stride (a
+ *              multiple of 16, at least ULA_ROW_BYTES: L * 656 writes one layer of
+ *              ula_alloc's [n][L][656]).
+ */
+int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride,
+                  uint32_t n, uint32_t dtype, const void *d_latent, uint64_t latent_stride,
+                  const void *d_rope, uint64_t rope_stride, void *d_rows, uint64_t row_stride,
+                  void *stream);
+
+/*
+ * ula_rows_attend -- attention of a step's query tokens over the rows it selected.
+ * For query token (r, i) and head h, over the entries e of entry_row[r][i] with
+ * 0 <= entry_row < n_rows (others, such as the -1 of a pad, select nothing) and, with
+ * own_rows, over the rows of the request's own tokens 0..i of this step:
+ *   z[e]  = softmax_scale * <q[r][i][h], (latent(e), rope(e))>
+ *   out   = sum_e softmax(z)[e] * latent(e)          (bf16, [n_req][n_q][heads][512])
+ *   lse   = ln sum_e exp z[e]                        (fp32, [n_req][n_q][heads])
+ * A query token that selects nothing gets out = 0 and lse = -inf.
+ * Logits, maxima and sums are held in fp32; the probabilities enter the second product
+ * in 16 bits.
+ *   q         : device bf16, 576 channels (512 latent, 64 rope, already turned) at
+ *               q[r * q_req_stride + i * q_tok_stride + h * q_head_stride] (elements,
+ *               multiples of 8; 16-byte aligned).
+ *   rows      : device [n_rows][656]: one layer of ula_step_group's d_out.
+ *   entry_row : device int32 [n_req][n_q][k]: ula_step_group's d_entry_row.
+ *   own_rows  : device; row of token i of request r at byte r * own_req_stride +
+ *               i * own_tok_stride (multiples of 16), or NULL.
+ *   lse       : may be NULL.
+ *   workspace : device, 16-byte aligned, ula_rows_attend_workspace(...) bytes (may be
+ *               NULL when that is 0).  Calls that overlap on the GPU need workspaces
+ *               of their own.
+ */
+typedef struct ula_attend_args {
+  const void *q;
+  uint64_t q_req_stride, q_tok_stride, q_head_stride;
+  const void *rows;
+  const int32_t *entry_row;
+  const void *own_rows;
+  uint64_t own_req_stride, own_tok_stride;
+  void *out;
+  float *lse;
+  void *workspace;
+  uint64_t workspace_bytes;
+  uint32_t n_rows, n_req, n_q, heads, k;
+  float softmax_scale;
+} ula_attend_args;
+
+/* Bytes of workspace for these sizes on the current device (own: with own_rows). */
+uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k,
+                                   int own);
+int ula_rows_attend(const ula_attend_args *args, void *stream);
+
+/*
+ * ula_rows_join -- join `parts` partial results over disjoint rows (1..ULA_MAX_PARTS):
+ * lse = ln sum_p exp(lse_p), out = sum_p exp(lse_p - lse) * out_p, for n query heads.
+ * A part with lse -inf counts for nothing, whatever its out holds; all -inf: 0, -inf.
+ *   outs, lses : host arrays [parts] of device pointers, bf16 [n][512] (16-byte
+ *                aligned) and fp32 [n].
+ *   out, lse   : device, likewise; lse may be NULL.  out and lse may be one of the parts.
+ */
+int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t parts, uint64_t n,
+                  void *out, float *lse, void *stream);
+
+/*
+ * ula_rows_sync -- wait for `stream`, then return and clear the first error that a
+ * kernel of these operators latched on the current device (ULA_ERR_TIMEOUT: a bounded
+ * wait of ula_rows_attend expired and that call's outputs are not valid), or ULA_OK.
+ */
+int ula_rows_sync(void *stream);
+
 /*
  * TP mode, emulated on one GPU (§2 "Unified logical addresses", TP paragraph): the
  * pools of P GPUs form one distributed address space in which logical address t

@@ -1,0 +1,277 @@
+// Operators on the cache's FP8 rows: rotary positions with several axes, row packing and
+// the join of partial attention results (the attention itself: ula_attend.cu).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cmath>
+
+#include "ula.h"
+
+namespace {
+
+constexpr uint32_t kPairs = ULA_ROPE_PAIRS;
+
+// A rotary as the kernels take it: each pair's turns per position in 64-bit fixed point
+// (2^64 = one turn).  position * step modulo 2^64 is then the angle's fraction of a turn
+// in exact integer arithmetic, however far the position (an fp32 product of position and
+// frequency is off by up to 0.004 rad at position 10^5).
+struct RotaryDev {
+  unsigned long long step[kPairs];
+  uint8_t axis[kPairs];
+};
+
+bool rotary_to_dev(const ula_rotary *r, RotaryDev *out) {
+  if (!r || r->n_axes < 1 || r->n_axes > ULA_MAX_AXES || r->pairing > ULA_PAIR_HALVES) return false;
+  for (uint32_t j = 0; j < kPairs; ++j) {
+    if (r->axis[j] >= r->n_axes || !std::isfinite(r->freq[j])) return false;
+    double turns = std::fabs((double)r->freq[j]) / 6.283185307179586476925286766559;
+    turns -= std::floor(turns);
+    const unsigned long long s =
+        turns < 1.0 ? (unsigned long long)(turns * 18446744073709551616.0) : 0ull;
+    out->step[j] = r->freq[j] < 0 ? 0ull - s : s;
+    out->axis[j] = r->axis[j];
+  }
+  return true;
+}
+
+// (cos, sin) of pair j at a position; the top 32 bits of the phase are the signed
+// fraction of a turn (resolution 1.5e-9 rad), sincospi takes half turns.
+__device__ __forceinline__ float2 turn_of(const RotaryDev &r, uint32_t j, int32_t pos) {
+  const unsigned long long phase = (unsigned long long)(long long)pos * r.step[j];
+  const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c, s);
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f(float v) { return v; }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ float from_f(float v) { return v; }
+
+// ---------------------------------------------------------------- rotate
+
+struct RotateParams {
+  RotaryDev rot;
+  const int32_t *pos;
+  uint64_t pos_axis_stride;
+  uint32_t n, heads;
+  const void *x;
+  uint64_t xt, xh;
+  void *out;
+  uint64_t ot, oh;
+  float sign;  // -1 for the inverse
+};
+
+// One warp per token and head, one pair per lane.
+template <typename T, bool kHalves>
+__global__ void __launch_bounds__(256) k_rotate(const __grid_constant__ RotateParams p) {
+  const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t j = threadIdx.x & 31;
+  if (w >= (uint64_t)p.n * p.heads) return;
+  const uint32_t t = (uint32_t)(w / p.heads), h = (uint32_t)(w % p.heads);
+  const T *x = (const T *)p.x + t * p.xt + h * p.xh;
+  T *o = (T *)p.out + t * p.ot + h * p.oh;
+  const float2 cs = turn_of(p.rot, j, p.pos[p.rot.axis[j] * p.pos_axis_stride + t]);
+  const uint32_t ia = kHalves ? j : 2 * j, ib = kHalves ? j + kPairs : 2 * j + 1;
+  const float a = to_f(x[ia]), b = to_f(x[ib]), s = cs.y * p.sign;
+  o[ia] = from_f<T>(a * cs.x - b * s);
+  o[ib] = from_f<T>(a * s + b * cs.x);
+}
+
+// ---------------------------------------------------------------- pack
+
+struct PackParams {
+  RotaryDev rot;
+  const int32_t *pos;
+  uint64_t pos_axis_stride;
+  uint32_t n;
+  const void *latent;
+  uint64_t latent_stride;
+  const void *rope;
+  uint64_t rope_stride;
+  uint8_t *rows;
+  uint64_t row_stride;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;  // (the second source goes to the low byte)
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// One warp per token: lane l holds latents 16l..16l+15 (8 lanes share a block's scale)
+// and turns rope pair l.
+template <typename T, bool kHalves>
+__global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
+  const uint32_t t = blockIdx.x * 8 + (threadIdx.x >> 5), l = threadIdx.x & 31;
+  if (t >= p.n) return;
+  const T *x = (const T *)p.latent + t * p.latent_stride + 16 * l;
+  const T *r = (const T *)p.rope + t * p.rope_stride;
+  uint8_t *row = p.rows + t * p.row_stride;
+  const uint32_t ia = kHalves ? l : 2 * l, ib = kHalves ? l + kPairs : 2 * l + 1;
+  const float a = to_f(r[ia]), b = to_f(r[ib]);
+  const int32_t pos = p.pos[p.rot.axis[l] * p.pos_axis_stride + t];
+  float v[16], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = to_f(x[i]);
+    amax = max_nan(amax, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3x4(__fdiv_rn(v[4 * i], scale), __fdiv_rn(v[4 * i + 1], scale),
+                  __fdiv_rn(v[4 * i + 2], scale), __fdiv_rn(v[4 * i + 3], scale));
+  reinterpret_cast<uint4 *>(row)[l] = make_uint4(c[0], c[1], c[2], c[3]);
+  if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;
+  const float2 cs = turn_of(p.rot, l, pos);
+  __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(row + ULA_ROW_LATENT + 16);
+  o[ia] = __float2bfloat16_rn(a * cs.x - b * cs.y);
+  o[ib] = __float2bfloat16_rn(a * cs.y + b * cs.x);
+}
+
+// ---------------------------------------------------------------- join
+
+struct JoinParams {
+  const uint4 *outs[ULA_MAX_PARTS];
+  const float *lses[ULA_MAX_PARTS];
+  uint32_t parts;
+  uint64_t n;
+  uint4 *out;
+  float *lse;
+};
+
+// 64 threads per query head, 8 channels each.
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ JoinParams p) {
+  const uint64_t i = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const uint32_t c = threadIdx.x & 63;
+  if (i >= p.n) return;
+  uint4 v[ULA_MAX_PARTS];
+  float z[ULA_MAX_PARTS], top = -INFINITY;
+#pragma unroll
+  for (uint32_t q = 0; q < ULA_MAX_PARTS; ++q)
+    if (q < p.parts) {
+      z[q] = p.lses[q][i];
+      v[q] = p.outs[q][i * 64 + c];
+    }
+#pragma unroll
+  for (uint32_t q = 0; q < ULA_MAX_PARTS; ++q)
+    if (q < p.parts) top = max_nan(top, z[q]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float total = 0.f, acc[8] = {};
+#pragma unroll
+  for (uint32_t q = 0; q < ULA_MAX_PARTS; ++q)
+    if (q < p.parts && z[q] != -INFINITY) {
+      const float w = expf(z[q] - ref);
+      total += w;
+      const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[2 * k] += w * __uint_as_float(u[k] << 16);
+        acc[2 * k + 1] += w * __uint_as_float(u[k] & 0xffff0000u);
+      }
+    }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  __nv_bfloat162 b[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  p.out[i * 64 + c] = *reinterpret_cast<uint4 *>(b);
+  // (a part's lse may be the output: the row's 64 threads have all read theirs first)
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + (threadIdx.x >> 6)) : "memory");
+  if (p.lse && c == 0) p.lse[i] = ref + logf(total);
+}
+
+template <typename P>
+cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t block, cudaStream_t st, const P &p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+uint32_t type_size(uint32_t dtype) { return dtype == ULA_TYPE_F32 ? 4u : 2u; }
+bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+template <typename T>
+void (*rotate_kernel(bool halves))(RotateParams) { return halves ? k_rotate<T, true> : k_rotate<T, false>; }
+template <typename T>
+void (*pack_kernel(bool halves))(PackParams) { return halves ? k_pack<T, true> : k_pack<T, false>; }
+
+}  // namespace
+
+extern "C" int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const int32_t *d_pos,
+                               uint64_t pos_axis_stride, uint32_t n, uint32_t heads,
+                               uint32_t dtype, const void *d_x, uint64_t x_token_stride,
+                               uint64_t x_head_stride, void *d_out, uint64_t out_token_stride,
+                               uint64_t out_head_stride, void *stream) {
+  RotateParams p{};
+  if (!rotary_to_dev(rotary, &p.rot) || (flags & ~ULA_ROTATE_INVERSE) || dtype > ULA_TYPE_F32)
+    return ULA_ERR_INVALID_ARG;
+  const uint64_t work = (uint64_t)n * heads;
+  if (work == 0) return ULA_OK;
+  if (!d_pos || !d_x || !d_out || (work + 7) / 8 > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
+  if (!aligned(d_pos, 4) || !aligned(d_x, type_size(dtype)) || !aligned(d_out, type_size(dtype)))
+    return ULA_ERR_INVALID_ARG;
+  p.pos = d_pos, p.pos_axis_stride = pos_axis_stride, p.n = n, p.heads = heads;
+  p.x = d_x, p.xt = x_token_stride, p.xh = x_head_stride;
+  p.out = d_out, p.ot = out_token_stride, p.oh = out_head_stride;
+  p.sign = (flags & ULA_ROTATE_INVERSE) ? -1.f : 1.f;
+  const bool halves = rotary->pairing == ULA_PAIR_HALVES;
+  auto k = dtype == ULA_TYPE_BF16 ? rotate_kernel<__nv_bfloat16>(halves)
+           : dtype == ULA_TYPE_F16 ? rotate_kernel<__half>(halves) : rotate_kernel<float>(halves);
+  return launch(k, (work + 7) / 8, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
+                             uint64_t pos_axis_stride, uint32_t n, uint32_t dtype,
+                             const void *d_latent, uint64_t latent_stride, const void *d_rope,
+                             uint64_t rope_stride, void *d_rows, uint64_t row_stride,
+                             void *stream) {
+  PackParams p{};
+  if (!rotary_to_dev(rotary, &p.rot) || dtype > ULA_TYPE_F32) return ULA_ERR_INVALID_ARG;
+  if (n == 0) return ULA_OK;
+  if (!d_pos || !d_latent || !d_rope || !d_rows || row_stride < ULA_ROW_BYTES || row_stride % 16)
+    return ULA_ERR_INVALID_ARG;
+  if (!aligned(d_pos, 4) || !aligned(d_latent, type_size(dtype)) ||
+      !aligned(d_rope, type_size(dtype)) || !aligned(d_rows, 16))
+    return ULA_ERR_INVALID_ARG;
+  p.pos = d_pos, p.pos_axis_stride = pos_axis_stride, p.n = n;
+  p.latent = d_latent, p.latent_stride = latent_stride;
+  p.rope = d_rope, p.rope_stride = rope_stride;
+  p.rows = (uint8_t *)d_rows, p.row_stride = row_stride;
+  const bool halves = rotary->pairing == ULA_PAIR_HALVES;
+  auto k = dtype == ULA_TYPE_BF16 ? pack_kernel<__nv_bfloat16>(halves)
+           : dtype == ULA_TYPE_F16 ? pack_kernel<__half>(halves) : pack_kernel<float>(halves);
+  return launch(k, ((uint64_t)n + 7) / 8, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+extern "C" int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t parts,
+                             uint64_t n, void *out, float *lse, void *stream) {
+  if (!outs || !lses || parts < 1 || parts > ULA_MAX_PARTS || (n + 3) / 4 > 0x7fffffffull)
+    return ULA_ERR_INVALID_ARG;
+  if (n == 0) return ULA_OK;
+  JoinParams p{};
+  for (uint32_t q = 0; q < parts; ++q) {
+    if (!outs[q] || !lses[q] || !aligned(outs[q], 16) || !aligned(lses[q], 4)) return ULA_ERR_INVALID_ARG;
+    p.outs[q] = (const uint4 *)outs[q];
+    p.lses[q] = lses[q];
+  }
+  if (!out || !aligned(out, 16) || !aligned(lse, 4)) return ULA_ERR_INVALID_ARG;
+  p.parts = parts, p.n = n, p.out = (uint4 *)out, p.lse = lse;
+  return launch(k_join, (n + 3) / 4, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}

@@ -1,0 +1,588 @@
+"""The operators on FP8 rows against plain implementations in 64 bits.
+
+Tolerances, derived from the number formats:
+  * an output rounded once to bf16 (f16, f32), which hold 8 (11, 24) significant bits, is off
+    by at most half a unit of its last place, 2^-8 (2^-11, 2^-24) of its size, plus what the
+    fp32 arithmetic before it loses;
+  * rotary angles are exact to 2^-24 of a turn's half and sincospi to a few fp32 ulp:
+    each turned pair is off by at most 2^-20 of its length before the rounding;
+  * attention: logits are fp32 sums of 576 products, off by at most 2^-20 * sum |q k| *
+    scale; probabilities enter the second product in 16 bits (relative 2^-8 at worst), so
+    an output channel is off by at most 2^-8 * sum_e p_e |v_e| on top of its own rounding;
+    logits off by d change a probability by a factor of at most e^(2d); and exp in fp32
+    holds nothing below 2^-126 (its argument taken from a maximum that may lag by 2^8), so
+    each row may lose 2^-118 * |v|.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+HALF_ULP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+SMALLEST = {"bf16": 2.0 ** -133, "f16": 2.0 ** -24, "f32": 2.0 ** -149}
+
+
+def _e4m3():
+    v = np.zeros(256)
+    for b in range(256):
+        e, m = (b >> 3) & 15, b & 7
+        x = m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)
+        v[b] = math.nan if (b & 127) == 127 else (-x if b & 128 else x)
+    return v
+
+
+E4M3 = _e4m3()
+
+
+def unpack(rows: torch.Tensor):
+    """rows uint8 [n][656] -> latent, rope in float64 numpy."""
+    b = rows.cpu().numpy().reshape(-1, 656)
+    codes = E4M3[b[:, :512]]
+    scales = np.ascontiguousarray(b[:, 512:528]).view(np.float32).astype(np.float64)
+    bits = np.ascontiguousarray(b[:, 528:]).view(np.uint16).astype(np.uint32) << 16
+    return codes * np.repeat(scales, 128, axis=1), bits.view(np.float32).astype(np.float64)
+
+
+def random_rows(n, rng, spread=0.3):
+    """Rows of random codes (no NaN codes) and scales, as bytes."""
+    codes = rng.integers(0, 256, (n, 512), dtype=np.uint8)
+    codes[(codes & 127) == 127] = 0
+    scales = (np.exp(spread * rng.standard_normal((n, 4))) / 200).astype(np.float32)
+    rope = rng.standard_normal((n, 64)).astype(np.float32).view(np.uint32) >> 16
+    return torch.from_numpy(np.concatenate(
+        [codes, scales.view(np.uint8).reshape(n, 16),
+         rope.astype(np.uint16).view(np.uint8).reshape(n, 128)], axis=1)).cuda()
+
+
+# ------------------------------------------------------------------------------- rotary
+
+def make_rotary(rng, axes, pairing):
+    from serving_step_sparse_gb300 import rows
+    freq = np.float32(10000.0) ** (-np.arange(32, dtype=np.float32) / 32)
+    axis = rng.integers(0, axes, 32)
+    axis[0], axis[31] = 0, axes - 1
+    return rows.Rotary(freq.tolist(), axis.tolist(), pairing), freq.astype(np.float64), axis
+
+
+def turned(x, pos, freq, axis, pairing, sign=1.0):
+    x = np.asarray(x, dtype=np.float64)
+    ang = pos.astype(np.float64)[axis].T * freq[None]            # [n][32]
+    ang = ang.reshape(ang.shape[0], *([1] * (x.ndim - 2)), 32)
+    c, s = np.cos(ang), sign * np.sin(ang)
+    out = np.empty_like(x)
+    ia, ib = ((slice(0, None, 2), slice(1, None, 2)) if pairing == "adjacent"
+              else (slice(0, 32), slice(32, 64)))
+    a, b = x[..., ia], x[..., ib]
+    out[..., ia], out[..., ib] = a * c - b * s, a * s + b * c
+    length = np.empty_like(x)
+    length[..., ia] = length[..., ib] = np.hypot(a, b)
+    return out, length
+
+
+def positions(rng, axes, n, top=131072):
+    pos = rng.integers(0, top, (axes, n)).astype(np.int32)
+    pos[0, 0] = 0
+    if n > 2:
+        pos[0, 1], pos[axes - 1, 2] = 2 ** 30 + 12345, -7
+    return pos
+
+
+def check_turned(got, x, pos, freq, axis, pairing, dtype, sign=1.0):
+    want, length = turned(x, pos, freq, axis, pairing, sign)
+    tol = HALF_ULP[dtype] * np.abs(want) * 1.01 + 2.0 ** -20 * length + SMALLEST[dtype]
+    assert (np.abs(got.double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,heads,axes", [(1, 1, 1), (3, 5, 3), (17, 64, 2), (700, 1, 4), (33, 128, 8)])
+def test_rotate(n, heads, axes, dtype, pairing):
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(n * 131 + heads)
+    rot, freq, axis = make_rotary(rng, axes, pairing)
+    x = torch.from_numpy(rng.standard_normal((n, heads, 64))).to(DT[dtype]).cuda()
+    pos = positions(rng, axes, n)
+    pos_d = torch.from_numpy(pos).cuda()
+    out = rows.rotate(x, pos_d, rot)
+    check_turned(out, x.double().cpu(), pos, freq, axis, pairing, dtype)
+    back = rows.rotate(x, pos_d, rot, inverse=True)
+    check_turned(back, x.double().cpu(), pos, freq, axis, pairing, dtype, sign=-1.0)
+    y = x.clone()
+    assert rows.rotate(y, pos_d, rot, out=y) is y and torch.equal(y, out)  # in place
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("offset,head_stride,token_extra", [(0, 64, 0), (512, 576, 0), (8, 80, 16),
+                                                            (1, 65, 3), (2, 66, 2), (512, 576, 1)])
+def test_rotate_strides_and_alignment(dtype, offset, head_stride, token_extra):
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(offset + head_stride)
+    n, heads = 37, 6
+    for pairing in ("adjacent", "halves"):
+        rot, freq, axis = make_rotary(rng, 3, pairing)
+        store = torch.from_numpy(rng.standard_normal(
+            offset + n * (heads * head_stride + token_extra) + 64)).to(DT[dtype]).cuda()
+        view = store.as_strided((n, heads, 64), (heads * head_stride + token_extra, head_stride, 1), offset)
+        x = view.clone()
+        pos = positions(rng, 5, n)
+        pos_d = torch.from_numpy(pos).cuda()
+        dense = rows.rotate(view, pos_d, rot)            # strided in, dense out
+        check_turned(dense, x.double().cpu(), pos, freq, axis, pairing, dtype)
+        before = store.clone()
+        rows.rotate(view, pos_d, rot, out=view)          # strided, in place
+        assert torch.equal(view, dense)
+        mask = torch.ones_like(store, dtype=torch.bool)
+        mask.as_strided(view.shape, view.stride(), offset).fill_(False)
+        assert torch.equal(store[mask], before[mask])    # nothing beside the channels
+    assert torch.equal(rows.rotate(x[:, 0], pos_d, rot), dense[:, 0])  # no head axis
+
+
+def test_rotate_gradient():
+    """The inverse turn is the gradient: <g, rotate(x)> = <rotate_inverse(g), x>, and it agrees
+    with central differences of the turn (linear in x, so exact up to fp32 rounding: each inner
+    product of 64 terms is off by at most 2^-18 of the vectors' lengths)."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(3)
+    rot, freq, axis = make_rotary(rng, 3, "halves")
+    pos = torch.from_numpy(positions(rng, 3, 9)).cuda()
+    x = torch.from_numpy(rng.standard_normal((9, 2, 64))).float().cuda()
+    g = torch.from_numpy(rng.standard_normal((9, 2, 64))).float().cuda()
+    grad = rows.rotate(g, pos, rot, inverse=True).double()
+    size = (x.norm() * g.norm()).double()
+    assert abs((g.double() * rows.rotate(x, pos, rot).double()).sum() - (grad * x.double()).sum()) <= 2.0 ** -18 * size
+    for _ in range(8):
+        d = torch.from_numpy(rng.standard_normal((9, 2, 64))).float().cuda()
+        step = (rows.rotate(x + d, pos, rot).double() - rows.rotate(x - d, pos, rot).double()) / 2
+        assert abs((g.double() * step).sum() - (grad * d.double()).sum()) <= 2.0 ** -18 * (
+            g.norm() * (x.norm() + d.norm())).double()
+
+
+# ------------------------------------------------------------------------------- pack
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,layers", [(1, 1), (7, 4), (8, 1), (129, 3), (1000, 1)])
+def test_pack(n, layers, dtype, pairing):
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(n * 7 + layers)
+    rot, freq, axis = make_rotary(rng, 3, pairing)
+    x = rng.standard_normal((n, 512)) * np.exp(rng.standard_normal((n, 1)))
+    x[0, :128] = 0                      # a block of zeros
+    x[n // 2, 128:256] *= 1e-4          # blocks of other sizes
+    x[n - 1, 384:] *= 50
+    latent = torch.from_numpy(x).to(DT[dtype]).cuda()
+    rope = torch.from_numpy(rng.standard_normal((n, 64))).to(DT[dtype]).cuda()
+    pos = positions(rng, 3, n)
+    dest = torch.full((n, layers, 656), 0xA5, dtype=torch.uint8, device="cuda")
+    got = rows.pack(latent, rope, torch.from_numpy(pos).cuda(), rot, dest[:, layers - 1])
+    assert got.data_ptr() == dest[:, layers - 1].data_ptr()
+    assert (dest[:, :layers - 1] == 0xA5).all()
+    b = got.cpu().numpy()
+    v = latent.double().cpu().numpy().reshape(n, 4, 128)
+    scale = np.ascontiguousarray(b[:, 512:528]).view(np.float32).astype(np.float64)
+    want = np.maximum(np.abs(v).max(-1) / 448, 2.0 ** -126)
+    assert (np.abs(scale - want) <= 2.0 ** -23 * want).all()
+    codes = E4M3[b[:, :512]].reshape(n, 4, 128)
+    y = v / scale[..., None]
+    # the nearest e4m3 value: half the spacing around |y|, and the quotient's fp32 roundings
+    spacing = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -6))) - 3)
+    assert (np.abs(codes - y) <= spacing / 2 + 2.0 ** -21 * np.abs(y)).all()
+    got_rope = torch.from_numpy(np.ascontiguousarray(b[:, 528:])).view(torch.bfloat16)
+    check_turned(got_rope, rope.double().cpu(), pos, freq, axis, pairing, "bf16")
+
+
+def test_pack_not_finite():
+    """A block with a NaN or an infinity stands for NaN throughout; its neighbours are whole."""
+    from serving_step_sparse_gb300 import rows
+    rot = rows.Rotary([0.0] * 32)
+    latent = torch.ones(3, 512, device="cuda")
+    latent[0, 5], latent[1, 200], latent[2, 511] = math.nan, math.inf, -math.inf
+    got = rows.pack(latent, torch.zeros(3, 64, device="cuda"),
+                    torch.zeros(3, dtype=torch.int32, device="cuda"), rot)
+    lat, rope = unpack(got)
+    for t, blk in ((0, 0), (1, 1), (2, 3)):
+        v = lat[t].reshape(4, 128)
+        assert np.isnan(v[blk]).all()
+        rest = [b for b in range(4) if b != blk]
+        assert (np.abs(v[rest] - 1) <= 2.0 ** -20).all()   # 1 is the block's largest: code 448
+    assert (rope == 0).all()
+
+
+def test_pack_strides():
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(5)
+    rot, _, _ = make_rotary(rng, 2, "adjacent")
+    n = 21
+    for dtype in DT.values():
+        wide = torch.from_numpy(rng.standard_normal((n, 600))).to(dtype).cuda()
+        pos = torch.from_numpy(positions(rng, 2, n)).cuda()
+        for at in (0, 1, 8, 13):                      # an unaligned start, rows apart
+            latent, rope = wide[:, at:at + 512], wide[:, at + 513:at + 577]
+            want = rows.pack(latent.contiguous(), rope.contiguous(), pos, rot)
+            assert torch.equal(rows.pack(latent, rope, pos, rot), want)
+        turned_over = torch.flip(wide, [1]).t().contiguous().t()   # channels apart
+        assert torch.equal(rows.pack(turned_over[:, :512], turned_over[:, 512:576], pos, rot),
+                           rows.pack(turned_over[:, :512].contiguous(),
+                                     turned_over[:, 512:576].contiguous(), pos, rot))
+
+
+# ------------------------------------------------------------------------------- attend
+
+def attend64(q, rows, entry, scale, own=None):
+    """(out, lse, slack): slack bounds an output channel's error per unit (see the top)."""
+    R, Q, H, _ = q.shape
+    lat_all, rope_all = unpack(rows) if rows.shape[0] else (np.zeros((0, 512)), np.zeros((0, 64)))
+    qd = q.double().cpu().numpy()
+    e = entry.cpu().numpy()
+    out, lse = np.zeros((R, Q, H, 512)), np.full((R, Q, H), -np.inf)
+    slack, zslack = np.zeros((R, Q, H, 512)), np.zeros((R, Q, H))
+    for r in range(R):
+        for i in range(Q):
+            idx = e[r, i][(e[r, i] >= 0) & (e[r, i] < rows.shape[0])]
+            lat, rope = lat_all[idx], rope_all[idx]
+            if own is not None:
+                ol, orp = unpack(own[r, :i + 1].contiguous())
+                lat, rope = np.concatenate([lat, ol]), np.concatenate([rope, orp])
+            if not len(lat):
+                continue
+            keys = np.concatenate([lat, rope], axis=1)
+            z = qd[r, i] @ keys.T * scale
+            zslack[r, i] = (2.0 ** -20 * abs(scale) * (np.abs(qd[r, i]) @ np.abs(keys).T)).max(-1)
+            top = z.max(-1, keepdims=True)
+            p = np.exp(z - top)
+            lse[r, i] = (top + np.log(p.sum(-1, keepdims=True)))[:, 0]
+            p /= p.sum(-1, keepdims=True)
+            out[r, i] = p @ lat
+            slack[r, i] = p @ np.abs(lat) + 2.0 ** -110 * np.abs(lat).sum(0)
+    return out, lse, slack, zslack
+
+
+def check_attend(got, want):
+    (o, z), (out, lse, slack, zslack) = got, want
+    o, z = o.double().cpu().numpy(), z.double().cpu().numpy()
+    none = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(z), none)
+    assert (o[none] == 0).all()
+    ok = ~none
+    # lse: the largest logit's error, and exp, log and the sum in fp32
+    assert (np.abs(z - lse)[ok] <= (zslack + 2.0 ** -20 * (1 + np.abs(lse)))[ok]).all()
+    tol = 2.0 ** -8 * np.abs(out) * 1.01 + (2.0 ** -8 + np.expm1(2 * zslack[..., None])) * slack + 2.0 ** -133
+    assert (np.abs(o - out) <= tol)[ok].all()
+
+
+def attend_case(R, Q, H, K, n_rows, seed, pads=0.0, own=False, qscale=1.0, spread=0.3):
+    rng = np.random.default_rng(seed)
+    q = torch.from_numpy(qscale * rng.standard_normal((R, Q, H, 576))).to(torch.bfloat16).cuda()
+    rows = random_rows(n_rows, rng, spread)
+    entry = rng.integers(0, max(n_rows, 1), (R, Q, K)).astype(np.int32)
+    if pads:
+        entry[rng.random(entry.shape) < pads] = -1
+    own_rows = random_rows(R * Q, rng, spread).view(R, Q, 656) if own else None
+    return q, rows, torch.from_numpy(entry).cuda(), own_rows
+
+
+SCALE = 192 ** -0.5
+
+
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("R,Q,H,K", [
+    (1, 1, 1, 1), (1, 1, 16, 127), (1, 1, 17, 128), (2, 3, 32, 129), (1, 2, 33, 255),
+    (3, 1, 64, 256), (1, 1, 65, 300), (2, 2, 128, 517), (1, 1, 130, 64), (1, 4, 20, 2048),
+    (40, 1, 8, 96), (1, 1, 64, 8192)])
+def test_attend(R, Q, H, K, own):
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(R, Q, H, K, max(1, 3 * K // 2), R * 1000 + H + K, own=own)
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(got, attend64(q, kv, entry, SCALE, own_rows))
+    rows.sync()
+
+
+@pytest.mark.parametrize("H", [5, 64, 100])
+@pytest.mark.parametrize("own", [False, True])
+def test_attend_pads(H, own):
+    """Pads anywhere, whole tiles of pads, a query without rows, entries out of range."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(3, 2, H, 700, 500, H, pads=0.3, own=own)
+    entry[0, 0] = -1
+    entry[0, 1, :400] = -1
+    entry[1, 0, 130:] = -1
+    entry[1, 1, ::2] = torch.iinfo(torch.int32).min
+    entry[2, 0, 1::3] = 500
+    entry[2, 1, 5] = torch.iinfo(torch.int32).max
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(got, attend64(q, kv, entry, SCALE, own_rows))
+
+
+def test_attend_empty_lengths():
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(2, 3, 24, 0, 4, 1, own=True)
+    check_attend(rows.attend(q, kv, entry, SCALE), attend64(q, kv, entry, SCALE))
+    check_attend(rows.attend(q, kv, entry, SCALE, own_rows=own_rows),
+                 attend64(q, kv, entry, SCALE, own_rows))
+    entry = torch.zeros(2, 3, 5, dtype=torch.int32, device="cuda")
+    none = kv[:0].contiguous()
+    check_attend(rows.attend(q, none, entry, SCALE), attend64(q, none, entry, SCALE))
+    out, lse = rows.attend(q[:0], kv, entry[:0], SCALE)
+    assert out.shape == (0, 3, 24, 512) and lse.shape == (0, 3, 24)
+    out, lse = rows.attend(q[:, :, :0], kv, entry, SCALE)
+    assert out.shape == (2, 3, 0, 512)
+
+
+@pytest.mark.parametrize("qscale,spread", [(30.0, 0.3), (1e-3, 0.3), (1.0, 4.0), (8.0, 2.0)])
+def test_attend_sizes_of_values(qscale, spread):
+    """Peaked and flat distributions, scales over many orders: running maxima that move."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(2, 2, 40, 900, 900, 77, own=True, qscale=qscale, spread=spread)
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(got, attend64(q, kv, entry, SCALE, own_rows))
+
+
+def test_attend_growing_logits():
+    """Rows ordered by their logit, ascending and descending: the maximum moves in every tile,
+    or is the first one; and a negative scale."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(1, 1, 48, 1500, 1500, 5, qscale=20.0)
+    q[:] = q[:, :, :1]
+    lat, rope = unpack(kv)
+    z = np.concatenate([lat, rope], 1) @ q[0, 0, 0].double().cpu().numpy()
+    for order in (np.argsort(z), np.argsort(-z)):
+        entry[0, 0] = torch.from_numpy(order.astype(np.int32)).cuda()
+        for scale in (SCALE, -SCALE):
+            check_attend(rows.attend(q, kv, entry, scale), attend64(q, kv, entry, scale))
+
+
+def test_attend_block_sizes_differ():
+    """Blocks of channels, tokens and heads of very different sizes keep their own precision."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(1, 2, 64, 400, 400, 9)
+    sc = kv[:, 512:528].contiguous().view(torch.float32)
+    sc[:, 1] *= 2.0 ** -40
+    sc[:, 2] *= 2.0 ** 20
+    sc[:200, 3] *= 2.0 ** -60
+    sc[300:] *= 2.0 ** 10
+    kv[:, 512:528] = sc.view(torch.uint8)
+    q[:, :, ::3] *= 2.0 ** -50
+    q[:, :, 1::3] *= 2.0 ** -20
+    q[:, :, :, 256:384] *= 2.0 ** -30     # block 2's share of the logits
+    check_attend(rows.attend(q, kv, entry, SCALE), attend64(q, kv, entry, SCALE))
+
+
+def test_attend_not_finite():
+    """A NaN row poisons the queries that select it and no others; in rows that a query does
+    not select, NaN and infinity count for nothing; so does a NaN head for other heads."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(1, 3, 33, 260, 300, 21)
+    bad = kv.clone()
+    bad[299, 512:528] = torch.tensor([math.nan] * 4).view(torch.uint8).cuda()
+    bad[298, :512] = 0x7F                                       # NaN codes under whole scales
+    bad[297, 528:] = 0xFF                                       # NaN rope
+    entry = entry.clamp_max(296)
+    clean = rows.attend(q, kv, entry, SCALE)
+    same = rows.attend(q, bad, entry, SCALE)
+    assert torch.equal(clean[0], same[0]) and torch.equal(clean[1], same[1])
+    entry[0, 1, 77] = -1
+    entry[0, 0, 3], entry[0, 2, 200] = 299, 298
+    out, lse = rows.attend(q, bad, entry, SCALE)
+    assert torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0]).all()
+    assert torch.isnan(out[0, 2]).all() and torch.isnan(lse[0, 2]).all()
+    want = attend64(q[:, 1:2], kv, entry[:, 1:2], SCALE)
+    check_attend((out[:, 1:2], lse[:, 1:2]), want)
+    entry[0, 0, 3], entry[0, 2, 200] = 0, 297
+    out, lse = rows.attend(q, bad, entry, SCALE)
+    assert torch.isnan(out[0, 2]).all() and not torch.isnan(out[0, :2]).any()
+    q2 = q.clone()
+    q2[0, 0, 7, 100] = math.nan
+    q2[0, 0, 8, 570] = math.inf
+    o1, l1 = rows.attend(q2, kv, entry.clamp_max(296), SCALE)
+    o0, l0 = rows.attend(q, kv, entry.clamp_max(296), SCALE)
+    others = [h for h in range(33) if h not in (7, 8)]
+    assert torch.equal(o1[0, 0, others], o0[0, 0, others]) and torch.equal(l1[0, 0, others], l0[0, 0, others])
+    assert torch.isnan(o1[0, 0, 7]).all() and torch.isnan(l1[0, 0, 7])
+    assert torch.isnan(o1[0, 0, 8]).all()
+
+
+def test_attend_strides():
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(3, 2, 12, 200, 150, 4, own=True)
+    want = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    wide = torch.zeros(3, 2, 12, 640, dtype=torch.bfloat16, device="cuda")
+    wide[..., 8:584] = q
+    heads_first = q.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+    odd = torch.zeros(3, 2, 12, 577, dtype=torch.bfloat16, device="cuda")
+    odd[..., 1:] = q
+    own_wide = torch.zeros(3, 4, 2, 656, dtype=torch.uint8, device="cuda")
+    own_wide[:, 1:3, 1] = own_rows
+    back = torch.zeros(200, 2, 3, dtype=torch.int32, device="cuda")
+    back[:] = entry.permute(2, 1, 0)
+    for qq in (wide[..., 8:584], heads_first, odd[..., 1:]):
+        got = rows.attend(qq, kv, back.permute(2, 1, 0), SCALE, own_rows=own_wide[:, 1:3, 1])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_attend_far_rows():
+    """A gathered buffer past 2^32 bytes."""
+    from serving_step_sparse_gb300 import rows
+    n = 2 ** 32 // 656 + 1000
+    big = torch.zeros(n, 656, dtype=torch.uint8, device="cuda")
+    q, kv, entry, _ = attend_case(1, 1, 16, 300, 300, 6)
+    big[-300:] = kv
+    want = rows.attend(q, kv, entry, SCALE)
+    got = rows.attend(q, big, entry + (n - 300), SCALE)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attend_repeats():
+    """The same call gives the same bits."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(4, 3, 64, 1000, 900, 8, own=True)
+    a = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    for _ in range(5):
+        b = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_attend_other_stream():
+    """Calls on streams of their own: inputs and temporaries are held until they have run."""
+    from serving_step_sparse_gb300 import rows
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    cases = [attend_case(2, 2, 40, 600, 500, 30 + s) for s in range(3)]
+    want = [rows.attend(q, kv, e, SCALE) for q, kv, e, _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, (q, kv, e, _) in zip(streams, cases):
+            odd = torch.zeros(*q.shape[:3], 577, dtype=torch.bfloat16, device="cuda")
+            odd[..., 1:] = q
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(rows.attend(odd[..., 1:], kv, e, SCALE, stream=s))
+            del odd
+            torch.zeros(2, 2, 40, 577, dtype=torch.bfloat16, device="cuda").fill_(7.0)
+    torch.cuda.synchronize()
+    for i, (o, z) in enumerate(got):
+        assert torch.equal(o, want[i % 3][0]) and torch.equal(z, want[i % 3][1])
+
+
+# ------------------------------------------------------------------------------- join
+
+def join64(outs, lses):
+    z = np.stack([x.double().cpu().numpy() for x in lses])
+    o = np.stack([x.double().cpu().numpy() for x in outs])
+    top = z.max(0)
+    ref = np.where(np.isneginf(top), 0.0, top)
+    w = np.exp(z - ref)
+    total = w.sum(0)
+    p = w / np.where(total == 0, 1, total)
+    o = np.where(np.isneginf(z)[..., None], 0, o)
+    with np.errstate(divide="ignore"):
+        lse = ref + np.log(total)
+    return (o * p[..., None]).sum(0), lse, (np.abs(o) * p[..., None]).sum(0)
+
+
+@pytest.mark.parametrize("parts", [1, 2, 3, 8])
+@pytest.mark.parametrize("shape", [(1,), (3,), (5, 7), (2, 3, 64)])
+def test_join(parts, shape):
+    """fp32 arithmetic (each weight and sum off by at most 2^-20), rounded once to bf16."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(parts)
+    outs = [torch.from_numpy(rng.standard_normal((*shape, 512))).to(torch.bfloat16).cuda() for _ in range(parts)]
+    lses = [torch.from_numpy(5 * rng.standard_normal(shape)).float().cuda() for _ in range(parts)]
+    for p in range(parts):
+        lses[p].view(-1)[p % lses[p].numel()] = -math.inf
+        lses[p].view(-1)[-1] = -math.inf
+        outs[p].view(-1, 512)[-1] = math.nan                    # (not read where lse is -inf)
+    want, lse, slack = join64(outs, lses)
+    o, z = rows.join(outs, lses)
+    o, z = o.double().cpu().numpy(), z.double().cpu().numpy()
+    none = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(z), none) and (o[none] == 0).all()
+    assert (np.abs(z - lse)[~none] <= 2.0 ** -20 * (1 + np.abs(lse[~none]))).all()
+    assert (np.abs(o - want) <= 2.0 ** -8 * 1.01 * np.abs(want) + 2.0 ** -18 * slack + 2.0 ** -133).all()
+    keep = [x.clone() for x in outs], [x.clone() for x in lses]
+    again = rows.join(outs, lses, out=outs[0], lse=lses[0])     # in place of the first part
+    assert again[0] is outs[0]
+    first = rows.join(*keep)
+    assert torch.equal(first[0], outs[0]) and torch.equal(first[1], lses[0])
+
+
+def test_join_of_attends():
+    """Two halves of a selection, joined, against the whole one (TP: local and remote rows)."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(3, 2, 24, 500, 400, 12, pads=0.05)
+    odd = (entry & 1).bool()
+    a = rows.attend(q, kv, torch.where(odd, entry, -1), SCALE)
+    b = rows.attend(q, kv, torch.where(odd, -1, entry), SCALE)
+    o, z = rows.join([a[0], b[0]], [a[1], b[1]])
+    out, lse, slack, zslack = attend64(q, kv, entry, SCALE)
+    assert (np.abs(z.double().cpu().numpy() - lse) <= zslack + 2.0 ** -19 * (1 + np.abs(lse))).all()
+    # each half was rounded to bf16 as well
+    tol = 2.0 ** -8 * 1.01 * np.abs(out) + (2.0 ** -8 + 2.0 ** -8 + np.expm1(2 * zslack[..., None])) * slack
+    assert (np.abs(o.double().cpu().numpy() - out) <= tol).all()
+
+
+# ------------------------------------------------------------------------------- refusals
+
+def test_refusals():
+    from serving_step_sparse_gb300 import rows, ula
+    q, kv, entry, own_rows = attend_case(2, 2, 8, 16, 16, 1, own=True)
+    pos = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    rot = rows.Rotary([1.0] * 32)
+    x = torch.zeros(4, 8, 64, device="cuda")
+    bad = [
+        lambda: rows.Rotary([1.0] * 31),
+        lambda: rows.Rotary([1.0] * 32, [8] * 32),
+        lambda: rows.Rotary([1.0] * 32, pairing="thirds"),
+        lambda: rows.rotate(x[..., :32], pos, rot),
+        lambda: rows.rotate(x.double(), pos, rot),
+        lambda: rows.rotate(x, pos.long(), rot),
+        lambda: rows.rotate(x, pos[:, :3], rot),
+        lambda: rows.rotate(x, pos, rows.Rotary([1.0] * 32, [0] * 31 + [1])),
+        lambda: rows.rotate(x, pos, rot, out=x.half()),
+        lambda: rows.rotate(x, pos.cpu(), rot),
+        lambda: rows.rotate(x.cpu(), pos.cpu(), rot),
+        lambda: rows.pack(x[:, 0], x[:, 0], pos, rot),
+        lambda: rows.pack(torch.zeros(4, 512, device="cuda"), x[:, 0].half(), pos, rot),
+        lambda: rows.pack(torch.zeros(4, 512, device="cuda"), x[:, 0], pos, rot,
+                          torch.zeros(4, 640, dtype=torch.uint8, device="cuda")),
+        lambda: rows.pack(torch.zeros(4, 512, device="cuda"), x[:, 0], pos, rot,
+                          torch.zeros(1, 656, dtype=torch.uint8, device="cuda").expand(4, 656)),
+        lambda: rows.attend(q.float(), kv, entry, SCALE),
+        lambda: rows.attend(q[..., :512], kv, entry, SCALE),
+        lambda: rows.attend(q, kv[:, :640], entry, SCALE),
+        lambda: rows.attend(q, kv[::2], entry, SCALE),
+        lambda: rows.attend(q, kv, entry.long(), SCALE),
+        lambda: rows.attend(q, kv, entry[:1], SCALE),
+        lambda: rows.attend(q, kv, entry, SCALE, own_rows=own_rows[:1]),
+        lambda: rows.attend(q, kv, entry, SCALE, out=torch.empty(2, 2, 8, 512, device="cuda")),
+        lambda: rows.attend(q, kv.cpu(), entry, SCALE),
+        lambda: rows.join([], []),
+        lambda: rows.join([q[..., :512]], [entry[..., :8].float()]),
+        lambda: rows.join([torch.zeros(3, 512, dtype=torch.bfloat16, device="cuda")] * 9,
+                          [torch.zeros(3, device="cuda")] * 9),
+        lambda: rows.join([torch.zeros(3, 512, dtype=torch.bfloat16, device="cuda")],
+                          [torch.zeros(4, device="cuda")]),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {i} was accepted")
+    lat = torch.zeros(4, 512, device="cuda")
+    store = torch.zeros(4 * 656 + 64, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ula.UlaError) as e:                       # rows that are not 16-byte aligned
+        rows.pack(lat, x[:, 0], pos, rot, store[8:8 + 4 * 656].view(4, 656))
+    assert e.value.code == ula.ERR_INVALID_ARG
+    with pytest.raises(ula.UlaError):
+        rows.pack(lat, x[:, 0], pos, rot, store.as_strided((4, 656), (664, 1)))
+    with pytest.raises(ula.UlaError):
+        rows.rotate(x, pos, rows.Rotary([math.inf] + [1.0] * 31))
+    with pytest.raises(ula.UlaError):
+        rows.attend(q, store[8:8 + 3 * 656].view(3, 656), entry, SCALE)
+    rows.sync()

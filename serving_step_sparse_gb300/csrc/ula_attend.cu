@@ -1,4 +1,20 @@
 // Attention over the cache's FP8 rows (ula_rows_attend).
+//
+// For a query token and its entries e, with codes c (e4m3), block scales s, rope k and a
+// head's query (q_0..q_3 latent blocks, q_r rope):
+//   z[e] = c0 * (sum_b s_b(e) <q_b, c_b(e)> + <q_r, k(e)>),  p = exp2(z - m),
+//   out  = sum_e p[e] s_b(e) c_b(e) / sum_e p[e]   (channels of block b),
+// with c0 = softmax_scale * log2(e) and m a running maximum.
+//
+// Both products run on the tensor cores with the rows transposed into the M dimension:
+// S^T[128 rows][heads] = C_b Q_b^T for each block b (and the rope part), and
+// O^T[128 channels][heads] += C_b^T P_b^T.  So any head count fits in N without waste, a
+// thread of the softmax owns one row (its scales are four registers), and the codes serve
+// both products from one bf16 copy in shared memory (K-major for the first, MN-major for
+// the second).  A code is exact in bf16 and its scale multiplies fp32 accumulators, so the
+// logits are as exact as fp32 sums; the probabilities times the scales enter the second
+// product in bf16 (half a unit 2^-9 relative on each, which averages out over the rows;
+// bf16 and not f16 since scales may span many orders).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -8,101 +24,737 @@ namespace {
 
 __device__ int g_status;  // the first error that a kernel of this file latched
 
-constexpr uint32_t kChannels = ULA_ROW_LATENT + ULA_ROW_ROPE;
+constexpr uint32_t kTile = 128;                      // rows per tile
+constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
+constexpr uint32_t kGroups = 9;                      // 8 of latents, 1 of rope
+constexpr uint32_t kWarps = 16;
+constexpr uint32_t kThreads = kWarps * 32;           // 128 registers each
+constexpr uint32_t kColS = 256;                      // TMEM: O^T in columns 0.., S^T from here
 
-__device__ __forceinline__ float2 e4m3x2_to_f(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  return __half22float2(*reinterpret_cast<__half2 *>(&h));
+struct AttendParams {
+  ula_attend_args a;
+  unsigned long long total;  // tiles of all items (an item: a query token and a tile of heads)
+  uint32_t blocks;           // block c takes tiles [c * total / blocks, (c + 1) * total / blocks)
+  uint32_t tiles;            // tiles per item
+  uint32_t head_tiles;
+  uint32_t keys;             // entries per query token, own rows included
+  float c0;
+  float *part_out;           // [2 * blocks][NH][512]: unfinished items' results, normalised
+  float *part_lse;           // [2 * blocks][NH]: their log2 sums
+};
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long v;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(v));
+  return v;
 }
 
-// One warp per query token and head: lane l holds latents 16l..16l+15 and rope channels
-// 2l, 2l+1 of the query; one row at a time with a running maximum and sum.
-__global__ void __launch_bounds__(256) k_attend(const ula_attend_args a) {
-  const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const uint32_t l = threadIdx.x & 31;
-  const uint64_t n = (uint64_t)a.n_req * a.n_q * a.heads;
-  if (w >= n) return;
-  const uint32_t h = (uint32_t)(w % a.heads);
-  const uint64_t tok = w / a.heads;
-  const uint32_t r = (uint32_t)(tok / a.n_q), i = (uint32_t)(tok % a.n_q);
-  const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q + r * a.q_req_stride + i * a.q_tok_stride + h * a.q_head_stride;
-  float ql[16], acc[16] = {};
-#pragma unroll
-  for (int c = 0; c < 16; ++c) ql[c] = __bfloat162float(q[16 * l + c]);
-  const float q0 = __bfloat162float(q[ULA_ROW_LATENT + 2 * l]), q1 = __bfloat162float(q[ULA_ROW_LATENT + 2 * l + 1]);
-  float top = -INFINITY, total = 0.f;
-  const uint32_t keys = a.k + (a.own_rows ? i + 1 : 0);
-  for (uint32_t e = 0; e < keys; ++e) {
-    const uint8_t *row;
-    if (e < a.k) {
-      const int32_t u = a.entry_row[tok * a.k + e];
-      if (u < 0 || (uint32_t)u >= a.n_rows) continue;
-      row = (const uint8_t *)a.rows + (uint64_t)u * ULA_ROW_BYTES;
-    } else {
-      row = (const uint8_t *)a.own_rows + r * a.own_req_stride + (e - a.k) * a.own_tok_stride;
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done;
+}
+
+// Bounded: after 1 s, or once another thread of the block has given up, it returns false.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    if (mbar_try(bar, parity)) return true;
+    if (*gave_up) return false;
+    if (global_ns() - t0 > 1000000000ull) {
+      *gave_up = 1;
+      atomicCAS(&g_status, 0, (int)ULA_ERR_TIMEOUT);
+      return false;
     }
-    const uint4 codes = reinterpret_cast<const uint4 *>(row)[l];
-    const float s = reinterpret_cast<const float *>(row + ULA_ROW_LATENT)[l >> 3];
-    const __nv_bfloat162 rope = reinterpret_cast<const __nv_bfloat162 *>(row + ULA_ROW_LATENT + 16)[l];
-    const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-    float v[16], z = 0.f;
+  }
+}
+
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait_slow(bar, parity, gave_up);
+}
+
+// By a whole warp: the same answer in every lane, so that a warp leaves its work as one.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, gave_up));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One MMA of K = 16: D[128][N] (+)= A B, all operands in shared memory.
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// N consecutive TMEM columns of this warp's 32 lanes.
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]);
+template <int N> __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]);
+template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t addr, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7]) : "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+        "=f"(v[15]) : "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
+               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                 "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15};"
+      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float v) {  // NaN counts for nothing
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float2 lo = e4m3x2_to_f(cw[c] & 0xffffu), hi = e4m3x2_to_f(cw[c] >> 16);
-      v[4 * c] = lo.x * s, v[4 * c + 1] = lo.y * s, v[4 * c + 2] = hi.x * s, v[4 * c + 3] = hi.y * s;
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle (the swizzle XORs bits 4-6 of an
+// address with bits 7-9, so every operand region starts on 1,024 bytes).  K-major: rows of
+// 64 elements, 8 rows in 1,024 bytes (stride); MN-major: 64 elements of M or N in 128
+// bytes, 8 of K in 1,024 bytes (stride), the next 64 of M `lead` bytes on.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// e4m3 codes (two in the low half of `two`) to bf16, exactly.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <uint32_t NH>
+struct Shared {
+  static constexpr uint32_t q = 0;                            // [9][NH][128 B]
+  static constexpr uint32_t k = kGroups * NH * 128;           // [9][128][128 B]
+  static constexpr uint32_t top = k + kGroups * kGroupBytes;  // [NH][4] tile maxima (then sums) by quadrant
+  static constexpr uint32_t ref = top + NH * 16;              // [2][NH] running maxima
+  static constexpr uint32_t bars = ref + 2 * NH * 4;
+  static constexpr uint32_t words = bars + 32 * 8;            // TMEM address, gave_up
+  static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
+};
+
+enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarEnd = 21, kBars = 22 };
+
+// One row's place: >= 0 a gathered row, -1 none, -2 - j own row j.
+__device__ __forceinline__ int32_t entry_of(const AttendParams &p, uint32_t token, uint32_t qi, uint32_t e) {
+  if (e < p.a.k) {
+    const int32_t u = __ldg(p.a.entry_row + (uint64_t)token * p.a.k + e);
+    return u >= 0 && (uint32_t)u < p.a.n_rows ? u : -1;
+  }
+  const uint32_t j = e - p.a.k;
+  return e < p.keys && j <= qi ? -2 - (int32_t)j : -1;
+}
+
+__device__ __forceinline__ const uint8_t *row_of(const AttendParams &p, uint32_t req, int32_t u) {
+  if (u >= 0) return (const uint8_t *)p.a.rows + (uint64_t)u * ULA_ROW_BYTES;
+  if (u == -1) return nullptr;
+  return (const uint8_t *)p.a.own_rows + req * p.a.own_req_stride + (uint64_t)(-2 - u) * p.a.own_tok_stride;
+}
+
+__device__ __forceinline__ uint4 load16(const uint8_t *row, uint32_t at) {
+  return row ? __ldg(reinterpret_cast<const uint4 *>(row + at)) : make_uint4(0, 0, 0, 0);
+}
+
+// The tiles of a block: from `first`, in item order.
+struct Place {
+  uint32_t item, tile;       // the tile's item and place in it
+  uint32_t token, req, qi, h0;
+};
+
+template <uint32_t NH>
+__device__ __forceinline__ void decode(const AttendParams &p, Place &w) {
+  w.token = w.item / p.head_tiles;
+  w.h0 = (w.item - w.token * p.head_tiles) * NH;
+  w.req = w.token / p.a.n_q;
+  w.qi = w.token - w.req * p.a.n_q;
+}
+
+template <uint32_t NH>
+__device__ __forceinline__ void step(const AttendParams &p, Place &w) {
+  if (++w.tile == p.tiles) {
+    w.tile = 0;
+    ++w.item;
+    decode<NH>(p, w);
+  }
+}
+
+// Persistent: one block per SM, block c runs an even share of all tiles, item after item
+// (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
+// joins them).  The 16 warps bring a tile's rows into registers one tile ahead, widen the
+// codes to bf16 in shared memory and run the softmax; warp w reads TMEM lanes (rows)
+// 32 (w % 4).. and the heads of column group w / 4.  Thread 0 issues the products.
+//
+// Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
+// 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_2 take
+// theirs and P_3 the rope's.  So the next tile's blocks are widened in the order 1, 2, 3, 0,
+// rope as O_1, O_2, O_3 finish, beside the rest of the products.
+template <uint32_t NH>
+__global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ AttendParams p) {
+  extern __shared__ uint8_t raw_smem[];
+  using L = Shared<NH>;
+  constexpr int HG = NH / 4;  // heads per column group
+  const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+  uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
+  volatile uint32_t *gave_up = reinterpret_cast<volatile uint32_t *>(sm + L::words + 4);
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < 5; ++i) mbar_init(bar(kBarFull + i), kWarps), mbar_init(bar(kBarS + i), 1);
+    mbar_init(bar(kBarDrained), kWarps);
+    mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
+    mbar_init(bar(kBarEnd), 1);
+    *gave_up = 0;
+    fence_async_smem();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::words) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::words);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const unsigned long long first = p.total * blockIdx.x / p.blocks;
+  const uint32_t count = (uint32_t)(p.total * (blockIdx.x + 1) / p.blocks - first);
+  Place w;
+  w.item = (uint32_t)(first / p.tiles);
+  w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
+  decode<NH>(p, w);
+
+  {
+    const uint32_t quad = warp & 3, grp = warp >> 2;
+    const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
+    const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
+    const uint32_t sk = base + L::k;
+    // widening: rows 8 warp + lane / 8 (+ 4), 16 channels lane % 8 of each block
+    const uint32_t r0 = 8 * warp + (lane >> 3), ch = lane & 7;
+    float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
+    float *ref = reinterpret_cast<float *>(sm + L::ref) + grp * HG;
+    // ---- the products, issued by one thread
+    // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
+    constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
+    constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
+    const bool issuer = threadIdx.x == 0;
+    // S_b^T of block b, once every warp has widened it (4: the rope's part, which goes to
+    // block 1's columns once they have been read)
+    auto issue_s = [&](uint32_t b, uint32_t par) {
+      if (issuer) {
+        bool there = mbar_wait(bar(kBarFull + b), par, gave_up);
+        if (b == 4) there = there && mbar_wait(bar(kBarDrained), par, gave_up);
+        if (there) {
+          tc_fence_after();
+          const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
+#pragma unroll
+          for (uint32_t s = 0; s < 8; ++s)
+            if (b < 4 || s < 4) {
+              const uint32_t g = 2 * b + (s >> 2), at = (s & 3) * 32;
+              mma_bf16(d, operand(sk + g * kGroupBytes + at, 16), operand(base + L::q + g * NH * 128 + at, 16),
+                       kIdS, s != 0);
+            }
+          mma_commit(bar(kBarS + b));
+        }
+      }
+      __syncwarp();
+    };
+    // O_b^T of block b
+    auto issue_o = [&](uint32_t b, bool fresh) {
+      const uint32_t sp = sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes;
+#pragma unroll
+      for (uint32_t s = 0; s < 8; ++s)
+        mma_bf16(tmem + b * NH, operand(sk + 2 * b * kGroupBytes + s * 2048, kGroupBytes),
+                 operand(sp + s * 2048, kGroupBytes), kIdO, !(fresh && s == 0));
+      mma_commit(bar(kBarPV + b));
+    };
+    uint32_t xph = 0;
+    auto exchange = [&]() -> bool {  // the four warps of a column group
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarX + grp));
+      const bool ok = warp_wait(bar(kBarX + grp), xph, gave_up);
+      xph ^= 1;
+      return ok;
+    };
+
+    uint4 raw[2][5];
+    float4 next_scale, scale;
+    bool next_valid, valid;
+    int32_t u0, u1, um;
+    auto fetch_entries = [&](const Place &at) {
+      const uint32_t e = at.tile * kTile;
+      u0 = entry_of(p, at.token, at.qi, e + r0);
+      u1 = entry_of(p, at.token, at.qi, e + r0 + 4);
+      um = entry_of(p, at.token, at.qi, e + mine);
+    };
+    auto fetch_rows = [&](uint32_t req) {
+      const uint8_t *a = row_of(p, req, u0), *b = row_of(p, req, u1), *c = row_of(p, req, um);
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        raw[0][i] = load16(a, i * 128 + ch * 16);
+        raw[1][i] = load16(b, i * 128 + ch * 16);
+      }
+      raw[0][4] = load16(a, ULA_ROW_LATENT + 16 + ch * 16);
+      raw[1][4] = load16(b, ULA_ROW_LATENT + 16 + ch * 16);
+      const uint4 s = load16(c, ULA_ROW_LATENT);
+      next_scale = make_float4(__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w));
+      next_valid = c != nullptr;
+    };
+    // block b (4: rope) of the fetched rows into shared memory
+    auto widen = [&](uint32_t b) {
+#pragma unroll
+      for (uint32_t j = 0; j < 2; ++j) {
+        const uint32_t r = r0 + 4 * j, x = r & 7;
+        const uint4 v = raw[j][b];
+        if (b == 4) {
+          *reinterpret_cast<uint4 *>(sm + L::k + 8 * kGroupBytes + r * 128 + ((ch ^ x) << 4)) = v;
+        } else {
+          uint8_t *at = sm + L::k + (2 * b + (ch >> 2)) * kGroupBytes + r * 128;
+          const uint32_t c = 2 * (ch & 3);
+          *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
+              make_uint4(codes_to_bf16(v.x), codes_to_bf16(v.x >> 16), codes_to_bf16(v.y), codes_to_bf16(v.y >> 16));
+          *reinterpret_cast<uint4 *>(at + (((c + 1) ^ x) << 4)) =
+              make_uint4(codes_to_bf16(v.z), codes_to_bf16(v.z >> 16), codes_to_bf16(v.w), codes_to_bf16(v.w >> 16));
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();  // (this warp's TMEM reads of the tile before)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarFull + b));
+    };
+
+    Place ahead = w;  // the tile whose entries are fetched next
+    bool ok = count > 0;
+    if (count > 0) {
+      fetch_entries(ahead);
+      fetch_rows(ahead.req);
+      step<NH>(p, ahead);
+      if (count > 1) fetch_entries(ahead);
     }
+    float sum[HG];
+    bool start = true;  // the first tile of a piece
+    uint32_t first_tile = w.tile;
+    for (uint32_t n = 0; n < count && ok; ++n) {
+      const uint32_t par = n & 1, prev = par ^ 1;
+      if (start) {
+        first_tile = w.tile;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) z += ql[c] * v[c];
-    z += q0 * __low2float(rope) + q1 * __high2float(rope);
+        for (int h = 0; h < HG; ++h) sum[h] = 0.f;
+        if (quad == 0 && lane < HG) ref[(par ^ 1) * NH + lane] = -INFINITY;
+        // the item's queries (the products that read the previous item's have ended)
+        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + w.req * p.a.q_req_stride + w.qi * p.a.q_tok_stride;
+        for (uint32_t i = threadIdx.x; i < NH * 72; i += kWarps * 32) {
+          const uint32_t h = i / 72, c = i - h * 72;
+          const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
+          const bool in = w.h0 + h < p.a.heads;
+          const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      // ---- widen the tile, block by block as the products before let go of their room
+      // (the issuer takes a block's product up one block later, when the other warps are done)
+      if (n) ok = warp_wait(bar(kBarPV + 1), prev, gave_up);
+      if (ok) widen(1);
+      if (n) ok = ok && warp_wait(bar(kBarPV + 2), prev, gave_up);
+      if (ok) widen(2);
+      if (warp == 0) issue_s(1, par);
+      if (n) ok = ok && warp_wait(bar(kBarPV + 3), prev, gave_up);
+      if (!ok) break;
+      widen(3);
+      if (warp == 0) issue_s(2, par);
+      widen(0);
+      if (warp == 0) issue_s(3, par);
+      widen(4);
+      if (warp == 0) issue_s(0, par);
+      scale = next_scale, valid = next_valid;
+      if (n + 1 < count) {  // the next tile's rows, and the entries of the one after
+        fetch_rows(ahead.req);
+        step<NH>(p, ahead);
+        if (n + 2 < count) fetch_entries(ahead);
+      }
+
+      // ---- logits (in units of log2): this thread's row, HG heads
+      float z[HG];
+      {
+        float v[HG];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    z *= a.softmax_scale;
-    const float up = fmaxf(top, z), ref = up == -INFINITY ? 0.f : up;
-    const float f = expf(top - ref), p = expf(z - ref);
-    top = up;
-    total = total * f + p;
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t b = (i + 1) & 3;
+          if (!(ok = ok && warp_wait(bar(kBarS + b), par, gave_up))) break;
+          tc_fence_after();
+          tmem_ld<HG>(lanes + kColS + b * NH + grp * HG, v);
+          tc_wait_ld();
+          const float s = b == 0 ? scale.x : b == 1 ? scale.y : b == 2 ? scale.z : scale.w;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) acc[c] = acc[c] * f + p * v[c];
+          for (int h = 0; h < HG; ++h) z[h] = i == 0 ? s * v[h] : fmaf(s, v[h], z[h]);
+          if (i == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarDrained));
+          }
+        }
+        if (warp == 0) issue_s(4, par);
+        if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
+        tc_fence_after();
+        tmem_ld<HG>(lanes + kColS + NH + grp * HG, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < HG; ++h) z[h] = valid ? (z[h] + v[h]) * p.c0 : -INFINITY;
+      }
+
+      // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
+      // above it, so that O^T is seldom rescaled; p stays below 2^8
+      {
+        float t = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float m = warp_max(z[h]);
+          if (lane == (uint32_t)h) t = m;
+        }
+        if (lane < HG) top[lane * 4 + quad] = t;
+      }
+      if (!(ok = exchange())) break;
+      const float *old_ref = ref + (par ^ 1) * NH;
+      float *new_ref = ref + par * NH;
+      bool moved = false;
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
+        const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), m = old_ref[h];
+        const bool up = t > m + 8.f;
+        const float now = up ? t : m;
+        if (quad == 0 && lane == (uint32_t)h) new_ref[h] = now;
+        if (up) {
+          moved = true;
+          sum[h] *= ex2(m - now);
+        }
+        z[h] = ex2(z[h] - (now == -INFINITY ? 0.f : now));
+        sum[h] += z[h];
+      }
+      if (moved && !start) {  // (the same decision in all four warps: top and ref are shared)
+#pragma unroll 1
+        for (uint32_t b = 0; b < 4; ++b) {
+          float o[HG];
+          tmem_ld<HG>(lanes + b * NH + grp * HG, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
+            const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), m = old_ref[h];
+            if (t > m + 8.f) o[h] *= ex2(m - t);
+          }
+          tmem_st<HG>(lanes + b * NH + grp * HG, o);
+        }
+        tc_wait_st();
+      }
+
+      // ---- P_b = p * s_b, a row's heads in one 128-byte row
+      auto put = [&](float s, uint32_t group) {
+        uint32_t u[HG / 2];
+#pragma unroll
+        for (int h = 0; h < HG / 2; ++h) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(z[2 * h] * s, z[2 * h + 1] * s);
+          u[h] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        uint8_t *at = sm + L::k + group * kGroupBytes + mine * 128;
+        const uint32_t x = mine & 7;
+        if constexpr (HG == 16) {
+          *reinterpret_cast<uint4 *>(at + (((2 * grp) ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4 *>(at + (((2 * grp + 1) ^ x) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
+        } else if constexpr (HG == 8) {
+          *reinterpret_cast<uint4 *>(at + ((grp ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+          *reinterpret_cast<uint2 *>(at + (((grp >> 1) ^ x) << 4) + (grp & 1) * 8) = make_uint2(u[0], u[1]);
+        }
+      };
+      auto hand_over = [&](uint32_t b) {
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+      };
+      put(scale.x, 8);
+      hand_over(kBarP);
+      if (issuer && mbar_wait(bar(kBarP), par, gave_up)) {
+        tc_fence_after();
+        issue_o(0, start);
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(bar(kBarPV), par, gave_up))) break;
+      put(scale.y, 0);
+      put(scale.z, 1);
+      put(scale.w, 8);
+      hand_over(kBarP + 1);
+      if (issuer && mbar_wait(bar(kBarP + 1), par, gave_up)) {
+        tc_fence_after();
+        for (uint32_t b = 1; b < 4; ++b) issue_o(b, start);
+      }
+      __syncwarp();
+      start = false;
+
+      // ---- the end of a piece: normalise and write
+      const bool item_ends = w.tile + 1 == p.tiles;
+      if (item_ends || n + 1 == count) {
+        float t = 0.f;
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float s = warp_sum(sum[h]);
+          if (lane == (uint32_t)h) t = s;
+        }
+        if (lane < HG) top[lane * 4 + quad] = t;
+        if (!(ok = exchange())) break;
+        if (!(ok = warp_wait(bar(kBarPV + 3), par, gave_up))) break;
+        tc_fence_after();
+        const bool whole = item_ends && first_tile == 0;
+        const uint32_t slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
+        float inv[HG];
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
+          const float s = (t4.x + t4.y) + (t4.z + t4.w), m = new_ref[h];
+          inv[h] = s == 0.f ? 0.f : 1.f / s;
+          if (quad == 0 && lane == (uint32_t)h) {
+            const uint32_t head = grp * HG + h;
+            const float l2 = (m == -INFINITY ? 0.f : m) + log2f(s);
+            if (!whole)
+              p.part_lse[(uint64_t)slot * NH + head] = l2;
+            else if (p.a.lse && w.h0 + head < p.a.heads)
+              p.a.lse[(uint64_t)w.token * p.a.heads + w.h0 + head] = l2 * 0.693147180559945309f;
+          }
+        }
+#pragma unroll 1
+        for (uint32_t b = 0; b < 4; ++b) {
+          float o[HG];
+          tmem_ld<HG>(lanes + b * NH + grp * HG, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const uint32_t head = grp * HG + h;
+            if (w.h0 + head < p.a.heads) {
+              if (whole)
+                ((__nv_bfloat16 *)p.a.out)[((uint64_t)w.token * p.a.heads + w.h0 + head) * ULA_ROW_LATENT + b * 128 + mine] =
+                    __float2bfloat16_rn(o[h] * inv[h]);
+              else
+                p.part_out[((uint64_t)slot * NH + head) * ULA_ROW_LATENT + b * 128 + mine] = o[h] * inv[h];
+            }
+          }
+        }
+        // (top is written again only after the next tile's barriers)
+        start = true;
+      }
+      if (item_ends) {
+        w.tile = 0;
+        ++w.item;
+        decode<NH>(p, w);
+      } else {
+        ++w.tile;
+      }
+    }
+    if (issuer) {  // every product has ended before the block's TMEM goes
+      mma_commit(bar(kBarEnd));
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the partial results of the items that several blocks share: 128 threads per query
+// token and head, 4 channels each.
+__global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh) {
+  const unsigned long long i = (unsigned long long)blockIdx.x * 2 + (threadIdx.x >> 7);
+  const uint32_t c = threadIdx.x & 127;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
+  const uint32_t head = (uint32_t)(i % p.a.heads), token = (uint32_t)(i / p.a.heads);
+  if (i >= (unsigned long long)p.a.n_req * p.a.n_q * p.a.heads) return;
+  const unsigned long long s = ((unsigned long long)token * p.head_tiles + head / nh) * p.tiles;
+  const uint32_t b0 = (uint32_t)(((s + 1) * p.blocks - 1) / p.total);
+  const uint32_t b1 = (uint32_t)(((s + p.tiles) * p.blocks - 1) / p.total);
+  if (b0 == b1) return;  // written whole
+  const uint32_t h = head % nh;
+  auto slot = [&](uint32_t b) { return (uint64_t)2 * b + (b == b0 ? 1 : 0); };
+  float top = -INFINITY;
+  for (uint32_t b = b0; b <= b1; ++b) top = fmaxf(top, p.part_lse[slot(b) * nh + h]);
+  const float m = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (uint32_t b = b0; b <= b1; ++b) {
+    const float f = ex2(p.part_lse[slot(b) * nh + h] - m);
+    const float4 o = reinterpret_cast<const float4 *>(p.part_out + (slot(b) * nh + h) * ULA_ROW_LATENT)[c];
+    total += f;
+    acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  __nv_bfloat162 o[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) o[c] = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-  uint4 *out = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + w * ULA_ROW_LATENT) + 2 * l;
-  out[0] = reinterpret_cast<uint4 *>(o)[0];
-  out[1] = reinterpret_cast<uint4 *>(o)[1];
-  if (a.lse && l == 0) a.lse[w] = (top == -INFINITY ? 0.f : top) + logf(total);
+  __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
+  reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + i * ULA_ROW_LATENT)[c] = *reinterpret_cast<uint2 *>(r);
+  if (p.a.lse && c == 0) p.a.lse[i] = (m + log2f(total)) * 0.693147180559945309f;
 }
 
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+struct Plan {
+  uint32_t nh, head_tiles, tiles, keys, blocks;
+  unsigned long long total;
+  bool parts;  // some item's tiles lie in several blocks
+  uint64_t workspace;
+};
+
+bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool own, Plan *pl) {
+  const uint64_t tokens = (uint64_t)n_req * n_q;
+  if (tokens > 0x7fffffffull || heads > 0x7fffffffu || k > 0x7fffffffu - kTile ||
+      (own && n_q > 0x7fffffffu - kTile - k))
+    return false;
+  pl->keys = k + (own ? n_q : 0);
+  pl->tiles = pl->keys ? (pl->keys + kTile - 1) / kTile : 1;
+  pl->nh = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
+  pl->head_tiles = (heads + pl->nh - 1) / pl->nh;
+  const uint64_t items = tokens * pl->head_tiles;
+  if (items > 0x7fffffffull || items * heads > (1ull << 40)) return false;
+  pl->total = items * pl->tiles;
+  const int sms = sm_count();
+  if (sms < 1 || pl->total > (1ull << 48)) return false;
+  pl->blocks = pl->total < (unsigned)sms ? (uint32_t)pl->total : (uint32_t)sms;
+  if (pl->total / (pl->blocks ? pl->blocks : 1) > 0x7fffffffull) return false;
+  pl->parts = pl->blocks && !(pl->total % pl->blocks == 0 && (pl->total / pl->blocks) % pl->tiles == 0);
+  pl->workspace = pl->parts ? (uint64_t)2 * pl->blocks * pl->nh * (ULA_ROW_LATENT + 1) * 4 : 0;
+  return true;
+}
+
+template <uint32_t NH>
+cudaError_t launch_attend(const AttendParams &p, cudaStream_t st) {
+  // (idempotent and cheap; a per-device flag would have to know about device resets)
+  cudaError_t e = cudaFuncSetAttribute(k_attend<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shared<NH>::bytes;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, k_attend<NH>, p);
+}
 
 }  // namespace
 
 extern "C" uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads,
                                               uint32_t k, int own) {
-  (void)n_req, (void)n_q, (void)heads, (void)k, (void)own;
-  return 0;
+  Plan pl;
+  return make_plan(n_req, n_q, heads, k, own != 0, &pl) ? pl.workspace : 0;
 }
 
 extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   if (!args) return ULA_ERR_INVALID_ARG;
   const ula_attend_args &a = *args;
-  const uint64_t tokens = (uint64_t)a.n_req * a.n_q;
-  if (tokens == 0 || a.heads == 0) return ULA_OK;
+  if (a.n_req == 0 || a.n_q == 0 || a.heads == 0) return ULA_OK;
   if (!a.q || !a.out || (a.k && (!a.entry_row || (!a.rows && a.n_rows)))) return ULA_ERR_INVALID_ARG;
   if (!aligned(a.q, 16) || !aligned(a.rows, 16) || !aligned(a.own_rows, 16) || !aligned(a.out, 16) ||
       !aligned(a.entry_row, 4) || !aligned(a.lse, 4) || !aligned(a.workspace, 16))
     return ULA_ERR_INVALID_ARG;
   if (a.q_req_stride % 8 || a.q_tok_stride % 8 || a.q_head_stride % 8 || a.own_req_stride % 16 ||
-      a.own_tok_stride % 16 || a.n_rows > 0x7fffffffu || a.k > 0x7fffffffu - a.n_q)
+      a.own_tok_stride % 16 || a.n_rows > 0x7fffffffu)
     return ULA_ERR_INVALID_ARG;
-  if (tokens > 0xffffffffull || (tokens * a.heads + 7) / 8 > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((tokens * a.heads + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = (cudaStream_t)stream;
-  return cudaLaunchKernelEx(&cfg, k_attend, a) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+  Plan pl;
+  if (!make_plan(a.n_req, a.n_q, a.heads, a.k, a.own_rows != nullptr, &pl)) return ULA_ERR_INVALID_ARG;
+  if (pl.workspace && (!a.workspace || a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
+  AttendParams p{};
+  p.a = a;
+  p.total = pl.total, p.blocks = pl.blocks, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
+  p.c0 = a.softmax_scale * 1.44269504088896341f;
+  p.part_out = (float *)a.workspace;
+  p.part_lse = p.part_out + (uint64_t)2 * pl.blocks * pl.nh * ULA_ROW_LATENT;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = pl.nh == 16 ? launch_attend<16>(p, st) : pl.nh == 32 ? launch_attend<32>(p, st) : launch_attend<64>(p, st);
+  if (e != cudaSuccess) return ULA_ERR_CUDA;
+  if (pl.parts) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(((uint64_t)a.n_req * a.n_q * a.heads + 1) / 2));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_join_parts, p, pl.nh);
+  }
+  return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 
 extern "C" int ula_rows_sync(void *stream) {

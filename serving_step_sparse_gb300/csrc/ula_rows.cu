@@ -66,9 +66,93 @@ struct RotateParams {
   float sign;  // -1 for the inverse
 };
 
-// One warp per token and head, one pair per lane.
+// 16 bytes of T, in fp32 and back.
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / (int)sizeof(T);
+  __device__ static __forceinline__ void load(const T *p, float (&v)[n]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = to_f(e[i]);
+  }
+  __device__ static __forceinline__ void store(T *p, const float (&v)[n]) {
+    uint4 u;
+    T *e = reinterpret_cast<T *>(&u);
+#pragma unroll
+    for (int i = 0; i < n; ++i) e[i] = from_f<T>(v[i]);
+    *reinterpret_cast<uint4 *>(p) = u;
+  }
+};
+
+// Bound by its bytes: every channel is read and written once.  A block takes `rows`
+// consecutive (token, head) rows; its threads first issue their loads (kItems rows each,
+// two 16-byte chunks of a row: channels of the first and of the second half), then work
+// out the sines of the block's tokens together (once for all heads of a token), then turn
+// and store.
+template <typename T, bool kHalves, int kItems>
+__global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ RotateParams p) {
+  constexpr int V = Vec<T>::n, kPer = 32 / V;          // threads per row
+  constexpr uint32_t kStep = 256 / kPer, kRows = kStep * kItems;
+  extern __shared__ float4 table4[];                   // [tokens of the block][32] (cos, sin)
+  float2 *table = reinterpret_cast<float2 *>(table4);
+  const uint64_t all = (uint64_t)p.n * p.heads, row0 = (uint64_t)blockIdx.x * kRows;
+  const uint64_t last = row0 + kRows < all ? row0 + kRows - 1 : all - 1;
+  const uint32_t t0 = (uint32_t)(row0 / p.heads), t1 = (uint32_t)(last / p.heads);
+  const uint32_t h0 = (uint32_t)(row0 - (uint64_t)t0 * p.heads);
+  const uint32_t c = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
+  float a[kItems][V], b[kItems][V];
+  uint32_t tok[kItems], head[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const uint32_t r = h0 + r0 + i * kStep;
+    tok[i] = r / p.heads, head[i] = r - tok[i] * p.heads;
+    if (row0 + r0 + i * kStep < all) {
+      const T *x = (const T *)p.x + (t0 + tok[i]) * p.xt + head[i] * p.xh + c * V;
+      Vec<T>::load(x, a[i]);
+      Vec<T>::load(x + kPairs, b[i]);
+    }
+  }
+  for (uint32_t k = threadIdx.x; k < (t1 - t0 + 1) * kPairs; k += 256) {
+    const uint32_t j = k & 31;
+    float2 cs = turn_of(p.rot, j, p.pos[p.rot.axis[j] * p.pos_axis_stride + t0 + (k >> 5)]);
+    cs.y *= p.sign;
+    table[k] = cs;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (row0 + r0 + i * kStep >= all) break;
+    const float4 *tb = table4 + tok[i] * (kPairs / 2);
+    float oa[V], ob[V];
+    if (kHalves) {  // pair j: channel j of the first half with channel j of the second
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const float4 cs = tb[(c * V + k) / 2];
+        oa[k] = a[i][k] * cs.x - b[i][k] * cs.y, ob[k] = a[i][k] * cs.y + b[i][k] * cs.x;
+        oa[k + 1] = a[i][k + 1] * cs.z - b[i][k + 1] * cs.w, ob[k + 1] = a[i][k + 1] * cs.w + b[i][k + 1] * cs.z;
+      }
+    } else {  // pair j: channels 2j, 2j + 1
+      auto turn = [&](const float (&v)[V], float (&o)[V], uint32_t pair0) {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+          const float4 cs = tb[(pair0 + k / 2) / 2];
+          o[k] = v[k] * cs.x - v[k + 1] * cs.y, o[k + 1] = v[k] * cs.y + v[k + 1] * cs.x;
+          o[k + 2] = v[k + 2] * cs.z - v[k + 3] * cs.w, o[k + 3] = v[k + 2] * cs.w + v[k + 3] * cs.z;
+        }
+      };
+      turn(a[i], oa, c * (V / 2));
+      turn(b[i], ob, kPairs / 2 + c * (V / 2));
+    }
+    T *o = (T *)p.out + (t0 + tok[i]) * p.ot + head[i] * p.oh + c * V;
+    Vec<T>::store(o, oa);
+    Vec<T>::store(o + kPairs, ob);
+  }
+}
+
+// Any alignment and strides: one warp per token and head, one pair per lane.
 template <typename T, bool kHalves>
-__global__ void __launch_bounds__(256) k_rotate(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(256) k_rotate_any(const __grid_constant__ RotateParams p) {
   const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const uint32_t j = threadIdx.x & 31;
   if (w >= (uint64_t)p.n * p.heads) return;
@@ -110,9 +194,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// One warp per token: lane l holds latents 16l..16l+15 (8 lanes share a block's scale)
-// and turns rope pair l.
-template <typename T, bool kHalves>
+// Bound by its bytes.  One warp per token: lane l holds latents 16l..16l+15 (8 lanes share
+// a block's scale) and turns rope pair l.  kVec: 16-byte loads of the latents (bases and
+// strides that allow them).  The quotient is a product with the scale's reciprocal (two
+// fp32 roundings; 16 divisions a lane were half of the instructions).
+template <typename T, bool kHalves, bool kVec>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
   const uint32_t t = blockIdx.x * 8 + (threadIdx.x >> 5), l = threadIdx.x & 31;
   if (t >= p.n) return;
@@ -120,28 +206,37 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams
   const T *r = (const T *)p.rope + t * p.rope_stride;
   uint8_t *row = p.rows + t * p.row_stride;
   const uint32_t ia = kHalves ? l : 2 * l, ib = kHalves ? l + kPairs : 2 * l + 1;
+  float v[16], amax = 0.f;
+  if (kVec) {
+    constexpr int V = Vec<T>::n;
+#pragma unroll
+    for (int i = 0; i < 16 / V; ++i) Vec<T>::load(x + i * V, reinterpret_cast<float (&)[V]>(v[i * V]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = to_f(x[i]);
+  }
   const float a = to_f(r[ia]), b = to_f(r[ib]);
   const int32_t pos = p.pos[p.rot.axis[l] * p.pos_axis_stride + t];
-  float v[16], amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = to_f(x[i]);
-    amax = max_nan(amax, fabsf(v[i]));
-  }
+  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(v[i]));
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f);
+  const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f), inv = __frcp_rn(scale);
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = e4m3x4(__fdiv_rn(v[4 * i], scale), __fdiv_rn(v[4 * i + 1], scale),
-                  __fdiv_rn(v[4 * i + 2], scale), __fdiv_rn(v[4 * i + 3], scale));
+    c[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
   reinterpret_cast<uint4 *>(row)[l] = make_uint4(c[0], c[1], c[2], c[3]);
   if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;
   const float2 cs = turn_of(p.rot, l, pos);
   __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(row + ULA_ROW_LATENT + 16);
-  o[ia] = __float2bfloat16_rn(a * cs.x - b * cs.y);
-  o[ib] = __float2bfloat16_rn(a * cs.y + b * cs.x);
+  const float oa = a * cs.x - b * cs.y, ob = a * cs.y + b * cs.x;
+  if (kHalves) {
+    o[ia] = __float2bfloat16_rn(oa);
+    o[ib] = __float2bfloat16_rn(ob);
+  } else {
+    reinterpret_cast<__nv_bfloat162 *>(o)[l] = __floats2bfloat162_rn(oa, ob);
+  }
 }
 
 // ---------------------------------------------------------------- join
@@ -196,10 +291,11 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ JoinParams
 }
 
 template <typename P>
-cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t block, cudaStream_t st, const P &p) {
+cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t smem, cudaStream_t st, const P &p) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(block);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
@@ -207,10 +303,33 @@ cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t block, cudaStream_
 uint32_t type_size(uint32_t dtype) { return dtype == ULA_TYPE_F32 ? 4u : 2u; }
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// kItems 4 keeps 8 loads in flight per thread where there are blocks for every SM several
+// times over; few rows are spread over more blocks of one row per thread (4,096 tokens x
+// 128 heads: see the measurements beside ula_rows_rotate; 96 x 64: 96 blocks instead of 24).
+template <typename T, bool kHalves>
+cudaError_t launch_rotate_vec(const RotateParams &p, cudaStream_t st) {
+  const uint64_t all = (uint64_t)p.n * p.heads;
+  constexpr uint32_t step = 256 / (32 / Vec<T>::n);
+  const bool many = all >= 4ull * step * 608 && p.heads >= 8;
+  const uint32_t rows = step * (many ? 4 : 1);
+  const uint32_t tokens = (rows - 1) / p.heads + 2;  // at most, whatever the first row
+  return launch(many ? k_rotate_vec<T, kHalves, 4> : k_rotate_vec<T, kHalves, 1>, (all + rows - 1) / rows,
+                tokens * kPairs * 8, st, p);
+}
+
 template <typename T>
-void (*rotate_kernel(bool halves))(RotateParams) { return halves ? k_rotate<T, true> : k_rotate<T, false>; }
+cudaError_t launch_rotate(const RotateParams &p, bool halves, bool vec, cudaStream_t st) {
+  if (vec) return halves ? launch_rotate_vec<T, true>(p, st) : launch_rotate_vec<T, false>(p, st);
+  const uint64_t blocks = ((uint64_t)p.n * p.heads + 7) / 8;
+  return launch(halves ? k_rotate_any<T, true> : k_rotate_any<T, false>, blocks, 0, st, p);
+}
+
 template <typename T>
-void (*pack_kernel(bool halves))(PackParams) { return halves ? k_pack<T, true> : k_pack<T, false>; }
+cudaError_t launch_pack(const PackParams &p, bool halves, bool vec, cudaStream_t st) {
+  auto k = halves ? (vec ? k_pack<T, true, true> : k_pack<T, true, false>)
+                  : (vec ? k_pack<T, false, true> : k_pack<T, false, false>);
+  return launch(k, ((uint64_t)p.n + 7) / 8, 0, st, p);
+}
 
 }  // namespace
 
@@ -232,9 +351,13 @@ extern "C" int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const i
   p.out = d_out, p.ot = out_token_stride, p.oh = out_head_stride;
   p.sign = (flags & ULA_ROTATE_INVERSE) ? -1.f : 1.f;
   const bool halves = rotary->pairing == ULA_PAIR_HALVES;
-  auto k = dtype == ULA_TYPE_BF16 ? rotate_kernel<__nv_bfloat16>(halves)
-           : dtype == ULA_TYPE_F16 ? rotate_kernel<__half>(halves) : rotate_kernel<float>(halves);
-  return launch(k, (work + 7) / 8, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+  const uint64_t strides = x_token_stride | x_head_stride | out_token_stride | out_head_stride;
+  const bool vec = aligned(d_x, 16) && aligned(d_out, 16) && strides * type_size(dtype) % 16 == 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_rotate<__nv_bfloat16>(p, halves, vec, st)
+                        : dtype == ULA_TYPE_F16 ? launch_rotate<__half>(p, halves, vec, st)
+                                                : launch_rotate<float>(p, halves, vec, st);
+  return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 
 extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
@@ -255,9 +378,12 @@ extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
   p.rope = d_rope, p.rope_stride = rope_stride;
   p.rows = (uint8_t *)d_rows, p.row_stride = row_stride;
   const bool halves = rotary->pairing == ULA_PAIR_HALVES;
-  auto k = dtype == ULA_TYPE_BF16 ? pack_kernel<__nv_bfloat16>(halves)
-           : dtype == ULA_TYPE_F16 ? pack_kernel<__half>(halves) : pack_kernel<float>(halves);
-  return launch(k, ((uint64_t)n + 7) / 8, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+  const bool vec = aligned(d_latent, 16) && latent_stride * type_size(dtype) % 16 == 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_pack<__nv_bfloat16>(p, halves, vec, st)
+                        : dtype == ULA_TYPE_F16 ? launch_pack<__half>(p, halves, vec, st)
+                                                : launch_pack<float>(p, halves, vec, st);
+  return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 
 extern "C" int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t parts,
@@ -273,5 +399,5 @@ extern "C" int ula_rows_join(const void *const *outs, const float *const *lses, 
   }
   if (!out || !aligned(out, 16) || !aligned(lse, 4)) return ULA_ERR_INVALID_ARG;
   p.parts = parts, p.n = n, p.out = (uint4 *)out, p.lse = lse;
-  return launch(k_join, (n + 3) / 4, 256, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+  return launch(k_join, (n + 3) / 4, 0, (cudaStream_t)stream, p) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }

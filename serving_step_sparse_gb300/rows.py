@@ -24,11 +24,6 @@ _TYPES = {torch.bfloat16: ula.TYPE_BF16, torch.float16: ula.TYPE_F16, torch.floa
 _PAIRINGS = {"adjacent": ula.PAIR_ADJACENT, "halves": ula.PAIR_HALVES}
 
 
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _on_stream(call):
     """Gives an operator its ``stream`` argument: the call runs (copies and outputs it makes
     included) on that stream, and the tensors handed in, which another stream's allocator may
@@ -57,12 +52,13 @@ def _tensors(v):
 
 def _stream_of(*tensors) -> int:
     """The current stream of the tensors' device, which has to be the current device."""
-    device = tensors[0].device
-    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
-          "the tensors must be on the current CUDA device")
+    index = tensors[0].get_device()
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
     for t in tensors:
-        _need(t is None or t.device == device, "the tensors must be on one device")
-    return torch.cuda.current_stream(device).cuda_stream
+        if t.get_device() != index:
+            raise ValueError("the tensors must be on one device")
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 class Rotary:
@@ -77,10 +73,12 @@ class Rotary:
     def __init__(self, freq, axis=None, pairing: str = "adjacent"):
         freq = [float(f) for f in freq]
         axis = [int(a) for a in axis] if axis is not None else [0] * ROPE_PAIRS
-        _need(len(freq) == ROPE_PAIRS and len(axis) == ROPE_PAIRS,
-              f"a rotary has {ROPE_PAIRS} frequencies and axes")
-        _need(all(0 <= a < ula.MAX_AXES for a in axis), f"an axis is in [0, {ula.MAX_AXES})")
-        _need(pairing in _PAIRINGS, f"pairing is one of {sorted(_PAIRINGS)}")
+        if not (len(freq) == ROPE_PAIRS and len(axis) == ROPE_PAIRS):
+            raise ValueError(f"a rotary has {ROPE_PAIRS} frequencies and axes")
+        if not all(0 <= a < ula.MAX_AXES for a in axis):
+            raise ValueError(f"an axis is in [0, {ula.MAX_AXES})")
+        if pairing not in _PAIRINGS:
+            raise ValueError(f"pairing is one of {sorted(_PAIRINGS)}")
         self.n_axes = max(axis) + 1
         self.config = ula.ula_rotary()
         self.config.n_axes, self.config.pairing = self.n_axes, _PAIRINGS[pairing]
@@ -89,11 +87,12 @@ class Rotary:
 
 
 def _positions(pos: torch.Tensor, rotary: Rotary, n: int):
-    _need(pos.dtype == torch.int32, "positions are int32")
+    if pos.dtype != torch.int32:
+        raise ValueError("positions are int32")
     if pos.dim() == 1:
         pos = pos[None]
-    _need(pos.dim() == 2 and pos.shape[0] >= rotary.n_axes and pos.shape[1] == n,
-          "positions are [axes][tokens]")
+    if not (pos.dim() == 2 and pos.shape[0] >= rotary.n_axes and pos.shape[1] == n):
+        raise ValueError("positions are [axes][tokens]")
     if pos.stride(1) != 1 and n > 1:
         pos = pos.contiguous()
     return pos
@@ -108,14 +107,14 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *, out: torch.Ten
     shape and type, such as the last 64 channels of the queries that ``attend`` reads.
     inverse turns back; it is also the gradient.
     """
-    _need(x.dim() in (2, 3) and x.shape[-1] == ROW_ROPE and x.dtype in _TYPES,
-          f"x is [tokens][heads][{ROW_ROPE}] of bf16, f16 or f32")
+    if not (x.dim() in (2, 3) and x.shape[-1] == ROW_ROPE and x.dtype in _TYPES):
+        raise ValueError(f"x is [tokens][heads][{ROW_ROPE}] of bf16, f16 or f32")
     n, heads = x.shape[0], x.shape[1] if x.dim() == 3 else 1
     pos = _positions(pos, rotary, n)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need(out.shape == x.shape and out.dtype == x.dtype and out.stride(-1) == 1,
-          "out has x's shape and type, and dense channels")
+    if not (out.shape == x.shape and out.dtype == x.dtype and out.stride(-1) == 1):
+        raise ValueError("out has x's shape and type, and dense channels")
     if x.stride(-1) != 1:
         x = x.contiguous()
     handle = _stream_of(x, pos, out)
@@ -137,10 +136,10 @@ def pack(latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor, rotary: Ro
     [n][L][656] that ``UlaCache.alloc`` takes), or None for a new tensor.  Returns rows.
     """
     n = latent.shape[0]
-    _need(latent.dtype in _TYPES and latent.shape == (n, ROW_LATENT),
-          f"latent is [tokens][{ROW_LATENT}] of bf16, f16 or f32")
-    _need(rope.dtype == latent.dtype and rope.shape == (n, ROW_ROPE),
-          f"rope is [tokens][{ROW_ROPE}] of the latent's type")
+    if not (latent.dtype in _TYPES and latent.shape == (n, ROW_LATENT)):
+        raise ValueError(f"latent is [tokens][{ROW_LATENT}] of bf16, f16 or f32")
+    if not (rope.dtype == latent.dtype and rope.shape == (n, ROW_ROPE)):
+        raise ValueError(f"rope is [tokens][{ROW_ROPE}] of the latent's type")
     if latent.stride(1) != 1:
         latent = latent.contiguous()
     if rope.stride(1) != 1:
@@ -148,9 +147,9 @@ def pack(latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor, rotary: Ro
     pos = _positions(pos, rotary, n)
     if rows is None:
         rows = torch.empty((n, ROW_BYTES), dtype=torch.uint8, device=latent.device)
-    _need(rows.dtype == torch.uint8 and rows.shape == (n, ROW_BYTES)
-          and rows.stride(1) == 1 and (n < 2 or rows.stride(0) >= ROW_BYTES),
-          f"rows is uint8 [tokens][{ROW_BYTES}]")
+    if not (rows.dtype == torch.uint8 and rows.shape == (n, ROW_BYTES)
+          and rows.stride(1) == 1 and (n < 2 or rows.stride(0) >= ROW_BYTES)):
+        raise ValueError(f"rows is uint8 [tokens][{ROW_BYTES}]")
     handle = _stream_of(latent, rope, pos, rows)
     ula.ula_rows_pack(rotary.config, pos.data_ptr(), pos.stride(0), n, _TYPES[latent.dtype],
                       latent.data_ptr(), latent.stride(0), rope.data_ptr(), rope.stride(0),
@@ -172,13 +171,15 @@ def attend(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax
     out: bf16 [R][Q][H][512], lse: float32 [R][Q][H], ln of the sum of exp(logits); a query token
     that selects nothing gets 0 and -inf.
     """
-    _need(q.dim() == 4 and q.shape[3] == ROW_LATENT + ROW_ROPE and q.dtype == torch.bfloat16,
-          f"q is bf16 [requests][query tokens][heads][{ROW_LATENT + ROW_ROPE}]")
+    if not (q.dim() == 4 and q.shape[3] == ROW_LATENT + ROW_ROPE and q.dtype == torch.bfloat16):
+        raise ValueError(f"q is bf16 [requests][query tokens][heads][{ROW_LATENT + ROW_ROPE}]")
     R, Q, H, _ = q.shape
-    _need(rows.dtype == torch.uint8 and rows.dim() == 2 and rows.shape[1] == ROW_BYTES
-          and rows.is_contiguous(), f"rows is contiguous uint8 [rows][{ROW_BYTES}]")
-    _need(entry_row.dtype == torch.int32 and entry_row.dim() == 3
-          and entry_row.shape[:2] == (R, Q), "entry_row is int32 [requests][query tokens][k]")
+    if not (rows.dtype == torch.uint8 and rows.dim() == 2 and rows.shape[1] == ROW_BYTES
+          and rows.is_contiguous()):
+        raise ValueError(f"rows is contiguous uint8 [rows][{ROW_BYTES}]")
+    if not (entry_row.dtype == torch.int32 and entry_row.dim() == 3
+          and entry_row.shape[:2] == (R, Q)):
+        raise ValueError("entry_row is int32 [requests][query tokens][k]")
     if not entry_row.is_contiguous():
         entry_row = entry_row.contiguous()
     sq = q.stride()
@@ -188,21 +189,22 @@ def attend(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax
     K = entry_row.shape[2]
     own, so = None, (0, 0)
     if own_rows is not None:
-        _need(own_rows.dtype == torch.uint8 and own_rows.shape == (R, Q, ROW_BYTES)
-              and own_rows.stride(2) == 1,
-              f"own_rows is uint8 [requests][query tokens][{ROW_BYTES}]")
+        if not (own_rows.dtype == torch.uint8 and own_rows.shape == (R, Q, ROW_BYTES)
+              and own_rows.stride(2) == 1):
+            raise ValueError(f"own_rows is uint8 [requests][query tokens][{ROW_BYTES}]")
         own, so = own_rows.data_ptr(), own_rows.stride()
     if out is None:
         out = torch.empty((R, Q, H, ROW_LATENT), dtype=torch.bfloat16, device=q.device)
     else:
-        _need(out.dtype == torch.bfloat16 and out.shape == (R, Q, H, ROW_LATENT)
-              and out.is_contiguous(), f"out is contiguous bf16 [{R}][{Q}][{H}][{ROW_LATENT}]")
+        if not (out.dtype == torch.bfloat16 and out.shape == (R, Q, H, ROW_LATENT)
+              and out.is_contiguous()):
+            raise ValueError(f"out is contiguous bf16 [{R}][{Q}][{H}][{ROW_LATENT}]")
     if lse is None:
         lse = torch.empty((R, Q, H), dtype=torch.float32, device=q.device)
     else:
-        _need(lse.dtype == torch.float32 and lse.shape == (R, Q, H) and lse.is_contiguous(),
-              f"lse is contiguous float32 [{R}][{Q}][{H}]")
-    handle = _stream_of(q, rows, entry_row, own_rows, out, lse)
+        if not (lse.dtype == torch.float32 and lse.shape == (R, Q, H) and lse.is_contiguous()):
+            raise ValueError(f"lse is contiguous float32 [{R}][{Q}][{H}]")
+    handle = _stream_of(q, rows, entry_row, out, lse, *(() if own_rows is None else (own_rows,)))
     nbytes = ula.ula_rows_attend_workspace(R, Q, H, K, own is not None)
     space = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     ula.ula_rows_attend(ula.ula_attend_args(
@@ -217,26 +219,27 @@ def join(outs, lses, *, out: torch.Tensor | None = None, lse: torch.Tensor | Non
     """Joins partial results over disjoint rows (at most 8 parts): lists of ``attend``'s outs
     (bf16 [...][512]) and lses (float32 [...]).  Returns (out, lse); a part with lse -inf counts
     for nothing.  out and lse may be one of the parts."""
-    _need(1 <= len(outs) <= ula.MAX_PARTS and len(outs) == len(lses),
-          f"1 to {ula.MAX_PARTS} parts, an out and an lse of each")
+    if not (1 <= len(outs) <= ula.MAX_PARTS and len(outs) == len(lses)):
+        raise ValueError(f"1 to {ula.MAX_PARTS} parts, an out and an lse of each")
     shape = outs[0].shape
-    _need(len(shape) >= 1 and shape[-1] == ROW_LATENT, f"a part's out is [...][{ROW_LATENT}]")
+    if not (len(shape) >= 1 and shape[-1] == ROW_LATENT):
+        raise ValueError(f"a part's out is [...][{ROW_LATENT}]")
     for o, z in zip(outs, lses):
-        _need(o.dtype == torch.bfloat16 and o.shape == shape and o.is_contiguous(),
-              f"a part's out is contiguous bf16 [...][{ROW_LATENT}], all of one shape")
-        _need(z.dtype == torch.float32 and z.shape == shape[:-1] and z.is_contiguous(),
-              "a part's lse is contiguous float32 of its out's shape without the channels")
+        if not (o.dtype == torch.bfloat16 and o.shape == shape and o.is_contiguous()):
+            raise ValueError(f"a part's out is contiguous bf16 [...][{ROW_LATENT}], all of one shape")
+        if not (z.dtype == torch.float32 and z.shape == shape[:-1] and z.is_contiguous()):
+            raise ValueError("a part's lse is contiguous float32 of its out's shape without the channels")
     device = outs[0].device
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)
     else:
-        _need(out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous(),
-              "out is contiguous bf16 of the parts' shape")
+        if not (out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous()):
+            raise ValueError("out is contiguous bf16 of the parts' shape")
     if lse is None:
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
     else:
-        _need(lse.dtype == torch.float32 and lse.shape == shape[:-1] and lse.is_contiguous(),
-              "lse is contiguous float32 of the parts' shape")
+        if not (lse.dtype == torch.float32 and lse.shape == shape[:-1] and lse.is_contiguous()):
+            raise ValueError("lse is contiguous float32 of the parts' shape")
     handle = _stream_of(*outs, *lses, out, lse)
     ula.ula_rows_join([o.data_ptr() for o in outs], [z.data_ptr() for z in lses],
                       lses[0].numel(), out.data_ptr(), lse.data_ptr(), handle)

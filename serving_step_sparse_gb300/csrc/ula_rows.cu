@@ -33,10 +33,10 @@ bool rotary_to_dev(const ula_rotary *r, RotaryDev *out) {
   return true;
 }
 
-// (cos, sin) of pair j at a position; the top 32 bits of the phase are the signed
+// (cos, sin) of a pair (of its step) at a position; the top 32 bits of the phase are the signed
 // fraction of a turn (resolution 1.5e-9 rad), sincospi takes half turns.
-__device__ __forceinline__ float2 turn_of(const RotaryDev &r, uint32_t j, int32_t pos) {
-  const unsigned long long phase = (unsigned long long)(long long)pos * r.step[j];
+__device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos) {
+  const unsigned long long phase = (unsigned long long)(long long)pos * step;
   const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
   float s, c;
   sincospif(half_turns, &s, &c);
@@ -70,18 +70,17 @@ struct RotateParams {
 template <typename T>
 struct Vec {
   static constexpr int n = 16 / (int)sizeof(T);
-  __device__ static __forceinline__ void load(const T *p, float (&v)[n]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  __device__ static __forceinline__ void open(const uint4 &u, float (&v)[n]) {
     const T *e = reinterpret_cast<const T *>(&u);
 #pragma unroll
     for (int i = 0; i < n; ++i) v[i] = to_f(e[i]);
   }
-  __device__ static __forceinline__ void store(T *p, const float (&v)[n]) {
+  __device__ static __forceinline__ uint4 close(const float (&v)[n]) {
     uint4 u;
     T *e = reinterpret_cast<T *>(&u);
 #pragma unroll
     for (int i = 0; i < n; ++i) e[i] = from_f<T>(v[i]);
-    *reinterpret_cast<uint4 *>(p) = u;
+    return u;
   }
 };
 
@@ -101,21 +100,22 @@ __global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ Rota
   const uint32_t t0 = (uint32_t)(row0 / p.heads), t1 = (uint32_t)(last / p.heads);
   const uint32_t h0 = (uint32_t)(row0 - (uint64_t)t0 * p.heads);
   const uint32_t c = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
-  float a[kItems][V], b[kItems][V];
-  uint32_t tok[kItems], head[kItems];
+  uint4 lo[kItems], hi[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    const uint32_t r = h0 + r0 + i * kStep;
-    tok[i] = r / p.heads, head[i] = r - tok[i] * p.heads;
+    const uint32_t r = h0 + r0 + i * kStep, tok = r / p.heads;
     if (row0 + r0 + i * kStep < all) {
-      const T *x = (const T *)p.x + (t0 + tok[i]) * p.xt + head[i] * p.xh + c * V;
-      Vec<T>::load(x, a[i]);
-      Vec<T>::load(x + kPairs, b[i]);
+      const T *x = (const T *)p.x + (t0 + tok) * p.xt + (r - tok * p.heads) * p.xh + c * V;
+      lo[i] = *reinterpret_cast<const uint4 *>(x);
+      hi[i] = *reinterpret_cast<const uint4 *>(x + kPairs);
     }
   }
+  // (a thread's pair is the same in every turn: the parameters' lane-wise reads, which the
+  // constant port serves one lane at a time, are made once)
+  const int32_t *pos = p.pos + p.rot.axis[threadIdx.x & 31] * p.pos_axis_stride + t0;
+  const unsigned long long step = p.rot.step[threadIdx.x & 31];
   for (uint32_t k = threadIdx.x; k < (t1 - t0 + 1) * kPairs; k += 256) {
-    const uint32_t j = k & 31;
-    float2 cs = turn_of(p.rot, j, p.pos[p.rot.axis[j] * p.pos_axis_stride + t0 + (k >> 5)]);
+    float2 cs = turn_of(step, pos[k >> 5]);
     cs.y *= p.sign;
     table[k] = cs;
   }
@@ -123,14 +123,17 @@ __global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ Rota
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     if (row0 + r0 + i * kStep >= all) break;
-    const float4 *tb = table4 + tok[i] * (kPairs / 2);
-    float oa[V], ob[V];
+    const uint32_t r = h0 + r0 + i * kStep, tok = r / p.heads;
+    const float4 *tb = table4 + tok * (kPairs / 2);
+    float a[V], b[V], oa[V], ob[V];
+    Vec<T>::open(lo[i], a);
+    Vec<T>::open(hi[i], b);
     if (kHalves) {  // pair j: channel j of the first half with channel j of the second
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
         const float4 cs = tb[(c * V + k) / 2];
-        oa[k] = a[i][k] * cs.x - b[i][k] * cs.y, ob[k] = a[i][k] * cs.y + b[i][k] * cs.x;
-        oa[k + 1] = a[i][k + 1] * cs.z - b[i][k + 1] * cs.w, ob[k + 1] = a[i][k + 1] * cs.w + b[i][k + 1] * cs.z;
+        oa[k] = a[k] * cs.x - b[k] * cs.y, ob[k] = a[k] * cs.y + b[k] * cs.x;
+        oa[k + 1] = a[k + 1] * cs.z - b[k + 1] * cs.w, ob[k + 1] = a[k + 1] * cs.w + b[k + 1] * cs.z;
       }
     } else {  // pair j: channels 2j, 2j + 1
       auto turn = [&](const float (&v)[V], float (&o)[V], uint32_t pair0) {
@@ -141,12 +144,12 @@ __global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ Rota
           o[k + 2] = v[k + 2] * cs.z - v[k + 3] * cs.w, o[k + 3] = v[k + 2] * cs.w + v[k + 3] * cs.z;
         }
       };
-      turn(a[i], oa, c * (V / 2));
-      turn(b[i], ob, kPairs / 2 + c * (V / 2));
+      turn(a, oa, c * (V / 2));
+      turn(b, ob, kPairs / 2 + c * (V / 2));
     }
-    T *o = (T *)p.out + (t0 + tok[i]) * p.ot + head[i] * p.oh + c * V;
-    Vec<T>::store(o, oa);
-    Vec<T>::store(o + kPairs, ob);
+    T *o = (T *)p.out + (t0 + tok) * p.ot + (r - tok * p.heads) * p.oh + c * V;
+    *reinterpret_cast<uint4 *>(o) = Vec<T>::close(oa);
+    *reinterpret_cast<uint4 *>(o + kPairs) = Vec<T>::close(ob);
   }
 }
 
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(256) k_rotate_any(const __grid_constant__ Rota
   const uint32_t t = (uint32_t)(w / p.heads), h = (uint32_t)(w % p.heads);
   const T *x = (const T *)p.x + t * p.xt + h * p.xh;
   T *o = (T *)p.out + t * p.ot + h * p.oh;
-  const float2 cs = turn_of(p.rot, j, p.pos[p.rot.axis[j] * p.pos_axis_stride + t]);
+  const float2 cs = turn_of(p.rot.step[j], p.pos[p.rot.axis[j] * p.pos_axis_stride + t]);
   const uint32_t ia = kHalves ? j : 2 * j, ib = kHalves ? j + kPairs : 2 * j + 1;
   const float a = to_f(x[ia]), b = to_f(x[ib]), s = cs.y * p.sign;
   o[ia] = from_f<T>(a * cs.x - b * s);
@@ -195,47 +198,66 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // Bound by its bytes.  One warp per token: lane l holds latents 16l..16l+15 (8 lanes share
-// a block's scale) and turns rope pair l.  kVec: 16-byte loads of the latents (bases and
-// strides that allow them).  The quotient is a product with the scale's reciprocal (two
-// fp32 roundings; 16 divisions a lane were half of the instructions).
+// a block's scale) and turns rope pair l; a warp has the next token's loads in flight
+// while it works on one.  kVec: 16-byte loads of the latents (bases and strides that allow
+// them).  The quotient is a product with the scale's reciprocal (two fp32 roundings; 16
+// divisions a lane were half of the instructions).
 template <typename T, bool kHalves, bool kVec>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
-  const uint32_t t = blockIdx.x * 8 + (threadIdx.x >> 5), l = threadIdx.x & 31;
-  if (t >= p.n) return;
-  const T *x = (const T *)p.latent + t * p.latent_stride + 16 * l;
-  const T *r = (const T *)p.rope + t * p.rope_stride;
-  uint8_t *row = p.rows + t * p.row_stride;
+  constexpr int V = Vec<T>::n, N = 16 / V;
+  const uint32_t l = threadIdx.x & 31, warps = gridDim.x * 8;
   const uint32_t ia = kHalves ? l : 2 * l, ib = kHalves ? l + kPairs : 2 * l + 1;
-  float v[16], amax = 0.f;
-  if (kVec) {
-    constexpr int V = Vec<T>::n;
+  uint4 next[N];
+  T next_a, next_b;
+  int32_t next_pos;
+  const int32_t *posl = p.pos + p.rot.axis[l] * p.pos_axis_stride;
+  const unsigned long long step = p.rot.step[l];
+  auto fetch = [&](uint32_t t) {
+    const T *x = (const T *)p.latent + t * p.latent_stride + 16 * l;
+    const T *r = (const T *)p.rope + t * p.rope_stride;
 #pragma unroll
-    for (int i = 0; i < 16 / V; ++i) Vec<T>::load(x + i * V, reinterpret_cast<float (&)[V]>(v[i * V]));
-  } else {
+    for (int i = 0; i < N; ++i) {
+      if (kVec) {
+        next[i] = *reinterpret_cast<const uint4 *>(x + i * V);
+      } else {
+        T *e = reinterpret_cast<T *>(&next[i]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = to_f(x[i]);
-  }
-  const float a = to_f(r[ia]), b = to_f(r[ib]);
-  const int32_t pos = p.pos[p.rot.axis[l] * p.pos_axis_stride + t];
+        for (int k = 0; k < V; ++k) e[k] = x[i * V + k];
+      }
+    }
+    next_a = r[ia], next_b = r[ib];
+    next_pos = posl[t];
+  };
+  uint64_t t = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t < p.n) fetch((uint32_t)t);
+  for (; t < p.n; t += warps) {
+    float v[16], amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(v[i]));
+    for (int i = 0; i < N; ++i) Vec<T>::open(next[i], reinterpret_cast<float (&)[V]>(v[i * V]));
+    const float a = to_f(next_a), b = to_f(next_b);
+    const int32_t pos = next_pos;
+    if (t + warps < p.n) fetch((uint32_t)(t + warps));
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f), inv = __frcp_rn(scale);
-  uint32_t c[4];
+    for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(v[i]));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-  reinterpret_cast<uint4 *>(row)[l] = make_uint4(c[0], c[1], c[2], c[3]);
-  if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;
-  const float2 cs = turn_of(p.rot, l, pos);
-  __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(row + ULA_ROW_LATENT + 16);
-  const float oa = a * cs.x - b * cs.y, ob = a * cs.y + b * cs.x;
-  if (kHalves) {
-    o[ia] = __float2bfloat16_rn(oa);
-    o[ib] = __float2bfloat16_rn(ob);
-  } else {
-    reinterpret_cast<__nv_bfloat162 *>(o)[l] = __floats2bfloat162_rn(oa, ob);
+    for (int d = 1; d < 8; d <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f), inv = __frcp_rn(scale);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    uint8_t *row = p.rows + t * p.row_stride;
+    reinterpret_cast<uint4 *>(row)[l] = make_uint4(c[0], c[1], c[2], c[3]);
+    if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;
+    const float2 cs = turn_of(step, pos);
+    __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(row + ULA_ROW_LATENT + 16);
+    const float oa = a * cs.x - b * cs.y, ob = a * cs.y + b * cs.x;
+    if (kHalves) {
+      o[ia] = __float2bfloat16_rn(oa);
+      o[ib] = __float2bfloat16_rn(ob);
+    } else {
+      reinterpret_cast<__nv_bfloat162 *>(o)[l] = __floats2bfloat162_rn(oa, ob);
+    }
   }
 }
 
@@ -303,17 +325,18 @@ cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t smem, cudaStream_t
 uint32_t type_size(uint32_t dtype) { return dtype == ULA_TYPE_F32 ? 4u : 2u; }
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// kItems 4 keeps 8 loads in flight per thread where there are blocks for every SM several
-// times over; few rows are spread over more blocks of one row per thread (4,096 tokens x
-// 128 heads: see the measurements beside ula_rows_rotate; 96 x 64: 96 blocks instead of 24).
+// Two rows per thread (4 loads in flight) where there are blocks for every SM several times
+// over: 4,096 tokens x 128 heads of bf16, 26.0 us (5.2 TB/s) against 29.3 with one and 27.8
+// with four.  Fewer rows are spread over more blocks of one row per thread, and so are
+// tokens of few heads, whose sines would need more shared memory.
 template <typename T, bool kHalves>
 cudaError_t launch_rotate_vec(const RotateParams &p, cudaStream_t st) {
   const uint64_t all = (uint64_t)p.n * p.heads;
   constexpr uint32_t step = 256 / (32 / Vec<T>::n);
-  const bool many = all >= 4ull * step * 608 && p.heads >= 8;
-  const uint32_t rows = step * (many ? 4 : 1);
+  const bool many = all >= 2ull * step * 608 && p.heads >= 8;
+  const uint32_t rows = step * (many ? 2 : 1);
   const uint32_t tokens = (rows - 1) / p.heads + 2;  // at most, whatever the first row
-  return launch(many ? k_rotate_vec<T, kHalves, 4> : k_rotate_vec<T, kHalves, 1>, (all + rows - 1) / rows,
+  return launch(many ? k_rotate_vec<T, kHalves, 2> : k_rotate_vec<T, kHalves, 1>, (all + rows - 1) / rows,
                 tokens * kPairs * 8, st, p);
 }
 
@@ -328,7 +351,10 @@ template <typename T>
 cudaError_t launch_pack(const PackParams &p, bool halves, bool vec, cudaStream_t st) {
   auto k = halves ? (vec ? k_pack<T, true, true> : k_pack<T, true, false>)
                   : (vec ? k_pack<T, false, true> : k_pack<T, false, false>);
-  return launch(k, ((uint64_t)p.n + 7) / 8, 0, st, p);
+  // a warp takes more than one token once every SM has its 4 resident blocks (131,072 tokens
+  // of bf16: 42.6 us, 5.6 TB/s, with 4; 53.6 / 46.3 / 47.5 / 43.5 with 2 / 3 / 6 / 8)
+  const uint64_t blocks = ((uint64_t)p.n + 7) / 8, most = 4ull * 152;
+  return launch(k, blocks < most ? blocks : most, 0, st, p);
 }
 
 }  // namespace

@@ -27,8 +27,11 @@ __device__ int g_status;  // the first error that a kernel of this file latched
 constexpr uint32_t kTile = 128;                      // rows per tile
 constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
 constexpr uint32_t kGroups = 9;                      // 8 of latents, 1 of rope
-constexpr uint32_t kWarps = 16;
-constexpr uint32_t kThreads = kWarps * 32;           // 128 registers each
+constexpr uint32_t kWarps = 8;                       // compute warps; the ninth issues the products
+constexpr uint32_t kThreads = (kWarps + 4) * 32;     // (registers move between groups of 4 warps)
+// Launched with 168 registers a thread: 3 * 168 = 2 * 216 + 72.
+constexpr uint32_t kRegsCompute = 216, kRegsIssue = 72;
+constexpr uint32_t kSlots = kTile / (4 * kWarps);    // rows per lane of the widening
 constexpr uint32_t kColS = 256;                      // TMEM: O^T in columns 0.., S^T from here
 
 struct AttendParams {
@@ -71,7 +74,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 
 // Bounded: after 1 s, or once another thread of the block has given up, it returns false.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
+__device__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
   const unsigned long long t0 = global_ns();
   for (;;) {
     if (mbar_try(bar, parity)) return true;
@@ -100,6 +103,12 @@ __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sy
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p;
+}
+
 // One MMA of K = 16: D[128][N] (+)= A B, all operands in shared memory.
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -115,10 +124,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // N consecutive TMEM columns of this warp's 32 lanes.
 template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]);
 template <int N> __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]);
-template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t addr, float (&v)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
-}
 template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
@@ -132,33 +137,55 @@ template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float (&v
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
         "=f"(v[15]) : "r"(addr) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float (&v)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
-               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(addr) : "memory");
+template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float (&v)[32]) {
+  tmem_ld<16>(addr, reinterpret_cast<float (&)[16]>(v[0]));
+  tmem_ld<16>(addr + 16, reinterpret_cast<float (&)[16]>(v[16]));
 }
 template <> __device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
                ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
                  "r"(addr) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15};"
-      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(addr)
-      : "memory");
-}
 
 __device__ __forceinline__ float warp_max(float v) {  // NaN counts for nothing
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float s, float v0, float v1) {  // x += s * v
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %2};\n mov.b64 b, {%3, %4};\n mov.b64 c, {%0, %1};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(s), "f"(v0), "f"(v1));
+}
+__device__ __forceinline__ void mul2(float &x0, float &x1, float s, float v0, float v1) {  // x = s * v
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %2};\n mov.b64 b, {%3, %4};\n mul.rn.f32x2 b, a, b;\n"
+      " mov.b64 {%0, %1}, b;\n}\n"
+      : "=f"(x0), "=f"(x1) : "f"(s), "f"(v0), "f"(v1));
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&b);
+}
+// Sums of N values over a warp's lanes: lane h (and h + N, ...) gets the h-th.  Each step
+// sends the half of the values that the other lane will keep.
+template <int N>
+__device__ __forceinline__ float sum_rows(const float (&v)[N], uint32_t lane) {
+  float x[N];
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
+  for (int i = 0; i < N; ++i) x[i] = v[i];
+#pragma unroll
+  for (int d = N / 2; d; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < d; ++i) {
+      const bool up = lane & d;
+      const float keep = up ? x[i + d] : x[i], send = up ? x[i] : x[i + d];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+    }
+  float r = x[0];
+#pragma unroll
+  for (int d = N; d < 32; d <<= 1) r += __shfl_xor_sync(0xffffffffu, r, d);
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -191,29 +218,12 @@ struct Shared {
   static constexpr uint32_t q = 0;                            // [9][NH][128 B]
   static constexpr uint32_t k = kGroups * NH * 128;           // [9][128][128 B]
   static constexpr uint32_t top = k + kGroups * kGroupBytes;  // [NH][4] tile maxima (then sums) by quadrant
-  static constexpr uint32_t ref = top + NH * 16;              // [2][NH] running maxima
-  static constexpr uint32_t bars = ref + 2 * NH * 4;
+  static constexpr uint32_t bars = top + NH * 16;
   static constexpr uint32_t words = bars + 32 * 8;            // TMEM address, gave_up
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
 
-enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarEnd = 21, kBars = 22 };
-
-// One row's place: >= 0 a gathered row, -1 none, -2 - j own row j.
-__device__ __forceinline__ int32_t entry_of(const AttendParams &p, uint32_t token, uint32_t qi, uint32_t e) {
-  if (e < p.a.k) {
-    const int32_t u = __ldg(p.a.entry_row + (uint64_t)token * p.a.k + e);
-    return u >= 0 && (uint32_t)u < p.a.n_rows ? u : -1;
-  }
-  const uint32_t j = e - p.a.k;
-  return e < p.keys && j <= qi ? -2 - (int32_t)j : -1;
-}
-
-__device__ __forceinline__ const uint8_t *row_of(const AttendParams &p, uint32_t req, int32_t u) {
-  if (u >= 0) return (const uint8_t *)p.a.rows + (uint64_t)u * ULA_ROW_BYTES;
-  if (u == -1) return nullptr;
-  return (const uint8_t *)p.a.own_rows + req * p.a.own_req_stride + (uint64_t)(-2 - u) * p.a.own_tok_stride;
-}
+enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarEnd = 19 };
 
 __device__ __forceinline__ uint4 load16(const uint8_t *row, uint32_t at) {
   return row ? __ldg(reinterpret_cast<const uint4 *>(row + at)) : make_uint4(0, 0, 0, 0);
@@ -242,11 +252,25 @@ __device__ __forceinline__ void step(const AttendParams &p, Place &w) {
   }
 }
 
+// Entry e of a tile's query token as it stands in memory (0 past the list).  What it means is
+// worked out by row_of, when the rows are fetched: a comparison here would wait for the load.
+__device__ __forceinline__ int32_t entry_of(const AttendParams &p, const Place &at, uint32_t e) {
+  return e < p.a.k ? __ldg(p.a.entry_row + (uint64_t)at.token * p.a.k + e) : 0;
+}
+
+__device__ __forceinline__ const uint8_t *row_of(const AttendParams &p, const Place &at, uint32_t e, int32_t u) {
+  if (e < p.a.k)
+    return u >= 0 && (uint32_t)u < p.a.n_rows ? (const uint8_t *)p.a.rows + (uint64_t)u * ULA_ROW_BYTES : nullptr;
+  const uint32_t j = e - p.a.k;  // an own row
+  if (e >= p.keys || j > at.qi) return nullptr;
+  return (const uint8_t *)p.a.own_rows + at.req * p.a.own_req_stride + j * p.a.own_tok_stride;
+}
+
 // Persistent: one block per SM, block c runs an even share of all tiles, item after item
 // (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
-// joins them).  The 16 warps bring a tile's rows into registers one tile ahead, widen the
-// codes to bf16 in shared memory and run the softmax; warp w reads TMEM lanes (rows)
-// 32 (w % 4).. and the heads of column group w / 4.  Thread 0 issues the products.
+// joins them).  Eight compute warps bring a tile's rows into registers one tile ahead, widen
+// the codes to bf16 in shared memory and run the softmax; warp w reads TMEM lanes (rows)
+// 32 (w % 4).. and the heads of column group w / 4.  A ninth warp issues the products.
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_2 take
@@ -256,7 +280,7 @@ template <uint32_t NH>
 __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NH>;
-  constexpr int HG = NH / 4;  // heads per column group
+  constexpr int HG = NH / 2;  // heads per column group
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -266,19 +290,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     for (uint32_t i = 0; i < 5; ++i) mbar_init(bar(kBarFull + i), kWarps), mbar_init(bar(kBarS + i), 1);
     mbar_init(bar(kBarDrained), kWarps);
     mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1);
+    mbar_init(bar(kBarX), 4), mbar_init(bar(kBarX + 1), 4);
     mbar_init(bar(kBarEnd), 1);
     *gave_up = 0;
     fence_async_smem();
   }
-  if (warp == 0) {
+  if (warp == kWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::words) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::words);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::words), 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const unsigned long long first = p.total * blockIdx.x / p.blocks;
@@ -286,52 +311,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
   Place w;
   w.item = (uint32_t)(first / p.tiles);
   w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
-  decode<NH>(p, w);
+  const uint32_t sk = base + L::k;
 
-  {
-    const uint32_t quad = warp & 3, grp = warp >> 2;
-    const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
-    const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
-    const uint32_t sk = base + L::k;
-    // widening: rows 8 warp + lane / 8 (+ 4), 16 channels lane % 8 of each block
-    const uint32_t r0 = 8 * warp + (lane >> 3), ch = lane & 7;
-    float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
-    float *ref = reinterpret_cast<float *>(sm + L::ref) + grp * HG;
-    // ---- the products, issued by one thread
+  if (warp >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kWarps) {
+    // ---- the products.  The warp waits as one and one elected lane issues: so the operands'
+    // descriptors stay in uniform registers (53 clocks an MMA of N = 64, which is what its
+    // 6 KB of operands take; issued under a thread's own branch it took 63, whatever N)
     // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
     constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
     constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
-    const bool issuer = threadIdx.x == 0;
-    // S_b^T of block b, once every warp has widened it (4: the rope's part, which goes to
-    // block 1's columns once they have been read)
-    auto issue_s = [&](uint32_t b, uint32_t par) {
-      if (issuer) {
-        bool there = mbar_wait(bar(kBarFull + b), par, gave_up);
-        if (b == 4) there = there && mbar_wait(bar(kBarDrained), par, gave_up);
-        if (there) {
-          tc_fence_after();
-          const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
+    uint32_t tile = w.tile;
+    bool ok = true, fresh = true;
+    for (uint32_t n = 0; n < count && ok; ++n) {
+      const uint32_t par = n & 1;
+#pragma unroll 1
+      for (uint32_t i = 0; i < 5; ++i) {
+        // block 1, 2, 3, 0, then the rope's part, which goes to block 1's columns once they
+        // have been read
+        const uint32_t b = i < 4 ? (i + 1) & 3 : 4;
+        if (b == 4 && !(ok = warp_wait(bar(kBarDrained), par, gave_up))) break;
+        if (!(ok = warp_wait(bar(kBarFull + b), par, gave_up))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
+        const uint64_t da = operand(sk + 2 * b * kGroupBytes, 16), db = operand(base + L::q + 2 * b * NH * 128, 16);
+        if (elect_one()) {
 #pragma unroll
-          for (uint32_t s = 0; s < 8; ++s)
-            if (b < 4 || s < 4) {
-              const uint32_t g = 2 * b + (s >> 2), at = (s & 3) * 32;
-              mma_bf16(d, operand(sk + g * kGroupBytes + at, 16), operand(base + L::q + g * NH * 128 + at, 16),
-                       kIdS, s != 0);
-            }
+          for (uint32_t s = 0; s < 4; ++s) mma_bf16(d, da + 2 * s, db + 2 * s, kIdS, s != 0);
+          if (b < 4) {
+#pragma unroll
+            for (uint32_t s = 0; s < 4; ++s)
+              mma_bf16(d, da + (kGroupBytes >> 4) + 2 * s, db + (NH * 128 >> 4) + 2 * s, kIdS, true);
+          }
           mma_commit(bar(kBarS + b));
         }
+        __syncwarp();
       }
-      __syncwarp();
-    };
-    // O_b^T of block b
-    auto issue_o = [&](uint32_t b, bool fresh) {
-      const uint32_t sp = sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes;
+#pragma unroll 1
+      for (uint32_t b = 0; b < 4 && ok; ++b) {
+        if (b < 2 && !(ok = warp_wait(bar(kBarP + b), par, gave_up))) break;
+        tc_fence_after();
+        const uint64_t da = operand(sk + 2 * b * kGroupBytes, kGroupBytes);
+        const uint64_t db = operand(sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes, kGroupBytes);
+        if (elect_one()) {
 #pragma unroll
-      for (uint32_t s = 0; s < 8; ++s)
-        mma_bf16(tmem + b * NH, operand(sk + 2 * b * kGroupBytes + s * 2048, kGroupBytes),
-                 operand(sp + s * 2048, kGroupBytes), kIdO, !(fresh && s == 0));
-      mma_commit(bar(kBarPV + b));
-    };
+          for (uint32_t s = 0; s < 8; ++s)
+            mma_bf16(tmem + b * NH, da + s * 128, db + s * 128, kIdO, s != 0 || !fresh);
+          mma_commit(bar(kBarPV + b));
+        }
+        __syncwarp();
+      }
+      fresh = false;
+      if (++tile == p.tiles) tile = 0, fresh = true;
+    }
+    if (elect_one()) {  // every product has ended before the block's TMEM goes
+      mma_commit(bar(kBarEnd));
+      const unsigned long long t0 = global_ns();
+      while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
+    }
+    __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+    decode<NH>(p, w);
+    const uint32_t quad = warp & 3, grp = warp >> 2;
+    const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
+    const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
+    // widening: rows r0, r0 + 4, ..., 16 channels ch of each block
+    const uint32_t r0 = 4 * kSlots * warp + (lane >> 3), ch = lane & 7;
+    float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
     uint32_t xph = 0;
     auto exchange = [&]() -> bool {  // the four warps of a column group
       __syncwarp();
@@ -341,25 +390,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
       return ok;
     };
 
-    uint4 raw[2][5];
+    uint4 raw[kSlots][5];
     float4 next_scale, scale;
-    bool next_valid, valid;
-    int32_t u0, u1, um;
+    bool next_valid;
+    int32_t u[kSlots], um;
     auto fetch_entries = [&](const Place &at) {
-      const uint32_t e = at.tile * kTile;
-      u0 = entry_of(p, at.token, at.qi, e + r0);
-      u1 = entry_of(p, at.token, at.qi, e + r0 + 4);
-      um = entry_of(p, at.token, at.qi, e + mine);
-    };
-    auto fetch_rows = [&](uint32_t req) {
-      const uint8_t *a = row_of(p, req, u0), *b = row_of(p, req, u1), *c = row_of(p, req, um);
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        raw[0][i] = load16(a, i * 128 + ch * 16);
-        raw[1][i] = load16(b, i * 128 + ch * 16);
-      }
-      raw[0][4] = load16(a, ULA_ROW_LATENT + 16 + ch * 16);
-      raw[1][4] = load16(b, ULA_ROW_LATENT + 16 + ch * 16);
+      for (uint32_t j = 0; j < kSlots; ++j) u[j] = entry_of(p, at, at.tile * kTile + r0 + 4 * j);
+      um = entry_of(p, at, at.tile * kTile + mine);
+    };
+    auto fetch_row = [&](const Place &at, uint32_t j) {
+      const uint8_t *a = row_of(p, at, at.tile * kTile + r0 + 4 * j, u[j]);
+#pragma unroll
+      for (uint32_t i = 0; i < 5; ++i) raw[j][i] = load16(a, i * 128 + (i == 4 ? 16 : 0) + ch * 16);
+    };
+    auto fetch_scale = [&](const Place &at) {
+      const uint8_t *c = row_of(p, at, at.tile * kTile + mine, um);
       const uint4 s = load16(c, ULA_ROW_LATENT);
       next_scale = make_float4(__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w));
       next_valid = c != nullptr;
@@ -367,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     // block b (4: rope) of the fetched rows into shared memory
     auto widen = [&](uint32_t b) {
 #pragma unroll
-      for (uint32_t j = 0; j < 2; ++j) {
+      for (uint32_t j = 0; j < kSlots; ++j) {
         const uint32_t r = r0 + 4 * j, x = r & 7;
         const uint4 v = raw[j][b];
         if (b == 4) {
@@ -386,16 +432,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarFull + b));
     };
+    auto hand_over = [&](uint32_t b) {
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
 
     Place ahead = w;  // the tile whose entries are fetched next
     bool ok = count > 0;
     if (count > 0) {
       fetch_entries(ahead);
-      fetch_rows(ahead.req);
+#pragma unroll
+      for (uint32_t j = 0; j < kSlots; ++j) fetch_row(ahead, j);
+      fetch_scale(ahead);
       step<NH>(p, ahead);
       if (count > 1) fetch_entries(ahead);
     }
-    float sum[HG];
+    float sum[HG], ref = -INFINITY;  // this row's sums; lane h: head h's running maximum
     bool start = true;  // the first tile of a piece
     uint32_t first_tile = w.tile;
     for (uint32_t n = 0; n < count && ok; ++n) {
@@ -404,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         first_tile = w.tile;
 #pragma unroll
         for (int h = 0; h < HG; ++h) sum[h] = 0.f;
-        if (quad == 0 && lane < HG) ref[(par ^ 1) * NH + lane] = -INFINITY;
+        ref = -INFINITY;
         // the item's queries (the products that read the previous item's have ended)
         const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + w.req * p.a.q_req_stride + w.qi * p.a.q_tok_stride;
         for (uint32_t i = threadIdx.x; i < NH * 72; i += kWarps * 32) {
@@ -417,58 +471,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
       // ---- widen the tile, block by block as the products before let go of their room
-      // (the issuer takes a block's product up one block later, when the other warps are done)
-      if (n) ok = warp_wait(bar(kBarPV + 1), prev, gave_up);
+      if (n) ok = ok && warp_wait(bar(kBarPV + 1), prev, gave_up);
       if (ok) widen(1);
       if (n) ok = ok && warp_wait(bar(kBarPV + 2), prev, gave_up);
       if (ok) widen(2);
-      if (warp == 0) issue_s(1, par);
       if (n) ok = ok && warp_wait(bar(kBarPV + 3), prev, gave_up);
       if (!ok) break;
       widen(3);
-      if (warp == 0) issue_s(2, par);
       widen(0);
-      if (warp == 0) issue_s(3, par);
-      widen(4);
-      if (warp == 0) issue_s(0, par);
-      scale = next_scale, valid = next_valid;
-      if (n + 1 < count) {  // the next tile's rows, and the entries of the one after
-        fetch_rows(ahead.req);
-        step<NH>(p, ahead);
-        if (n + 2 < count) fetch_entries(ahead);
-      }
 
-      // ---- logits (in units of log2): this thread's row, HG heads
+      // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0, a
+      // row without an entry (its codes are zeros) gets -inf.  Block 1's part comes first, so
+      // that the rope's product can take its columns.
+      scale = next_scale;
+      const float off = next_valid ? 0.f : -INFINITY;
+      const bool more = n + 1 < count;  // (the next tile's rows are fetched bit by bit)
       float z[HG];
       {
         float v[HG];
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t b = (i + 1) & 3;
-          if (!(ok = ok && warp_wait(bar(kBarS + b), par, gave_up))) break;
-          tc_fence_after();
-          tmem_ld<HG>(lanes + kColS + b * NH + grp * HG, v);
-          tc_wait_ld();
-          const float s = b == 0 ? scale.x : b == 1 ? scale.y : b == 2 ? scale.z : scale.w;
-#pragma unroll
-          for (int h = 0; h < HG; ++h) z[h] = i == 0 ? s * v[h] : fmaf(s, v[h], z[h]);
-          if (i == 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarDrained));
-          }
-        }
-        if (warp == 0) issue_s(4, par);
-        if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
+        if (!(ok = warp_wait(bar(kBarS + 1), par, gave_up))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, v);
         tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarDrained));
+        widen(4);
+        const float s = scale.y * p.c0;
 #pragma unroll
-        for (int h = 0; h < HG; ++h) z[h] = valid ? (z[h] + v[h]) * p.c0 : -INFINITY;
+        for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
+      }
+      if (more) fetch_row(ahead, 0);
+      {
+        float v[HG], x[HG];
+        ok = warp_wait(bar(kBarS + 2), par, gave_up);
+        if (!(ok = ok && warp_wait(bar(kBarS + 3), par, gave_up))) break;
+        tc_fence_after();
+        tmem_ld<HG>(lanes + kColS + 2 * NH + grp * HG, v);
+        tmem_ld<HG>(lanes + kColS + 3 * NH + grp * HG, x);
+        tc_wait_ld();
+        float s = scale.z * p.c0, t = scale.w * p.c0;
+#pragma unroll
+        for (int h = 0; h < HG; h += 2) {
+          fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
+          fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
+        }
+        ok = warp_wait(bar(kBarS), par, gave_up);
+        if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
+        tc_fence_after();
+        tmem_ld<HG>(lanes + kColS + grp * HG, v);
+        tmem_ld<HG>(lanes + kColS + NH + grp * HG, x);
+        tc_wait_ld();
+        s = scale.x * p.c0, t = p.c0;
+#pragma unroll
+        for (int h = 0; h < HG; h += 2) {
+          fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
+          fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
+        }
       }
 
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
-      // above it, so that O^T is seldom rescaled; p stays below 2^8
+      // above it, so that O^T is seldom rescaled; p stays below 2^8.  Lane h keeps head h's.
       {
         float t = -INFINITY;
 #pragma unroll
@@ -478,133 +541,116 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
         if (lane < HG) top[lane * 4 + quad] = t;
       }
+      if (more) fetch_row(ahead, 1);
       if (!(ok = exchange())) break;
-      const float *old_ref = ref + (par ^ 1) * NH;
-      float *new_ref = ref + par * NH;
-      bool moved = false;
+      {
+        const float4 t4 = *reinterpret_cast<const float4 *>(top + (lane & (HG - 1)) * 4);
+        const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+        const bool up = t > ref + 8.f;
+        const float now = up ? t : ref;
+        if (__any_sync(0xffffffffu, up)) {  // (the same in all four warps)
+          const float f = up ? ex2(ref - now) : 1.f;
 #pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
-        const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), m = old_ref[h];
-        const bool up = t > m + 8.f;
-        const float now = up ? t : m;
-        if (quad == 0 && lane == (uint32_t)h) new_ref[h] = now;
-        if (up) {
-          moved = true;
-          sum[h] *= ex2(m - now);
-        }
-        z[h] = ex2(z[h] - (now == -INFINITY ? 0.f : now));
-        sum[h] += z[h];
-      }
-      if (moved && !start) {  // (the same decision in all four warps: top and ref are shared)
+          for (int h = 0; h < HG; ++h) sum[h] *= __shfl_sync(0xffffffffu, f, h);
+          if (!start) {
 #pragma unroll 1
-        for (uint32_t b = 0; b < 4; ++b) {
-          float o[HG];
-          tmem_ld<HG>(lanes + b * NH + grp * HG, o);
-          tc_wait_ld();
+            for (uint32_t b = 0; b < 4; ++b) {
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
-            const float t = fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), m = old_ref[h];
-            if (t > m + 8.f) o[h] *= ex2(m - t);
+              for (int c = 0; c < HG; c += 8) {
+                float o[8];
+                tmem_ld<8>(lanes + b * NH + grp * HG + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 8; ++h) o[h] *= __shfl_sync(0xffffffffu, f, c + h);
+                tmem_st<8>(lanes + b * NH + grp * HG + c, o);
+              }
+            }
+            tc_wait_st();
           }
-          tmem_st<HG>(lanes + b * NH + grp * HG, o);
         }
-        tc_wait_st();
+        ref = now;
+        const float m = now == -INFINITY ? 0.f : now;
+#pragma unroll
+        for (int h = 0; h < HG; ++h) {
+          z[h] = ex2(z[h] - __shfl_sync(0xffffffffu, m, h));
+          sum[h] += z[h];
+        }
       }
 
       // ---- P_b = p * s_b, a row's heads in one 128-byte row
       auto put = [&](float s, uint32_t group) {
-        uint32_t u[HG / 2];
-#pragma unroll
-        for (int h = 0; h < HG / 2; ++h) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(z[2 * h] * s, z[2 * h + 1] * s);
-          u[h] = *reinterpret_cast<const uint32_t *>(&b);
-        }
         uint8_t *at = sm + L::k + group * kGroupBytes + mine * 128;
         const uint32_t x = mine & 7;
-        if constexpr (HG == 16) {
-          *reinterpret_cast<uint4 *>(at + (((2 * grp) ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-          *reinterpret_cast<uint4 *>(at + (((2 * grp + 1) ^ x) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
-        } else if constexpr (HG == 8) {
-          *reinterpret_cast<uint4 *>(at + ((grp ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
-          *reinterpret_cast<uint2 *>(at + (((grp >> 1) ^ x) << 4) + (grp & 1) * 8) = make_uint2(u[0], u[1]);
+#pragma unroll
+        for (int c = 0; c < HG / 8; ++c) {
+          uint32_t v[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float lo, hi;
+            mul2(lo, hi, s, z[8 * c + 2 * h], z[8 * c + 2 * h + 1]);
+            v[h] = bf16x2(lo, hi);
+          }
+          *reinterpret_cast<uint4 *>(at + (((HG / 8 * grp + c) ^ x) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-      };
-      auto hand_over = [&](uint32_t b) {
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(b));
       };
       put(scale.x, 8);
       hand_over(kBarP);
-      if (issuer && mbar_wait(bar(kBarP), par, gave_up)) {
-        tc_fence_after();
-        issue_o(0, start);
-      }
-      __syncwarp();
+      if (more) fetch_row(ahead, 2);
       if (!(ok = warp_wait(bar(kBarPV), par, gave_up))) break;
       put(scale.y, 0);
       put(scale.z, 1);
       put(scale.w, 8);
       hand_over(kBarP + 1);
-      if (issuer && mbar_wait(bar(kBarP + 1), par, gave_up)) {
-        tc_fence_after();
-        for (uint32_t b = 1; b < 4; ++b) issue_o(b, start);
+      if (more) {
+        fetch_row(ahead, 3);
+        fetch_scale(ahead);
+        step<NH>(p, ahead);
+        if (n + 2 < count) fetch_entries(ahead);
       }
-      __syncwarp();
       start = false;
 
-      // ---- the end of a piece: normalise and write
+      // ---- the end of a piece: normalise and write (a warp's 32 lanes: 32 channels of a head)
       const bool item_ends = w.tile + 1 == p.tiles;
       if (item_ends || n + 1 == count) {
-        float t = 0.f;
-#pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          const float s = warp_sum(sum[h]);
-          if (lane == (uint32_t)h) t = s;
-        }
-        if (lane < HG) top[lane * 4 + quad] = t;
+        const float mine_sum = sum_rows<HG>(sum, lane);
+        if (lane < HG) top[lane * 4 + quad] = mine_sum;
         if (!(ok = exchange())) break;
-        if (!(ok = warp_wait(bar(kBarPV + 3), par, gave_up))) break;
-        tc_fence_after();
+        const float4 t4 = *reinterpret_cast<const float4 *>(top + (lane & (HG - 1)) * 4);
+        const float total = (t4.x + t4.y) + (t4.z + t4.w), inv = total == 0.f ? 0.f : 1.f / total;
         const bool whole = item_ends && first_tile == 0;
         const uint32_t slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
-        float inv[HG];
-#pragma unroll
-        for (int h = 0; h < HG; ++h) {
-          const float4 t4 = *reinterpret_cast<const float4 *>(top + h * 4);
-          const float s = (t4.x + t4.y) + (t4.z + t4.w), m = new_ref[h];
-          inv[h] = s == 0.f ? 0.f : 1.f / s;
-          if (quad == 0 && lane == (uint32_t)h) {
-            const uint32_t head = grp * HG + h;
-            const float l2 = (m == -INFINITY ? 0.f : m) + log2f(s);
-            if (!whole)
-              p.part_lse[(uint64_t)slot * NH + head] = l2;
-            else if (p.a.lse && w.h0 + head < p.a.heads)
-              p.a.lse[(uint64_t)w.token * p.a.heads + w.h0 + head] = l2 * 0.693147180559945309f;
-          }
+        if (quad == 0 && lane < HG) {
+          const uint32_t head = grp * HG + lane;
+          const float l2 = (ref == -INFINITY ? 0.f : ref) + log2f(total);
+          if (!whole)
+            p.part_lse[(uint64_t)slot * NH + head] = l2;
+          else if (p.a.lse && w.h0 + head < p.a.heads)
+            p.a.lse[(uint64_t)w.token * p.a.heads + w.h0 + head] = l2 * 0.693147180559945309f;
         }
+#pragma unroll
+        for (int h = 0; h < HG; ++h) sum[h] = __shfl_sync(0xffffffffu, inv, h);
+        const uint32_t h0 = w.h0 + grp * HG;
+        const int heads = p.a.heads < h0 ? 0 : p.a.heads - h0 < HG ? (int)(p.a.heads - h0) : HG;
+        __nv_bfloat16 *out = (__nv_bfloat16 *)p.a.out + ((uint64_t)w.token * p.a.heads + h0) * ULA_ROW_LATENT + mine;
+        float *part = p.part_out + ((uint64_t)slot * NH + grp * HG) * ULA_ROW_LATENT + mine;
 #pragma unroll 1
         for (uint32_t b = 0; b < 4; ++b) {
+          if (!(ok = warp_wait(bar(kBarPV + b), par, gave_up))) break;
+          tc_fence_after();
           float o[HG];
           tmem_ld<HG>(lanes + b * NH + grp * HG, o);
           tc_wait_ld();
+          if (whole) {
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const uint32_t head = grp * HG + h;
-            if (w.h0 + head < p.a.heads) {
-              if (whole)
-                ((__nv_bfloat16 *)p.a.out)[((uint64_t)w.token * p.a.heads + w.h0 + head) * ULA_ROW_LATENT + b * 128 + mine] =
-                    __float2bfloat16_rn(o[h] * inv[h]);
-              else
-                p.part_out[((uint64_t)slot * NH + head) * ULA_ROW_LATENT + b * 128 + mine] = o[h] * inv[h];
-            }
+            for (int h = 0; h < HG; ++h)
+              if (h < heads) out[h * (int)ULA_ROW_LATENT + b * 128] = __float2bfloat16_rn(o[h] * sum[h]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < HG; ++h)
+              if (h < heads) part[h * (int)ULA_ROW_LATENT + b * 128] = o[h] * sum[h];
           }
         }
-        // (top is written again only after the next tile's barriers)
+        if (!ok) break;
         start = true;
       }
       if (item_ends) {
@@ -615,17 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         ++w.tile;
       }
     }
-    if (issuer) {  // every product has ended before the block's TMEM goes
-      mma_commit(bar(kBarEnd));
-      const unsigned long long t0 = global_ns();
-      while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0)
+  if (warp == kWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 

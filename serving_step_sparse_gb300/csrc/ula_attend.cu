@@ -27,11 +27,12 @@ __device__ int g_status;  // the first error that a kernel of this file latched
 constexpr uint32_t kTile = 128;                      // rows per tile
 constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
 constexpr uint32_t kGroups = 9;                      // 8 of latents, 1 of rope
-constexpr uint32_t kWarps = 8;                       // compute warps; the ninth issues the products
+constexpr uint32_t kWarps = 16;                      // compute warps; then the issuing and the loading one
 constexpr uint32_t kThreads = (kWarps + 4) * 32;     // (registers move between groups of 4 warps)
-// Launched with 168 registers a thread: 3 * 168 = 2 * 216 + 72.
-constexpr uint32_t kRegsCompute = 216, kRegsIssue = 72;
-constexpr uint32_t kSlots = kTile / (4 * kWarps);    // rows per lane of the widening
+// Launched with 96 registers a thread: 5 * 96 = 4 * 104 + 64.
+constexpr uint32_t kRegsCompute = 104, kRegsIssue = 64;
+constexpr uint32_t kLoaders = 2;                     // loading warps, 64 rows each
+constexpr uint32_t kSlots = kTile / (4 * kWarps / 2);  // rows per lane of the widening
 constexpr uint32_t kColS = 256;                      // TMEM: O^T in columns 0.., S^T from here
 
 struct AttendParams {
@@ -117,6 +118,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
 
+// 16 bytes to shared memory without passing through registers; zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// This thread's arrival, once its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -124,6 +135,10 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 // N consecutive TMEM columns of this warp's 32 lanes.
 template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]);
 template <int N> __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]);
+template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t addr, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
+}
 template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
@@ -137,14 +152,9 @@ template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float (&v
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
         "=f"(v[15]) : "r"(addr) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float (&v)[32]) {
-  tmem_ld<16>(addr, reinterpret_cast<float (&)[16]>(v[0]));
-  tmem_ld<16>(addr + 16, reinterpret_cast<float (&)[16]>(v[16]));
-}
-template <> __device__ __forceinline__ void tmem_st<8>(uint32_t addr, const float (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
-               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-                 "r"(addr) : "memory");
+template <> __device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
+               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ float warp_max(float v) {  // NaN counts for nothing
@@ -217,19 +227,17 @@ template <uint32_t NH>
 struct Shared {
   static constexpr uint32_t q = 0;                            // [9][NH][128 B]
   static constexpr uint32_t k = kGroups * NH * 128;           // [9][128][128 B]
-  static constexpr uint32_t top = k + kGroups * kGroupBytes;  // [NH][4] tile maxima (then sums) by quadrant
+  static constexpr uint32_t scale = k + kGroups * kGroupBytes;  // [128][4] the rows' scales
+  static constexpr uint32_t place = scale + kTile * 16;       // [2][128] the rows' addresses, 0: no row
+  static constexpr uint32_t top = place + 2 * kTile * 8;      // [NH][4] tile maxima (then sums) by quadrant
   static constexpr uint32_t bars = top + NH * 16;
   static constexpr uint32_t words = bars + 32 * 8;            // TMEM address, gave_up
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
 
-enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarEnd = 19 };
+enum { kBarFull = 0, kBarS = 5, kBarLand = 10, kBarDrained = 15, kBarP = 16, kBarPV = 18, kBarX = 22, kBarPlace = 26, kBarEnd = 27 };
 
-__device__ __forceinline__ uint4 load16(const uint8_t *row, uint32_t at) {
-  return row ? __ldg(reinterpret_cast<const uint4 *>(row + at)) : make_uint4(0, 0, 0, 0);
-}
-
-// The tiles of a block: from `first`, in item order.
+// The tiles of a block, in item order.
 struct Place {
   uint32_t item, tile;       // the tile's item and place in it
   uint32_t token, req, qi, h0;
@@ -253,45 +261,56 @@ __device__ __forceinline__ void step(const AttendParams &p, Place &w) {
 }
 
 // Entry e of a tile's query token as it stands in memory (0 past the list).  What it means is
-// worked out by row_of, when the rows are fetched: a comparison here would wait for the load.
+// worked out when the rows are fetched: a comparison here would wait for the load.
 __device__ __forceinline__ int32_t entry_of(const AttendParams &p, const Place &at, uint32_t e) {
   return e < p.a.k ? __ldg(p.a.entry_row + (uint64_t)at.token * p.a.k + e) : 0;
 }
 
-__device__ __forceinline__ const uint8_t *row_of(const AttendParams &p, const Place &at, uint32_t e, int32_t u) {
+// Its row (0: none).  Entries behind the list stand for the request's own rows.
+__device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &at, uint32_t e, int32_t u) {
   if (e < p.a.k)
-    return u >= 0 && (uint32_t)u < p.a.n_rows ? (const uint8_t *)p.a.rows + (uint64_t)u * ULA_ROW_BYTES : nullptr;
-  const uint32_t j = e - p.a.k;  // an own row
-  if (e >= p.keys || j > at.qi) return nullptr;
-  return (const uint8_t *)p.a.own_rows + at.req * p.a.own_req_stride + j * p.a.own_tok_stride;
+    return u >= 0 && (uint32_t)u < p.a.n_rows ? (uint64_t)p.a.rows + (uint64_t)u * ULA_ROW_BYTES : 0;
+  const uint32_t j = e - p.a.k;
+  if (e >= p.keys || j > at.qi) return 0;
+  return (uint64_t)p.a.own_rows + at.req * p.a.own_req_stride + j * p.a.own_tok_stride;
 }
 
 // Persistent: one block per SM, block c runs an even share of all tiles, item after item
 // (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
-// joins them).  Eight compute warps bring a tile's rows into registers one tile ahead, widen
-// the codes to bf16 in shared memory and run the softmax; warp w reads TMEM lanes (rows)
-// 32 (w % 4).. and the heads of column group w / 4.  A ninth warp issues the products.
+// joins them).  Two warps fetch the rows with asynchronous copies, 16 compute warps widen
+// their codes to bf16 and run the softmax, one warp issues the products.  Compute warp w
+// reads TMEM lanes (rows) 32 (w % 4).. and the heads of column group w / 4.
 //
-// Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
-// 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_2 take
-// theirs and P_3 the rope's.  So the next tile's blocks are widened in the order 1, 2, 3, 0,
-// rope as O_1, O_2, O_3 finish, beside the rest of the products.
+// Shared memory holds one tile, and the tile's own parts make room for everything else:
+//  * block b's codes land in the second half of the room that they fill once widened; a
+//    row is widened in place by the 8 lanes that have all read it;
+//  * P (P_b = p * s_b, 16 KB): P_0 takes the rope's place; after O_0 has read block 0's
+//    codes, P_1 and P_2 take theirs and P_3 the rope's.
+// So the next tile's blocks are fetched and widened in the order 1, 2, 0, 3, rope as O_1, O_2
+// and O_3 finish, beside the rest of the products.  (Rows fetched by plain loads into
+// registers one tile ahead: the loads of a tile, 82 KB, met the L1 room that 224 KB of shared
+// memory leave, and held up the shared-memory instructions behind them; 177 us against XXX
+// for the long-document step with 128 heads.)
 template <uint32_t NH>
-__global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+k_attend(const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NH>;
-  constexpr int HG = NH / 2;  // heads per column group
+  constexpr int HG = NH / 4;  // heads per column group
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
   volatile uint32_t *gave_up = reinterpret_cast<volatile uint32_t *>(sm + L::words + 4);
   if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < 5; ++i) mbar_init(bar(kBarFull + i), kWarps), mbar_init(bar(kBarS + i), 1);
+    for (uint32_t i = 0; i < 5; ++i) {
+      mbar_init(bar(kBarFull + i), kWarps / 2), mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarLand + i), kLoaders * 32);
+    }
+    mbar_init(bar(kBarPlace), kLoaders);
     mbar_init(bar(kBarDrained), kWarps);
     mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1);
-    mbar_init(bar(kBarX), 4), mbar_init(bar(kBarX + 1), 4);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
     mbar_init(bar(kBarEnd), 1);
     *gave_up = 0;
     fence_async_smem();
@@ -316,61 +335,119 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kWarps) {
-    // ---- the products.  The warp waits as one and one elected lane issues: so the operands'
-    // descriptors stay in uniform registers (53 clocks an MMA of N = 64, which is what its
-    // 6 KB of operands take; issued under a thread's own branch it took 63, whatever N)
-    // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
-    constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
-    constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
-    uint32_t tile = w.tile;
-    bool ok = true, fresh = true;
-    for (uint32_t n = 0; n < count && ok; ++n) {
-      const uint32_t par = n & 1;
+      // ---- the products.  The warp waits as one and one elected lane issues: so the operands'
+      // descriptors stay in uniform registers (53 clocks an MMA of N = 64, which is what its
+      // 6 KB of operands take; issued under a thread's own branch it took 63, whatever N)
+      // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
+      constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
+      constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
+      uint32_t tile = w.tile;
+      bool ok = true, fresh = true;
+      for (uint32_t n = 0; n < count && ok; ++n) {
+        const uint32_t par = n & 1;
 #pragma unroll 1
-      for (uint32_t i = 0; i < 5; ++i) {
-        // block 1, 2, 3, 0, then the rope's part, which goes to block 1's columns once they
-        // have been read
-        const uint32_t b = i < 4 ? (i + 1) & 3 : 4;
-        if (b == 4 && !(ok = warp_wait(bar(kBarDrained), par, gave_up))) break;
-        if (!(ok = warp_wait(bar(kBarFull + b), par, gave_up))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
-        const uint64_t da = operand(sk + 2 * b * kGroupBytes, 16), db = operand(base + L::q + 2 * b * NH * 128, 16);
-        if (elect_one()) {
+        for (uint32_t i = 0; i < 5; ++i) {
+          // block 1, 2, 0, 3, then the rope's part, which goes to block 1's columns once they
+          // have been read
+          const uint32_t b = i == 0 ? 1 : i == 1 ? 2 : i == 2 ? 0 : i;
+          if (b == 4 && !(ok = warp_wait(bar(kBarDrained), par, gave_up))) break;
+          if (!(ok = warp_wait(bar(kBarFull + b), par, gave_up))) break;
+          if (fresh && i == 0 && !(ok = warp_wait(bar(kBarFull + 2), par, gave_up))) break;  // (every warp's queries)
+          tc_fence_after();
+          const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
+          const uint64_t da = operand(sk + 2 * b * kGroupBytes, 16), db = operand(base + L::q + 2 * b * NH * 128, 16);
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t s = 0; s < 4; ++s) mma_bf16(d, da + 2 * s, db + 2 * s, kIdS, s != 0);
-          if (b < 4) {
+            for (uint32_t s = 0; s < 4; ++s) mma_bf16(d, da + 2 * s, db + 2 * s, kIdS, s != 0);
+            if (b < 4) {
 #pragma unroll
-            for (uint32_t s = 0; s < 4; ++s)
-              mma_bf16(d, da + (kGroupBytes >> 4) + 2 * s, db + (NH * 128 >> 4) + 2 * s, kIdS, true);
+              for (uint32_t s = 0; s < 4; ++s)
+                mma_bf16(d, da + (kGroupBytes >> 4) + 2 * s, db + (NH * 128 >> 4) + 2 * s, kIdS, true);
+            }
+            mma_commit(bar(kBarS + b));
           }
-          mma_commit(bar(kBarS + b));
+          __syncwarp();
         }
-        __syncwarp();
-      }
 #pragma unroll 1
-      for (uint32_t b = 0; b < 4 && ok; ++b) {
-        if (b < 2 && !(ok = warp_wait(bar(kBarP + b), par, gave_up))) break;
-        tc_fence_after();
-        const uint64_t da = operand(sk + 2 * b * kGroupBytes, kGroupBytes);
-        const uint64_t db = operand(sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes, kGroupBytes);
-        if (elect_one()) {
+        for (uint32_t b = 0; b < 4 && ok; ++b) {
+          if (b < 2 && !(ok = warp_wait(bar(kBarP + b), par, gave_up))) break;
+          tc_fence_after();
+          const uint64_t da = operand(sk + 2 * b * kGroupBytes, kGroupBytes);
+          const uint64_t db = operand(sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes, kGroupBytes);
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t s = 0; s < 8; ++s)
-            mma_bf16(tmem + b * NH, da + s * 128, db + s * 128, kIdO, s != 0 || !fresh);
-          mma_commit(bar(kBarPV + b));
+            for (uint32_t s = 0; s < 8; ++s)
+              mma_bf16(tmem + b * NH, da + s * 128, db + s * 128, kIdO, s != 0 || !fresh);
+            mma_commit(bar(kBarPV + b));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        fresh = false;
+        if (++tile == p.tiles) tile = 0, fresh = true;
       }
-      fresh = false;
-      if (++tile == p.tiles) tile = 0, fresh = true;
-    }
-    if (elect_one()) {  // every product has ended before the block's TMEM goes
-      mma_commit(bar(kBarEnd));
-      const unsigned long long t0 = global_ns();
-      while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
-    }
-    __syncwarp();
+      if (elect_one()) {  // every product has ended before the block's TMEM goes
+        mma_commit(bar(kBarEnd));
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
+      }
+      __syncwarp();
+    } else if (warp <= kWarps + kLoaders) {
+      // ---- the rows: this warp's 64 of every tile.  A lane works out two rows' addresses, one
+      // tile ahead; 8 lanes copy a block of a row.
+      decode<NH>(p, w);
+      const uint32_t r0 = (warp - kWarps - 1) * 64;
+      int32_t u[2];
+      auto fetch_entries = [&]() {
+        u[0] = entry_of(p, w, w.tile * kTile + r0 + lane);
+        u[1] = entry_of(p, w, w.tile * kTile + r0 + lane + 32);
+      };
+      uint64_t row[16];  // of rows lane / 8, lane / 8 + 4, ... (0: none)
+      auto place_rows = [&](uint32_t par) {
+        uint64_t *place = reinterpret_cast<uint64_t *>(sm + L::place) + par * kTile + r0;
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) place[lane + 32 * j] = row_of(p, w, w.tile * kTile + r0 + lane + 32 * j, u[j]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPlace));
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i) row[i] = place[4 * i + (lane >> 3)];
+      };
+      auto fetch = [&](uint32_t b) {
+        // (16-byte chunk c of a row lands at c ^ 4 in odd rows: see widen)
+        const uint32_t c = (lane & 7) ^ ((lane >> 1) & 4);
+        const uint32_t dst = sk + (b == 4 ? 8 : 2 * b + 1) * kGroupBytes + (r0 + (lane >> 3)) * 128 + c * 16;
+        const uint32_t at = b * 128 + (b == 4 ? 16 : 0) + (lane & 7) * 16;
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i)
+          copy16(dst + i * 512, (const void *)(row[i] ? row[i] + at : (uint64_t)p.a.q), row[i] ? 16 : 0);
+        copy_arrive(bar(kBarLand + b));
+      };
+      auto fetch_scales = [&](uint32_t par) {  // (reported as block 1, which never lands here)
+        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile + r0;
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+          const uint64_t r = place[lane + 32 * j];
+          copy16(base + L::scale + (r0 + lane + 32 * j) * 16, (const void *)(r ? r + ULA_ROW_LATENT : (uint64_t)p.a.q), r ? 16 : 0);
+        }
+        copy_arrive(bar(kBarLand + 1));
+      };
+      fetch_entries();
+      place_rows(0);
+      for (uint32_t n = 0; n < count; ++n) {
+        const uint32_t par = n & 1, prev = par ^ 1;
+        if (n + 1 < count) {
+          step<NH>(p, w);
+          fetch_entries();
+        }
+        if (n && !warp_wait(bar(kBarPV + 1), prev, gave_up)) break;
+        fetch_scales(par);
+        if (n && !warp_wait(bar(kBarPV + 2), prev, gave_up)) break;
+        fetch(0);
+        if (n && !warp_wait(bar(kBarPV + 3), prev, gave_up)) break;
+        fetch(3);
+        fetch(4);
+        if (n + 1 < count) place_rows(prev);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
@@ -378,8 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
     const uint32_t quad = warp & 3, grp = warp >> 2;
     const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
     const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
-    // widening: rows r0, r0 + 4, ..., 16 channels ch of each block
-    const uint32_t r0 = 4 * kSlots * warp + (lane >> 3), ch = lane & 7;
+    // widening: the first 8 warps do blocks 1, 0 and the rope, the others blocks 2 and 3;
+    // a lane rows r0, r0 + 4, ..., 16 channels ch of a block.  (A row's lanes lie so that each
+    // quarter of a warp, which is what a 16-byte access is served by, meets 8 different chunks
+    // of the swizzled rows.)
+    const bool second = warp >= kWarps / 2;
+    const uint32_t r0 = 4 * kSlots * (warp & (kWarps / 2 - 1)) + (lane & 1) + ((lane >> 4) << 1), ch = (lane >> 1) & 7;
     float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
     uint32_t xph = 0;
     auto exchange = [&]() -> bool {  // the four warps of a column group
@@ -389,33 +470,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
       xph ^= 1;
       return ok;
     };
-
-    uint4 raw[kSlots][5];
-    float4 next_scale, scale;
-    bool next_valid;
-    int32_t u[kSlots], um;
-    auto fetch_entries = [&](const Place &at) {
+    auto hand_over = [&](uint32_t b) {
+      fence_async_smem();
+      tc_fence_before();  // (this warp's TMEM accesses so far)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    uint4 raw[kSlots];
+    // the first block (1 or 2) of tile n comes through registers, so that it can be widened
+    // as soon as its room is free; the others land in their own room
+    auto fetch_first = [&](uint32_t n) -> bool {
+      if (!warp_wait(bar(kBarPlace), n & 1, gave_up)) return false;
+      const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile;
 #pragma unroll
-      for (uint32_t j = 0; j < kSlots; ++j) u[j] = entry_of(p, at, at.tile * kTile + r0 + 4 * j);
-      um = entry_of(p, at, at.tile * kTile + mine);
+      for (uint32_t j = 0; j < kSlots; ++j) {
+        const uint64_t row = place[r0 + 4 * j];
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + (second ? 256 : 128) + ch * 16));
+      }
+      return true;
     };
-    auto fetch_row = [&](const Place &at, uint32_t j) {
-      const uint8_t *a = row_of(p, at, at.tile * kTile + r0 + 4 * j, u[j]);
+    auto landed = [&](uint32_t b, uint32_t par) -> bool {
+      if (!warp_wait(bar(kBarLand + b), par, gave_up)) return false;
 #pragma unroll
-      for (uint32_t i = 0; i < 5; ++i) raw[j][i] = load16(a, i * 128 + (i == 4 ? 16 : 0) + ch * 16);
+      for (uint32_t j = 0; j < kSlots; ++j)
+        raw[j] = *reinterpret_cast<const uint4 *>(sm + L::k + (b == 4 ? 8 : 2 * b + 1) * kGroupBytes + (r0 + 4 * j) * 128 +
+                                                  ((ch ^ ((lane & 1) << 2)) << 4));
+      __syncwarp();  // a row's 8 lanes have read it
+      return true;
     };
-    auto fetch_scale = [&](const Place &at) {
-      const uint8_t *c = row_of(p, at, at.tile * kTile + mine, um);
-      const uint4 s = load16(c, ULA_ROW_LATENT);
-      next_scale = make_float4(__uint_as_float(s.x), __uint_as_float(s.y), __uint_as_float(s.z), __uint_as_float(s.w));
-      next_valid = c != nullptr;
-    };
-    // block b (4: rope) of the fetched rows into shared memory
+    // block b (4: rope) in its final form
     auto widen = [&](uint32_t b) {
 #pragma unroll
       for (uint32_t j = 0; j < kSlots; ++j) {
         const uint32_t r = r0 + 4 * j, x = r & 7;
-        const uint4 v = raw[j][b];
+        const uint4 v = raw[j];
         if (b == 4) {
           *reinterpret_cast<uint4 *>(sm + L::k + 8 * kGroupBytes + r * 128 + ((ch ^ x) << 4)) = v;
         } else {
@@ -427,33 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
               make_uint4(codes_to_bf16(v.z), codes_to_bf16(v.z >> 16), codes_to_bf16(v.w), codes_to_bf16(v.w >> 16));
         }
       }
-      fence_async_smem();
-      tc_fence_before();  // (this warp's TMEM reads of the tile before)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarFull + b));
-    };
-    auto hand_over = [&](uint32_t b) {
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(b));
+      hand_over(kBarFull + b);
     };
 
-    Place ahead = w;  // the tile whose entries are fetched next
-    bool ok = count > 0;
-    if (count > 0) {
-      fetch_entries(ahead);
-#pragma unroll
-      for (uint32_t j = 0; j < kSlots; ++j) fetch_row(ahead, j);
-      fetch_scale(ahead);
-      step<NH>(p, ahead);
-      if (count > 1) fetch_entries(ahead);
-    }
     float sum[HG], ref = -INFINITY;  // this row's sums; lane h: head h's running maximum
-    bool start = true;  // the first tile of a piece
+    bool start = true;               // the first tile of a piece
     uint32_t first_tile = w.tile;
+    bool ok = fetch_first(0);
     for (uint32_t n = 0; n < count && ok; ++n) {
-      const uint32_t par = n & 1, prev = par ^ 1;
+      const uint32_t par = n & 1;
       if (start) {
         first_tile = w.tile;
 #pragma unroll
@@ -466,26 +537,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
           const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
           const bool in = w.h0 + h < p.a.heads;
           const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+          copy16(dst, src, in ? 16 : 0);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
-      // ---- widen the tile, block by block as the products before let go of their room
-      if (n) ok = ok && warp_wait(bar(kBarPV + 1), prev, gave_up);
-      if (ok) widen(1);
-      if (n) ok = ok && warp_wait(bar(kBarPV + 2), prev, gave_up);
-      if (ok) widen(2);
-      if (n) ok = ok && warp_wait(bar(kBarPV + 3), prev, gave_up);
-      if (!ok) break;
-      widen(3);
-      widen(0);
+      // ---- widen the tile, block by block as there is room and as it lands
+      if (n && !(ok = warp_wait(bar(kBarPV + (second ? 2 : 1)), par ^ 1, gave_up))) break;
+      widen(second ? 2 : 1);
+      if (!second) {
+        if (!(ok = landed(0, par))) break;
+        widen(0);
+      }
+      // this row's scales; a row without an entry (its codes are zeros) gets logits of -inf
+      if (!(ok = warp_wait(bar(kBarLand + 1), par, gave_up))) break;
+      const float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
+      const float off = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] ? 0.f : -INFINITY;
 
-      // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0, a
-      // row without an entry (its codes are zeros) gets -inf.  Block 1's part comes first, so
-      // that the rope's product can take its columns.
-      scale = next_scale;
-      const float off = next_valid ? 0.f : -INFINITY;
-      const bool more = n + 1 < count;  // (the next tile's rows are fetched bit by bit)
+      // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0.
+      // Block 1's part comes first, so that the rope's product can take its columns.
       float z[HG];
       {
         float v[HG];
@@ -496,33 +565,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarDrained));
-        widen(4);
         const float s = scale.y * p.c0;
 #pragma unroll
         for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
-      if (more) fetch_row(ahead, 0);
+      if (!(ok = landed(second ? 3 : 4, par))) break;
+      widen(second ? 3 : 4);
       {
         float v[HG], x[HG];
         ok = warp_wait(bar(kBarS + 2), par, gave_up);
-        if (!(ok = ok && warp_wait(bar(kBarS + 3), par, gave_up))) break;
+        if (!(ok = ok && warp_wait(bar(kBarS), par, gave_up))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + 2 * NH + grp * HG, v);
-        tmem_ld<HG>(lanes + kColS + 3 * NH + grp * HG, x);
+        tmem_ld<HG>(lanes + kColS + grp * HG, x);
         tc_wait_ld();
-        float s = scale.z * p.c0, t = scale.w * p.c0;
+        float s = scale.z * p.c0, t = scale.x * p.c0;
 #pragma unroll
         for (int h = 0; h < HG; h += 2) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
-        ok = warp_wait(bar(kBarS), par, gave_up);
+        ok = warp_wait(bar(kBarS + 3), par, gave_up);
         if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
         tc_fence_after();
-        tmem_ld<HG>(lanes + kColS + grp * HG, v);
+        tmem_ld<HG>(lanes + kColS + 3 * NH + grp * HG, v);
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, x);
         tc_wait_ld();
-        s = scale.x * p.c0, t = p.c0;
+        s = scale.w * p.c0, t = p.c0;
 #pragma unroll
         for (int h = 0; h < HG; h += 2) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
@@ -541,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
         if (lane < HG) top[lane * 4 + quad] = t;
       }
-      if (more) fetch_row(ahead, 1);
       if (!(ok = exchange())) break;
       {
         const float4 t4 = *reinterpret_cast<const float4 *>(top + (lane & (HG - 1)) * 4);
@@ -552,17 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
           const float f = up ? ex2(ref - now) : 1.f;
 #pragma unroll
           for (int h = 0; h < HG; ++h) sum[h] *= __shfl_sync(0xffffffffu, f, h);
-          if (!start) {
+          if (!start) {  // (O^T of the tiles before is complete: block 3 and the rope have landed)
 #pragma unroll 1
             for (uint32_t b = 0; b < 4; ++b) {
 #pragma unroll
-              for (int c = 0; c < HG; c += 8) {
-                float o[8];
-                tmem_ld<8>(lanes + b * NH + grp * HG + c, o);
+              for (int c = 0; c < HG; c += 4) {
+                float o[4];
+                tmem_ld<4>(lanes + b * NH + grp * HG + c, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int h = 0; h < 8; ++h) o[h] *= __shfl_sync(0xffffffffu, f, c + h);
-                tmem_st<8>(lanes + b * NH + grp * HG + c, o);
+                for (int h = 0; h < 4; ++h) o[h] *= __shfl_sync(0xffffffffu, f, c + h);
+                tmem_st<4>(lanes + b * NH + grp * HG + c, o);
               }
             }
             tc_wait_st();
@@ -577,36 +645,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         }
       }
 
+      if (n + 1 < count && !(ok = fetch_first(n + 1))) break;
+
       // ---- P_b = p * s_b, a row's heads in one 128-byte row
       auto put = [&](float s, uint32_t group) {
+        uint32_t u[HG / 2];
+#pragma unroll
+        for (int h = 0; h < HG / 2; ++h) {
+          float lo, hi;
+          mul2(lo, hi, s, z[2 * h], z[2 * h + 1]);
+          u[h] = bf16x2(lo, hi);
+        }
         uint8_t *at = sm + L::k + group * kGroupBytes + mine * 128;
         const uint32_t x = mine & 7;
-#pragma unroll
-        for (int c = 0; c < HG / 8; ++c) {
-          uint32_t v[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float lo, hi;
-            mul2(lo, hi, s, z[8 * c + 2 * h], z[8 * c + 2 * h + 1]);
-            v[h] = bf16x2(lo, hi);
-          }
-          *reinterpret_cast<uint4 *>(at + (((HG / 8 * grp + c) ^ x) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        if constexpr (HG == 16) {
+          *reinterpret_cast<uint4 *>(at + (((2 * grp) ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4 *>(at + (((2 * grp + 1) ^ x) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
+        } else if constexpr (HG == 8) {
+          *reinterpret_cast<uint4 *>(at + ((grp ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+          *reinterpret_cast<uint2 *>(at + (((grp >> 1) ^ x) << 4) + (grp & 1) * 8) = make_uint2(u[0], u[1]);
         }
       };
       put(scale.x, 8);
       hand_over(kBarP);
-      if (more) fetch_row(ahead, 2);
+      Place next = w;
+      step<NH>(p, next);
       if (!(ok = warp_wait(bar(kBarPV), par, gave_up))) break;
       put(scale.y, 0);
       put(scale.z, 1);
       put(scale.w, 8);
       hand_over(kBarP + 1);
-      if (more) {
-        fetch_row(ahead, 3);
-        fetch_scale(ahead);
-        step<NH>(p, ahead);
-        if (n + 2 < count) fetch_entries(ahead);
-      }
       start = false;
 
       // ---- the end of a piece: normalise and write (a warp's 32 lanes: 32 channels of a head)
@@ -653,13 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend(const __grid_constant__ 
         if (!ok) break;
         start = true;
       }
-      if (item_ends) {
-        w.tile = 0;
-        ++w.item;
-        decode<NH>(p, w);
-      } else {
-        ++w.tile;
-      }
+      w = next;
     }
   }
   tc_fence_before();

@@ -1,7 +1,9 @@
-"""Build the CUDA library in-tree: csrc/*.cu -> _build/libula.so (sm_103a only).
+"""Build the CUDA library in-tree: csrc/*.cu -> _build/libula.so (sm_103a only), and the
+binding of the operators on rows: csrc/rows_binding.cpp -> _build/_rows.so.
 
 Translation units compile in parallel, then link into one shared library that
-exports the C ABI declared in include/ula.h.
+exports the C ABI declared in include/ula.h; the binding (a Python extension module
+against torch's headers) links with it.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libula.so")
+BINDING = os.path.join(OUT_DIR, "_rows.so")
 SOURCES = ["ula_kernels.cu", "ula_api.cu", "ula_noalloc.cu", "ula_rows.cu", "ula_attend.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -26,10 +29,38 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+CXX = os.environ.get("CXX", "g++")
+
+
+def _binding_flags() -> list[str]:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    flags = ["-O2", "-std=c++17", "-fPIC", "-Wall",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+             "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(NVCC))), "include")]
+    for p in include_paths():
+        flags += ["-isystem", p]
+    return flags
+
+
+def _link_binding(obj: str) -> None:
+    """Links with the library beside it and with torch's libraries."""
+    import torch
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    subprocess.run([CXX, "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libula.so",
+                    "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+                    "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+                    "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -44,6 +75,11 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
+    binding = os.path.join(OUT_DIR, "rows_binding.o")
+    cmd = [CXX, *_binding_flags(), "-c", os.path.join(CSRC, "rows_binding.cpp"), "-o", binding]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    procs.append(("rows_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -52,10 +88,11 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
     tmp = LIB + f".{os.getpid()}.tmp"
     subprocess.run([NVCC, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

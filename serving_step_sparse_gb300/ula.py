@@ -36,11 +36,8 @@ ERR_INTERNAL = 7
 PHASES = ["dedup", "rotate", "mark", "select", "move", "gather", "alloc", "free", "stage"]
 NOALLOC_MAX_ENTRIES = 65536
 
-ROW_BYTES, ROW_LATENT, ROW_ROPE, ROW_BLOCK = 656, 512, 64, 128
-ROPE_PAIRS, MAX_AXES, MAX_PARTS = 32, 8, 8
-TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
+ROPE_PAIRS, MAX_AXES = 32, 8
 PAIR_ADJACENT, PAIR_HALVES = 0, 1
-ROTATE_INVERSE = 1
 
 
 class ula_config(C.Structure):
@@ -87,19 +84,10 @@ class ula_span(C.Structure):
                 ("end_ns", C.c_uint64)]
 
 
+# the operators on rows are called through the extension module that rows.py loads
 class ula_rotary(C.Structure):
     _fields_ = [("n_axes", C.c_uint32), ("pairing", C.c_uint32),
                 ("freq", C.c_float * ROPE_PAIRS), ("axis", C.c_uint8 * ROPE_PAIRS)]
-
-
-class ula_attend_args(C.Structure):
-    _fields_ = [("q", C.c_void_p), ("q_req_stride", C.c_uint64), ("q_tok_stride", C.c_uint64),
-                ("q_head_stride", C.c_uint64), ("rows", C.c_void_p), ("entry_row", C.c_void_p),
-                ("own_rows", C.c_void_p), ("own_req_stride", C.c_uint64),
-                ("own_tok_stride", C.c_uint64), ("out", C.c_void_p), ("lse", C.c_void_p),
-                ("workspace", C.c_void_p), ("workspace_bytes", C.c_uint64),
-                ("n_rows", C.c_uint32), ("n_req", C.c_uint32), ("n_q", C.c_uint32),
-                ("heads", C.c_uint32), ("k", C.c_uint32), ("softmax_scale", C.c_float)]
 
 
 def _load():
@@ -159,17 +147,6 @@ def _load():
     lib.ula_tp_context.restype = p
     lib.ula_tp_destroy.argtypes = [p]
     lib.ula_tp_destroy.restype = i32
-    u64 = C.c_uint64
-    lib.ula_rows_rotate.argtypes = [p, u32, p, u64, u32, u32, u32, p, u64, u64, p, u64, u64, p]
-    lib.ula_rows_rotate.restype = i32
-    lib.ula_rows_pack.argtypes = [p, p, u64, u32, u32, p, u64, p, u64, p, u64, p]
-    lib.ula_rows_pack.restype = i32
-    lib.ula_rows_attend_workspace.argtypes = [u32, u32, u32, u32, i32]
-    lib.ula_rows_attend_workspace.restype = u64
-    lib.ula_rows_attend.argtypes = [C.POINTER(ula_attend_args), p]
-    lib.ula_rows_attend.restype = i32
-    lib.ula_rows_join.argtypes = [p, p, u32, u64, p, p, p]
-    lib.ula_rows_join.restype = i32
     lib.ula_rows_sync.argtypes = [p]
     lib.ula_rows_sync.restype = i32
     return lib
@@ -363,36 +340,6 @@ def ula_dedup_noalloc(d_sel: int, n: int, d_uniq: int, d_entry_row: int, d_n_uni
     """First-occurrence dedup without a context and without allocating (fixed scratch)."""
     _check(lib.ula_dedup_noalloc(d_sel, n, d_uniq, d_entry_row, d_n_uniq, stream),
            "ula_dedup_noalloc")
-
-
-def ula_rows_rotate(rotary: ula_rotary, flags: int, d_pos: int, pos_axis_stride: int, n: int,
-                    heads: int, dtype: int, d_x: int, x_token_stride: int, x_head_stride: int,
-                    d_out: int, out_token_stride: int, out_head_stride: int, stream) -> None:
-    _check(lib.ula_rows_rotate(C.addressof(rotary), flags, d_pos, pos_axis_stride, n, heads, dtype,
-                               d_x, x_token_stride, x_head_stride, d_out, out_token_stride,
-                               out_head_stride, stream), "ula_rows_rotate")
-
-
-def ula_rows_pack(rotary: ula_rotary, d_pos: int, pos_axis_stride: int, n: int, dtype: int,
-                  d_latent: int, latent_stride: int, d_rope: int, rope_stride: int, d_rows: int,
-                  row_stride: int, stream) -> None:
-    _check(lib.ula_rows_pack(C.addressof(rotary), d_pos, pos_axis_stride, n, dtype, d_latent,
-                             latent_stride, d_rope, rope_stride, d_rows, row_stride, stream),
-           "ula_rows_pack")
-
-
-def ula_rows_attend_workspace(n_req: int, n_q: int, heads: int, k: int, own: bool) -> int:
-    return lib.ula_rows_attend_workspace(n_req, n_q, heads, k, 1 if own else 0)
-
-
-def ula_rows_attend(args: ula_attend_args, stream) -> None:
-    _check(lib.ula_rows_attend(args, stream), "ula_rows_attend")
-
-
-def ula_rows_join(outs, lses, n: int, out: int, lse: int | None, stream) -> None:
-    """outs, lses: lists of integer device addresses, one of each for every part."""
-    _check(lib.ula_rows_join(_ptr_array(outs), _ptr_array(lses), len(outs), n, out, lse, stream),
-           "ula_rows_join")
 
 
 def ula_rows_sync(stream) -> None:

@@ -235,7 +235,7 @@ struct Shared {
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
 
-enum { kBarFull = 0, kBarS = 5, kBarLand = 10, kBarDrained = 15, kBarP = 16, kBarPV = 18, kBarX = 22, kBarPlace = 26, kBarEnd = 27 };
+enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarPlace = 21, kBarScale = 22, kBarEnd = 23 };
 
 // The tiles of a block, in item order.
 struct Place {
@@ -277,20 +277,16 @@ __device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &a
 
 // Persistent: one block per SM, block c runs an even share of all tiles, item after item
 // (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
-// joins them).  Two warps fetch the rows with asynchronous copies, 16 compute warps widen
-// their codes to bf16 and run the softmax, one warp issues the products.  Compute warp w
-// reads TMEM lanes (rows) 32 (w % 4).. and the heads of column group w / 4.
+// joins them).  16 compute warps fetch the rows' codes into registers one tile ahead, widen
+// them to bf16 in shared memory and run the softmax; two warps look the rows up and copy
+// their scales and rope channels; one warp issues the products.  Compute warp w reads TMEM
+// lanes (rows) 32 (w % 4).. and the heads of column group w / 4.
 //
-// Shared memory holds one tile, and the tile's own parts make room for everything else:
-//  * block b's codes land in the second half of the room that they fill once widened; a
-//    row is widened in place by the 8 lanes that have all read it;
-//  * P (P_b = p * s_b, 16 KB): P_0 takes the rope's place; after O_0 has read block 0's
-//    codes, P_1 and P_2 take theirs and P_3 the rope's.
-// So the next tile's blocks are fetched and widened in the order 1, 2, 0, 3, rope as O_1, O_2
-// and O_3 finish, beside the rest of the products.  (Rows fetched by plain loads into
-// registers one tile ahead: the loads of a tile, 82 KB, met the L1 room that 224 KB of shared
-// memory leave, and held up the shared-memory instructions behind them; 177 us against XXX
-// for the long-document step with 128 heads.)
+// Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
+// 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
+// theirs and P_2 the rope's.  So the next tile's blocks are widened in the order 1, 2, then 0
+// and 3, as O_1, O_2 and O_3 finish, beside the rest of the products; their codes wait in
+// registers, and the rope is copied in after O_2.
 template <uint32_t NH>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend(const __grid_constant__ AttendParams p) {
@@ -304,10 +300,10 @@ k_attend(const __grid_constant__ AttendParams p) {
   volatile uint32_t *gave_up = reinterpret_cast<volatile uint32_t *>(sm + L::words + 4);
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < 5; ++i) {
-      mbar_init(bar(kBarFull + i), kWarps / 2), mbar_init(bar(kBarS + i), 1);
-      mbar_init(bar(kBarLand + i), kLoaders * 32);
+      mbar_init(bar(kBarFull + i), i < 4 ? kWarps / 2 : kLoaders);
+      mbar_init(bar(kBarS + i), 1);
     }
-    mbar_init(bar(kBarPlace), kLoaders);
+    mbar_init(bar(kBarPlace), kLoaders), mbar_init(bar(kBarScale), kLoaders * 32);
     mbar_init(bar(kBarDrained), kWarps);
     mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
@@ -373,7 +369,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           if (b < 2 && !(ok = warp_wait(bar(kBarP + b), par, gave_up))) break;
           tc_fence_after();
           const uint64_t da = operand(sk + 2 * b * kGroupBytes, kGroupBytes);
-          const uint64_t db = operand(sk + (b == 1 ? 0 : b == 2 ? 1 : 8) * kGroupBytes, kGroupBytes);
+          const uint64_t db = operand(sk + (b == 1 ? 0 : b == 3 ? 1 : 8) * kGroupBytes, kGroupBytes);
           if (elect_one()) {
 #pragma unroll
             for (uint32_t s = 0; s < 8; ++s)
@@ -392,8 +388,8 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
       __syncwarp();
     } else if (warp <= kWarps + kLoaders) {
-      // ---- the rows: this warp's 64 of every tile.  A lane works out two rows' addresses, one
-      // tile ahead; 8 lanes copy a block of a row.
+      // ---- this warp's 64 rows of every tile: their addresses, one tile ahead (two a lane),
+      // their scales, and their rope channels straight to where the products read them
       decode<NH>(p, w);
       const uint32_t r0 = (warp - kWarps - 1) * 64;
       int32_t u[2];
@@ -401,51 +397,42 @@ k_attend(const __grid_constant__ AttendParams p) {
         u[0] = entry_of(p, w, w.tile * kTile + r0 + lane);
         u[1] = entry_of(p, w, w.tile * kTile + r0 + lane + 32);
       };
-      uint64_t row[16];  // of rows lane / 8, lane / 8 + 4, ... (0: none)
       auto place_rows = [&](uint32_t par) {
         uint64_t *place = reinterpret_cast<uint64_t *>(sm + L::place) + par * kTile + r0;
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j) place[lane + 32 * j] = row_of(p, w, w.tile * kTile + r0 + lane + 32 * j, u[j]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPlace));
-#pragma unroll
-        for (uint32_t i = 0; i < 16; ++i) row[i] = place[4 * i + (lane >> 3)];
-      };
-      auto fetch = [&](uint32_t b) {
-        // (16-byte chunk c of a row lands at c ^ 4 in odd rows: see widen)
-        const uint32_t c = (lane & 7) ^ ((lane >> 1) & 4);
-        const uint32_t dst = sk + (b == 4 ? 8 : 2 * b + 1) * kGroupBytes + (r0 + (lane >> 3)) * 128 + c * 16;
-        const uint32_t at = b * 128 + (b == 4 ? 16 : 0) + (lane & 7) * 16;
-#pragma unroll
-        for (uint32_t i = 0; i < 16; ++i)
-          copy16(dst + i * 512, (const void *)(row[i] ? row[i] + at : (uint64_t)p.a.q), row[i] ? 16 : 0);
-        copy_arrive(bar(kBarLand + b));
-      };
-      auto fetch_scales = [&](uint32_t par) {  // (reported as block 1, which never lands here)
-        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile + r0;
-#pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) {
-          const uint64_t r = place[lane + 32 * j];
-          copy16(base + L::scale + (r0 + lane + 32 * j) * 16, (const void *)(r ? r + ULA_ROW_LATENT : (uint64_t)p.a.q), r ? 16 : 0);
-        }
-        copy_arrive(bar(kBarLand + 1));
       };
       fetch_entries();
       place_rows(0);
       for (uint32_t n = 0; n < count; ++n) {
         const uint32_t par = n & 1, prev = par ^ 1;
+        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile + r0;
         if (n + 1 < count) {
           step<NH>(p, w);
           fetch_entries();
         }
         if (n && !warp_wait(bar(kBarPV + 1), prev, gave_up)) break;
-        fetch_scales(par);
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j) {
+          const uint64_t row = place[lane + 32 * j];
+          copy16(base + L::scale + (r0 + lane + 32 * j) * 16, (const void *)(row ? row + ULA_ROW_LATENT : (uint64_t)p.a.q), row ? 16 : 0);
+        }
+        copy_arrive(bar(kBarScale));
         if (n && !warp_wait(bar(kBarPV + 2), prev, gave_up)) break;
-        fetch(0);
-        if (n && !warp_wait(bar(kBarPV + 3), prev, gave_up)) break;
-        fetch(3);
-        fetch(4);
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i) {
+          const uint32_t r = r0 + 4 * i + (lane >> 3), ch = lane & 7;
+          const uint64_t row = place[4 * i + (lane >> 3)];
+          copy16(sk + 8 * kGroupBytes + r * 128 + ((ch ^ (r & 7)) << 4),
+                 (const void *)(row ? row + ULA_ROW_LATENT + 16 + ch * 16 : (uint64_t)p.a.q), row ? 16 : 0);
+        }
         if (n + 1 < count) place_rows(prev);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFull + 4));
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -455,10 +442,10 @@ k_attend(const __grid_constant__ AttendParams p) {
     const uint32_t quad = warp & 3, grp = warp >> 2;
     const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
     const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
-    // widening: the first 8 warps do blocks 1, 0 and the rope, the others blocks 2 and 3;
-    // a lane rows r0, r0 + 4, ..., 16 channels ch of a block.  (A row's lanes lie so that each
-    // quarter of a warp, which is what a 16-byte access is served by, meets 8 different chunks
-    // of the swizzled rows.)
+    // widening: the first 8 warps do blocks 1 and 0, the others 2 and 3; a lane rows r0,
+    // r0 + 4, ..., 16 channels ch of a block.  (A row's lanes lie so that each quarter of a
+    // warp, which is what a 16-byte access is served by, meets 8 different chunks of the
+    // swizzled rows.)
     const bool second = warp >= kWarps / 2;
     const uint32_t r0 = 4 * kSlots * (warp & (kWarps / 2 - 1)) + (lane & 1) + ((lane >> 4) << 1), ch = (lane >> 1) & 7;
     float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
@@ -476,53 +463,42 @@ k_attend(const __grid_constant__ AttendParams p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(b));
     };
-    uint4 raw[kSlots];
-    // the first block (1 or 2) of tile n comes through registers, so that it can be widened
-    // as soon as its room is free; the others land in their own room
-    auto fetch_first = [&](uint32_t n) -> bool {
-      if (!warp_wait(bar(kBarPlace), n & 1, gave_up)) return false;
+    const uint32_t block1 = second ? 2 : 1, block2 = second ? 3 : 0;
+    // codes of tile n's rows j0..j1-1, of one block; fetched in pieces between other work, since
+    // a piece's loads hold up what the load/store unit gets behind them
+    auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block, uint32_t j0, uint32_t j1) {
       const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile;
 #pragma unroll
-      for (uint32_t j = 0; j < kSlots; ++j) {
+      for (uint32_t j = j0; j < j1; ++j) {
         const uint64_t row = place[r0 + 4 * j];
         raw[j] = make_uint4(0, 0, 0, 0);
-        if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + (second ? 256 : 128) + ch * 16));
+        if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + block * 128 + ch * 16));
       }
-      return true;
     };
-    auto landed = [&](uint32_t b, uint32_t par) -> bool {
-      if (!warp_wait(bar(kBarLand + b), par, gave_up)) return false;
-#pragma unroll
-      for (uint32_t j = 0; j < kSlots; ++j)
-        raw[j] = *reinterpret_cast<const uint4 *>(sm + L::k + (b == 4 ? 8 : 2 * b + 1) * kGroupBytes + (r0 + 4 * j) * 128 +
-                                                  ((ch ^ ((lane & 1) << 2)) << 4));
-      __syncwarp();  // a row's 8 lanes have read it
-      return true;
-    };
-    // block b (4: rope) in its final form
-    auto widen = [&](uint32_t b) {
+    auto widen = [&](const uint4 (&raw)[kSlots], uint32_t b) {
 #pragma unroll
       for (uint32_t j = 0; j < kSlots; ++j) {
         const uint32_t r = r0 + 4 * j, x = r & 7;
         const uint4 v = raw[j];
-        if (b == 4) {
-          *reinterpret_cast<uint4 *>(sm + L::k + 8 * kGroupBytes + r * 128 + ((ch ^ x) << 4)) = v;
-        } else {
-          uint8_t *at = sm + L::k + (2 * b + (ch >> 2)) * kGroupBytes + r * 128;
-          const uint32_t c = 2 * (ch & 3);
-          *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
-              make_uint4(codes_to_bf16(v.x), codes_to_bf16(v.x >> 16), codes_to_bf16(v.y), codes_to_bf16(v.y >> 16));
-          *reinterpret_cast<uint4 *>(at + (((c + 1) ^ x) << 4)) =
-              make_uint4(codes_to_bf16(v.z), codes_to_bf16(v.z >> 16), codes_to_bf16(v.w), codes_to_bf16(v.w >> 16));
-        }
+        uint8_t *at = sm + L::k + (2 * b + (ch >> 2)) * kGroupBytes + r * 128;
+        const uint32_t c = 2 * (ch & 3);
+        *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
+            make_uint4(codes_to_bf16(v.x), codes_to_bf16(v.x >> 16), codes_to_bf16(v.y), codes_to_bf16(v.y >> 16));
+        *reinterpret_cast<uint4 *>(at + (((c + 1) ^ x) << 4)) =
+            make_uint4(codes_to_bf16(v.z), codes_to_bf16(v.z >> 16), codes_to_bf16(v.w), codes_to_bf16(v.w >> 16));
       }
       hand_over(kBarFull + b);
     };
 
+    uint4 raw1[kSlots], raw2[kSlots];
     float sum[HG], ref = -INFINITY;  // this row's sums; lane h: head h's running maximum
     bool start = true;               // the first tile of a piece
     uint32_t first_tile = w.tile;
-    bool ok = fetch_first(0);
+    bool ok = warp_wait(bar(kBarPlace), 0, gave_up);
+    if (ok) {
+      fetch(raw1, 0, block1, 0, kSlots);
+      fetch(raw2, 0, block2, 0, kSlots);
+    }
     for (uint32_t n = 0; n < count && ok; ++n) {
       const uint32_t par = n & 1;
       if (start) {
@@ -541,17 +517,16 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
-      // ---- widen the tile, block by block as there is room and as it lands
-      if (n && !(ok = warp_wait(bar(kBarPV + (second ? 2 : 1)), par ^ 1, gave_up))) break;
-      widen(second ? 2 : 1);
-      if (!second) {
-        if (!(ok = landed(0, par))) break;
-        widen(0);
-      }
+      // ---- widen the tile, block by block as there is room
+      if (n && !(ok = warp_wait(bar(kBarPV + block1), par ^ 1, gave_up))) break;
+      widen(raw1, block1);
+      if (n && !(ok = warp_wait(bar(kBarPV + 3), par ^ 1, gave_up))) break;
+      widen(raw2, block2);
       // this row's scales; a row without an entry (its codes are zeros) gets logits of -inf
-      if (!(ok = warp_wait(bar(kBarLand + 1), par, gave_up))) break;
+      if (!(ok = warp_wait(bar(kBarScale), par, gave_up))) break;
       const float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
       const float off = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] ? 0.f : -INFINITY;
+      const bool more = n + 1 < count;
 
       // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0.
       // Block 1's part comes first, so that the rope's product can take its columns.
@@ -569,8 +544,7 @@ k_attend(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
-      if (!(ok = landed(second ? 3 : 4, par))) break;
-      widen(second ? 3 : 4);
+      if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1, gave_up))) break;
       {
         float v[HG], x[HG];
         ok = warp_wait(bar(kBarS + 2), par, gave_up);
@@ -585,6 +559,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
+        if (more) fetch(raw1, n + 1, block1, 0, kSlots / 2);
         ok = warp_wait(bar(kBarS + 3), par, gave_up);
         if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
         tc_fence_after();
@@ -598,6 +573,8 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
       }
+
+      if (more) fetch(raw1, n + 1, block1, kSlots / 2, kSlots);
 
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
       // above it, so that O^T is seldom rescaled; p stays below 2^8.  Lane h keeps head h's.
@@ -620,7 +597,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           const float f = up ? ex2(ref - now) : 1.f;
 #pragma unroll
           for (int h = 0; h < HG; ++h) sum[h] *= __shfl_sync(0xffffffffu, f, h);
-          if (!start) {  // (O^T of the tiles before is complete: block 3 and the rope have landed)
+          if (!start) {  // (the products into O^T so far have ended: waited for above)
 #pragma unroll 1
             for (uint32_t b = 0; b < 4; ++b) {
 #pragma unroll
@@ -645,8 +622,6 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
       }
 
-      if (n + 1 < count && !(ok = fetch_first(n + 1))) break;
-
       // ---- P_b = p * s_b, a row's heads in one 128-byte row
       auto put = [&](float s, uint32_t group) {
         uint32_t u[HG / 2];
@@ -669,12 +644,13 @@ k_attend(const __grid_constant__ AttendParams p) {
       };
       put(scale.x, 8);
       hand_over(kBarP);
+      if (more) fetch(raw2, n + 1, block2, 0, kSlots);
       Place next = w;
       step<NH>(p, next);
       if (!(ok = warp_wait(bar(kBarPV), par, gave_up))) break;
       put(scale.y, 0);
-      put(scale.z, 1);
-      put(scale.w, 8);
+      put(scale.z, 8);
+      put(scale.w, 1);
       hand_over(kBarP + 1);
       start = false;
 
@@ -735,31 +711,51 @@ k_attend(const __grid_constant__ AttendParams p) {
 // Joins the partial results of the items that several blocks share: 128 threads per query
 // token and head, 4 channels each.
 __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh) {
-  const unsigned long long i = (unsigned long long)blockIdx.x * 2 + (threadIdx.x >> 7);
-  const uint32_t c = threadIdx.x & 127;
+  const uint32_t i = blockIdx.x * 2 + (threadIdx.x >> 7), c = threadIdx.x & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
-  const uint32_t head = (uint32_t)(i % p.a.heads), token = (uint32_t)(i / p.a.heads);
-  if (i >= (unsigned long long)p.a.n_req * p.a.n_q * p.a.heads) return;
+  const uint32_t token = i / p.a.heads, head = i - token * p.a.heads;
+  if (token >= p.a.n_req * p.a.n_q) return;
   const unsigned long long s = ((unsigned long long)token * p.head_tiles + head / nh) * p.tiles;
-  const uint32_t b0 = (uint32_t)(((s + 1) * p.blocks - 1) / p.total);
-  const uint32_t b1 = (uint32_t)(((s + p.tiles) * p.blocks - 1) / p.total);
+  auto owner = [&](unsigned long long tile) -> uint32_t {  // (64-bit divisions only where they have to be)
+    const unsigned long long x = (tile + 1) * p.blocks - 1;
+    return (x | p.total) >> 32 ? (uint32_t)(x / p.total) : (uint32_t)x / (uint32_t)p.total;
+  };
+  const uint32_t b0 = owner(s), b1 = owner(s + p.tiles - 1);
   if (b0 == b1) return;  // written whole
   const uint32_t h = head % nh;
-  auto slot = [&](uint32_t b) { return (uint64_t)2 * b + (b == b0 ? 1 : 0); };
-  float top = -INFINITY;
-  for (uint32_t b = b0; b <= b1; ++b) top = fmaxf(top, p.part_lse[slot(b) * nh + h]);
-  const float m = top == -INFINITY ? 0.f : top;
-  float total = 0.f;
+  // a running maximum over batches of parts, whose loads are all in flight together
+  constexpr uint32_t kBatch = 8;
+  float m = -INFINITY, total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (uint32_t b = b0; b <= b1; ++b) {
-    const float f = ex2(p.part_lse[slot(b) * nh + h] - m);
-    const float4 o = reinterpret_cast<const float4 *>(p.part_out + (slot(b) * nh + h) * ULA_ROW_LATENT)[c];
-    total += f;
-    acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
+  for (uint32_t b = b0; b <= b1; b += kBatch) {
+    float l[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (b + k <= b1) {
+        const uint64_t row = ((uint64_t)2 * (b + k) + (b + k == b0 ? 1 : 0)) * nh + h;
+        l[k] = __ldcs(p.part_lse + row);
+        o[k] = __ldcs(reinterpret_cast<const float4 *>(p.part_out + row * ULA_ROW_LATENT) + c);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) top = fmaxf(top, l[k]);
+    const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
+    m = top;
+    total *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      const float f = ex2(l[k] - ref);
+      total += f;
+      acc.x += f * o[k].x, acc.y += f * o[k].y, acc.z += f * o[k].z, acc.w += f * o[k].w;
+    }
   }
+  if (m == -INFINITY) m = 0.f;
   const float inv = total == 0.f ? 0.f : 1.f / total;
   __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
-  reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + i * ULA_ROW_LATENT)[c] = *reinterpret_cast<uint2 *>(r);
+  reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + (uint64_t)i * ULA_ROW_LATENT)[c] = *reinterpret_cast<uint2 *>(r);
   if (p.a.lse && c == 0) p.a.lse[i] = (m + log2f(total)) * 0.693147180559945309f;
 }
 
@@ -790,7 +786,7 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->nh = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   pl->head_tiles = (heads + pl->nh - 1) / pl->nh;
   const uint64_t items = tokens * pl->head_tiles;
-  if (items > 0x7fffffffull || items * heads > (1ull << 40)) return false;
+  if (items > 0x7fffffffull || tokens * heads > 0x7fffffffull) return false;
   pl->total = items * pl->tiles;
   const int sms = sm_count();
   if (sms < 1 || pl->total > (1ull << 48)) return false;

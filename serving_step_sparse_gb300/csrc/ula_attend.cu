@@ -42,6 +42,7 @@ struct AttendParams {
   uint32_t tiles;            // tiles per item
   uint32_t head_tiles;
   uint32_t keys;             // entries per query token, own rows included
+  uint32_t cluster;          // blocks of a cluster (one item each), or 1
   float c0;
   float *part_out;           // [2 * blocks][NH][512]: unfinished items' results, normalised
   float *part_lse;           // [2 * blocks][NH]: their log2 sums
@@ -275,6 +276,34 @@ __device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &a
   return (uint64_t)p.a.own_rows + at.req * p.a.own_req_stride + j * p.a.own_tok_stride;
 }
 
+// The join of partial results of one query head: 4 channels, a running maximum over batches
+// of parts (whose loads are all in flight together).
+struct Joined {
+  static constexpr uint32_t kBatch = 8;
+  float m = -INFINITY, total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(const float (&l)[kBatch], const float4 (&o)[kBatch]) {
+    float top = m;
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) top = fmaxf(top, l[k]);
+    const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
+    m = top;
+    total *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      const float f = ex2(l[k] - ref);
+      total += f;
+      acc.x += f * o[k].x, acc.y += f * o[k].y, acc.z += f * o[k].z, acc.w += f * o[k].w;
+    }
+  }
+  __device__ __forceinline__ void write(const ula_attend_args &a, uint64_t row, uint32_t c) const {
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const uint2 r = make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.out + row * ULA_ROW_LATENT)[c] = r;
+    if (a.lse && c == 0) a.lse[row] = ((m == -INFINITY ? 0.f : m) + log2f(total)) * 0.693147180559945309f;
+  }
+};
+
 // Persistent: one block per SM, block c runs an even share of all tiles, item after item
 // (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
 // joins them).  16 compute warps fetch the rows' codes into registers one tile ahead, widen
@@ -287,7 +316,10 @@ __device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &a
 // theirs and P_2 the rope's.  So the next tile's blocks are widened in the order 1, 2, then 0
 // and 3, as O_1, O_2 and O_3 finish, beside the rest of the products; their codes wait in
 // registers, and the rope is copied in after O_2.
-template <uint32_t NH>
+//
+// kCluster: the tiles of one item spread over the blocks of a cluster, which join their
+// results through each other's shared memory (no second kernel, no trip through L2).
+template <uint32_t NH, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend(const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw_smem[];
@@ -319,13 +351,23 @@ k_attend(const __grid_constant__ AttendParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::words), 0);
+  // (launched while the kernel before it ends: nothing above touches memory that it may write)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const unsigned long long first = p.total * blockIdx.x / p.blocks;
-  const uint32_t count = (uint32_t)(p.total * (blockIdx.x + 1) / p.blocks - first);
   Place w;
-  w.item = (uint32_t)(first / p.tiles);
-  w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
+  uint32_t count;
+  if (kCluster) {
+    w.item = blockIdx.x / p.cluster;
+    const uint32_t rank = blockIdx.x - w.item * p.cluster;
+    w.tile = rank * p.tiles / p.cluster;
+    count = (rank + 1) * p.tiles / p.cluster - w.tile;
+  } else {
+    const unsigned long long first = p.total * blockIdx.x / p.blocks;
+    count = (uint32_t)(p.total * (blockIdx.x + 1) / p.blocks - first);
+    w.item = (uint32_t)(first / p.tiles);
+    w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
+  }
   const uint32_t sk = base + L::k;
 
   if (warp >= kWarps) {
@@ -428,11 +470,16 @@ k_attend(const __grid_constant__ AttendParams p) {
           copy16(sk + 8 * kGroupBytes + r * 128 + ((ch ^ (r & 7)) << 4),
                  (const void *)(row ? row + ULA_ROW_LATENT + 16 + ch * 16 : (uint64_t)p.a.q), row ? 16 : 0);
         }
-        if (n + 1 < count) place_rows(prev);
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarFull + 4));
+        // The next addresses only once every compute warp has this tile's: a second arrival of
+        // one loading warp may not stand for the first of the other.
+        if (n + 1 < count) {
+          if (!warp_wait(bar(kBarFull + 1), par, gave_up) || !warp_wait(bar(kBarFull + 2), par, gave_up)) break;
+          place_rows(prev);
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -662,12 +709,14 @@ k_attend(const __grid_constant__ AttendParams p) {
         if (!(ok = exchange())) break;
         const float4 t4 = *reinterpret_cast<const float4 *>(top + (lane & (HG - 1)) * 4);
         const float total = (t4.x + t4.y) + (t4.z + t4.w), inv = total == 0.f ? 0.f : 1.f / total;
-        const bool whole = item_ends && first_tile == 0;
+        const bool whole = !kCluster && item_ends && first_tile == 0;
         const uint32_t slot = 2 * blockIdx.x + (first_tile == 0 ? 1 : 0);
         if (quad == 0 && lane < HG) {
           const uint32_t head = grp * HG + lane;
           const float l2 = (ref == -INFINITY ? 0.f : ref) + log2f(total);
-          if (!whole)
+          if (kCluster)
+            reinterpret_cast<float *>(sm + L::scale)[head] = l2;
+          else if (!whole)
             p.part_lse[(uint64_t)slot * NH + head] = l2;
           else if (p.a.lse && w.h0 + head < p.a.heads)
             p.a.lse[(uint64_t)w.token * p.a.heads + w.h0 + head] = l2 * 0.693147180559945309f;
@@ -678,6 +727,8 @@ k_attend(const __grid_constant__ AttendParams p) {
         const int heads = p.a.heads < h0 ? 0 : p.a.heads - h0 < HG ? (int)(p.a.heads - h0) : HG;
         __nv_bfloat16 *out = (__nv_bfloat16 *)p.a.out + ((uint64_t)w.token * p.a.heads + h0) * ULA_ROW_LATENT + mine;
         float *part = p.part_out + ((uint64_t)slot * NH + grp * HG) * ULA_ROW_LATENT + mine;
+        // (a cluster's results lie across the whole tile's room: no product may read it any more)
+        if (kCluster && !(ok = warp_wait(bar(kBarPV + 3), par, gave_up))) break;
 #pragma unroll 1
         for (uint32_t b = 0; b < 4; ++b) {
           if (!(ok = warp_wait(bar(kBarPV + b), par, gave_up))) break;
@@ -685,7 +736,11 @@ k_attend(const __grid_constant__ AttendParams p) {
           float o[HG];
           tmem_ld<HG>(lanes + b * NH + grp * HG, o);
           tc_wait_ld();
-          if (whole) {
+          if (kCluster) {
+            float *at = reinterpret_cast<float *>(sm + L::k) + grp * HG * ULA_ROW_LATENT + b * 128 + mine;
+#pragma unroll
+            for (int h = 0; h < HG; ++h) at[h * ULA_ROW_LATENT] = o[h] * sum[h];
+          } else if (whole) {
 #pragma unroll
             for (int h = 0; h < HG; ++h)
               if (h < heads) out[h * (int)ULA_ROW_LATENT + b * 128] = __float2bfloat16_rn(o[h] * sum[h]);
@@ -706,6 +761,39 @@ k_attend(const __grid_constant__ AttendParams p) {
   tc_fence_after();
   if (warp == kWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (kCluster) {
+    // every block of the cluster gets here, also one that has given up
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
+    const uint32_t token = item / p.head_tiles, h0 = (item - token * p.head_tiles) * NH;
+    const uint32_t heads = p.a.heads - h0 < NH ? p.a.heads - h0 : NH;
+    // (by the compute warps: the others have fewer registers)
+    const uint32_t last = warp < kWarps ? (rank + 1) * heads * 128 / p.cluster : 0;
+    for (uint32_t i = rank * heads * 128 / p.cluster + threadIdx.x; i < last; i += kWarps * 32) {
+      const uint32_t h = i >> 7, c = i & 127;
+      Joined j;
+      for (uint32_t b = 0; b < p.cluster; b += Joined::kBatch) {
+        float l[Joined::kBatch];
+        float4 o[Joined::kBatch];
+#pragma unroll
+        for (uint32_t k = 0; k < Joined::kBatch; ++k) {
+          l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b + k < p.cluster) {
+            uint32_t at_l, at_o;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_l) : "r"(base + L::scale + h * 4), "r"(b + k));
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_o) : "r"(sk + h * 2048 + c * 16), "r"(b + k));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l[k]) : "r"(at_l) : "memory");
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w) : "r"(at_o) : "memory");
+          }
+        }
+        j.add(l, o);
+      }
+      j.write(p.a, (uint64_t)token * p.a.heads + h0 + h, c);
+    }
+    // (a block's shared memory stays until the others have read it)
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 }
 
 // Joins the partial results of the items that several blocks share: 128 threads per query
@@ -713,6 +801,7 @@ k_attend(const __grid_constant__ AttendParams p) {
 __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh) {
   const uint32_t i = blockIdx.x * 2 + (threadIdx.x >> 7), c = threadIdx.x & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t token = i / p.a.heads, head = i - token * p.a.heads;
   if (token >= p.a.n_req * p.a.n_q) return;
   const unsigned long long s = ((unsigned long long)token * p.head_tiles + head / nh) * p.tiles;
@@ -723,15 +812,12 @@ __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ Atte
   const uint32_t b0 = owner(s), b1 = owner(s + p.tiles - 1);
   if (b0 == b1) return;  // written whole
   const uint32_t h = head % nh;
-  // a running maximum over batches of parts, whose loads are all in flight together
-  constexpr uint32_t kBatch = 8;
-  float m = -INFINITY, total = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (uint32_t b = b0; b <= b1; b += kBatch) {
-    float l[kBatch];
-    float4 o[kBatch];
+  Joined j;
+  for (uint32_t b = b0; b <= b1; b += Joined::kBatch) {
+    float l[Joined::kBatch];
+    float4 o[Joined::kBatch];
 #pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) {
+    for (uint32_t k = 0; k < Joined::kBatch; ++k) {
       l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (b + k <= b1) {
         const uint64_t row = ((uint64_t)2 * (b + k) + (b + k == b0 ? 1 : 0)) * nh + h;
@@ -739,24 +825,9 @@ __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ Atte
         o[k] = __ldcs(reinterpret_cast<const float4 *>(p.part_out + row * ULA_ROW_LATENT) + c);
       }
     }
-    float top = m;
-#pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) top = fmaxf(top, l[k]);
-    const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
-    m = top;
-    total *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-#pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) {
-      const float f = ex2(l[k] - ref);
-      total += f;
-      acc.x += f * o[k].x, acc.y += f * o[k].y, acc.z += f * o[k].z, acc.w += f * o[k].w;
-    }
+    j.add(l, o);
   }
-  if (m == -INFINITY) m = 0.f;
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  __nv_bfloat162 r[2] = {__floats2bfloat162_rn(acc.x * inv, acc.y * inv), __floats2bfloat162_rn(acc.z * inv, acc.w * inv)};
-  reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + (uint64_t)i * ULA_ROW_LATENT)[c] = *reinterpret_cast<uint2 *>(r);
-  if (p.a.lse && c == 0) p.a.lse[i] = (m + log2f(total)) * 0.693147180559945309f;
+  j.write(p.a, i, c);
 }
 
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -770,11 +841,13 @@ int sm_count() {
 }
 
 struct Plan {
-  uint32_t nh, head_tiles, tiles, keys, blocks;
+  uint32_t nh, head_tiles, tiles, keys, blocks, cluster;
   unsigned long long total;
-  bool parts;  // some item's tiles lie in several blocks
+  bool parts;  // some item's tiles lie in several blocks that are no cluster
   uint64_t workspace;
 };
+
+constexpr uint32_t kMostCluster = 8;  // (the portable size)
 
 bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool own, Plan *pl) {
   const uint64_t tokens = (uint64_t)n_req * n_q;
@@ -790,6 +863,14 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->total = items * pl->tiles;
   const int sms = sm_count();
   if (sms < 1 || pl->total > (1ull << 48)) return false;
+  pl->cluster = 1;
+  if (pl->tiles > 1 && pl->tiles <= kMostCluster && pl->total <= (unsigned)sms) {
+    pl->cluster = pl->tiles;
+    pl->blocks = (uint32_t)pl->total;
+    pl->parts = false;
+    pl->workspace = 0;
+    return true;
+  }
   pl->blocks = pl->total < (unsigned)sms ? (uint32_t)pl->total : (uint32_t)sms;
   if (pl->total / (pl->blocks ? pl->blocks : 1) > 0x7fffffffull) return false;
   pl->parts = pl->blocks && !(pl->total % pl->blocks == 0 && (pl->total / pl->blocks) % pl->tiles == 0);
@@ -797,17 +878,31 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   return true;
 }
 
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint32_t smem, uint32_t cluster,
+                   cudaStream_t st, Args... args) {
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <uint32_t NH>
 cudaError_t launch_attend(const AttendParams &p, cudaStream_t st) {
+  auto kernel = p.cluster > 1 ? k_attend<NH, true> : k_attend<NH, false>;
   // (idempotent and cheap; a per-device flag would have to know about device resets)
-  cudaError_t e = cudaFuncSetAttribute(k_attend<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shared<NH>::bytes;
-  cfg.stream = st;
-  return cudaLaunchKernelEx(&cfg, k_attend<NH>, p);
+  return launch(kernel, p.blocks, kThreads, Shared<NH>::bytes, p.cluster, st, p);
 }
 
 }  // namespace
@@ -835,24 +930,15 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   AttendParams p{};
   p.a = a;
   p.total = pl.total, p.blocks = pl.blocks, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
+  p.cluster = pl.cluster;
   p.c0 = a.softmax_scale * 1.44269504088896341f;
   p.part_out = (float *)a.workspace;
   p.part_lse = p.part_out + (uint64_t)2 * pl.blocks * pl.nh * ULA_ROW_LATENT;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = pl.nh == 16 ? launch_attend<16>(p, st) : pl.nh == 32 ? launch_attend<32>(p, st) : launch_attend<64>(p, st);
   if (e != cudaSuccess) return ULA_ERR_CUDA;
-  if (pl.parts) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((uint64_t)a.n_req * a.n_q * a.heads + 1) / 2));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_join_parts, p, pl.nh);
-  }
+  if (pl.parts)
+    e = launch(k_join_parts, (uint32_t)(((uint64_t)a.n_req * a.n_q * a.heads + 1) / 2), 256, 0, 1, st, p, pl.nh);
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 

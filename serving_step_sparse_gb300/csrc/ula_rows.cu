@@ -43,6 +43,13 @@ __device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos) 
   return make_float2(c, s);
 }
 
+// Every kernel here may be launched while the one before it on the stream ends, and lets the
+// next one do so: it waits before it touches memory.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -100,6 +107,7 @@ __global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ Rota
   const uint32_t t0 = (uint32_t)(row0 / p.heads), t1 = (uint32_t)(last / p.heads);
   const uint32_t h0 = (uint32_t)(row0 - (uint64_t)t0 * p.heads);
   const uint32_t c = threadIdx.x % kPer, r0 = threadIdx.x / kPer;
+  after_previous();
   uint4 lo[kItems], hi[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
@@ -158,6 +166,7 @@ template <typename T, bool kHalves>
 __global__ void __launch_bounds__(256) k_rotate_any(const __grid_constant__ RotateParams p) {
   const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const uint32_t j = threadIdx.x & 31;
+  after_previous();
   if (w >= (uint64_t)p.n * p.heads) return;
   const uint32_t t = (uint32_t)(w / p.heads), h = (uint32_t)(w % p.heads);
   const T *x = (const T *)p.x + t * p.xt + h * p.xh;
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams
     next_pos = posl[t];
   };
   uint64_t t = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  after_previous();
   if (t < p.n) fetch((uint32_t)t);
   for (; t < p.n; t += warps) {
     float v[16], amax = 0.f;
@@ -276,6 +286,7 @@ struct JoinParams {
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ JoinParams p) {
   const uint64_t i = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const uint32_t c = threadIdx.x & 63;
+  after_previous();
   if (i >= p.n) return;
   uint4 v[ULA_MAX_PARTS];
   float z[ULA_MAX_PARTS], top = -INFINITY;
@@ -319,6 +330,11 @@ cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t smem, cudaStream_t
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -450,6 +450,20 @@ def test_attend_repeats():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("R,Q,H,K", [(220, 1, 64, 11), (55, 2, 69, 11), (400, 1, 3, 100), (90, 2, 20, 300)])
+def test_attend_many_items(R, Q, H, K):
+    """More query tokens than blocks, so that a block takes several whole items, many times
+    over: blocks' warps drift apart and must not meet another tile's addresses."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(R, Q, H, K, 500, R + K, pads=0.2, own=True)
+    want = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(want, attend64(q, kv, entry, SCALE, own_rows))
+    for _ in range(300):
+        got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    rows.sync()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attend_other_stream():
     """Calls on streams of their own: inputs and temporaries are held until they have run."""
     from serving_step_sparse_gb300 import rows

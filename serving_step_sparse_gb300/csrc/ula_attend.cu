@@ -33,6 +33,7 @@ constexpr uint32_t kThreads = (kWarps + 4) * 32;     // (registers move between 
 constexpr uint32_t kRegsCompute = 104, kRegsIssue = 64;
 constexpr uint32_t kLoaders = 2;                     // loading warps, 64 rows each
 constexpr uint32_t kSlots = kTile / (4 * kWarps / 2);  // rows per lane of the widening
+constexpr uint32_t kMostCluster = 8;                  // (the portable size)
 constexpr uint32_t kColS = 256;                      // TMEM: O^T in columns 0.., S^T from here
 
 struct AttendParams {
@@ -339,10 +340,12 @@ k_attend(const __grid_constant__ AttendParams p) {
     mbar_init(bar(kBarDrained), kWarps);
     mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
     for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
-    mbar_init(bar(kBarEnd), 1);
+    mbar_init(bar(kBarEnd), 1), mbar_init(bar(kBarEnd + 1), 1);
     *gave_up = 0;
     fence_async_smem();
   }
+  // (an address read before its time, after a wait that ran out, is no address)
+  if (threadIdx.x < 2 * kTile) reinterpret_cast<uint64_t *>(sm + L::place)[threadIdx.x] = 0;
   if (warp == kWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::words) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -369,64 +372,88 @@ k_attend(const __grid_constant__ AttendParams p) {
     w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
   }
   const uint32_t sk = base + L::k;
+  // all threads of the cluster; those that have given up on a wait as well
+  auto meet = [] {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
 
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kWarps) {
-      // ---- the products.  The warp waits as one and one elected lane issues: so the operands'
-      // descriptors stay in uniform registers (53 clocks an MMA of N = 64, which is what its
-      // 6 KB of operands take; issued under a thread's own branch it took 63, whatever N)
+    if (warp == kWarps || warp == kWarps + 1 + kLoaders) {
+      // ---- the products, issued by two warps.  A warp waits as one and one elected lane
+      // issues, so that the operands' descriptors stay in uniform registers.  A wait is held
+      // up until the warp's products before it have left the queue (155 clocks each with the
+      // queue run dry), so the warps take the S_b^T in turn: 36 products of N = 64 in 1,900
+      // clocks, which is what their operands take, instead of 2,990.  For the same reason a
+      // wait that has run out does not leave the loop (the compiler would then take all that
+      // follows for divergent): the rest goes unwaited for, and is reported at the end.
       // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
       constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
       constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
-      uint32_t tile = w.tile;
-      bool ok = true, fresh = true;
-      for (uint32_t n = 0; n < count && ok; ++n) {
-        const uint32_t par = n & 1;
-#pragma unroll 1
-        for (uint32_t i = 0; i < 5; ++i) {
-          // block 1, 2, 0, 3, then the rope's part, which goes to block 1's columns once they
-          // have been read
-          const uint32_t b = i == 0 ? 1 : i == 1 ? 2 : i == 2 ? 0 : i;
-          if (b == 4 && !(ok = warp_wait(bar(kBarDrained), par, gave_up))) break;
-          if (!(ok = warp_wait(bar(kBarFull + b), par, gave_up))) break;
-          if (fresh && i == 0 && !(ok = warp_wait(bar(kBarFull + 2), par, gave_up))) break;  // (every warp's queries)
+      const uint64_t k_rows = operand(sk, 16), k_channels = operand(sk, kGroupBytes), q_rows = operand(base + L::q, 16);
+      // S_b^T; the rope's part (4) goes to block 1's columns
+      auto issue_s = [&](uint32_t b) {
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
+        const uint64_t da = k_rows + b * (2 * kGroupBytes >> 4), db = q_rows + b * (2 * NH * 128 >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (uint32_t s = 0; s < (b == 4 ? 4 : 8); ++s)
+            mma_bf16(d, da + (s >> 2) * (kGroupBytes >> 4) + (s & 3) * 2, db + (s >> 2) * (NH * 128 >> 4) + (s & 3) * 2, kIdS, s != 0);
+          mma_commit(bar(kBarS + b));
+        }
+        __syncwarp();
+      };
+      bool ok = true;
+      if (warp == kWarps) {
+        uint32_t tile = w.tile;
+        bool fresh = true;
+        for (uint32_t n = 0; n < count; ++n) {
+          const uint32_t par = n & 1;
+          ok = ok && warp_wait(bar(kBarFull + 1), par, gave_up);
+          ok = ok && warp_wait(bar(kBarFull + 2), par, gave_up);  // (every warp's queries)
+          issue_s(1);
+          ok = ok && warp_wait(bar(kBarFull), par, gave_up);
+          issue_s(0);
+          ok = ok && warp_wait(bar(kBarP), par, gave_up);
           tc_fence_after();
-          const uint32_t d = tmem + kColS + (b == 4 ? 1 : b) * NH;
-          const uint64_t da = operand(sk + 2 * b * kGroupBytes, 16), db = operand(base + L::q + 2 * b * NH * 128, 16);
-          if (elect_one()) {
 #pragma unroll
-            for (uint32_t s = 0; s < 4; ++s) mma_bf16(d, da + 2 * s, db + 2 * s, kIdS, s != 0);
-            if (b < 4) {
-#pragma unroll
-              for (uint32_t s = 0; s < 4; ++s)
-                mma_bf16(d, da + (kGroupBytes >> 4) + 2 * s, db + (NH * 128 >> 4) + 2 * s, kIdS, true);
+          for (uint32_t b = 0; b < 4; ++b) {  // O_b^T
+            if (b == 1) {
+              ok = ok && warp_wait(bar(kBarP + 1), par, gave_up);
+              tc_fence_after();
             }
-            mma_commit(bar(kBarS + b));
-          }
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (uint32_t b = 0; b < 4 && ok; ++b) {
-          if (b < 2 && !(ok = warp_wait(bar(kBarP + b), par, gave_up))) break;
-          tc_fence_after();
-          const uint64_t da = operand(sk + 2 * b * kGroupBytes, kGroupBytes);
-          const uint64_t db = operand(sk + (b == 1 ? 0 : b == 3 ? 1 : 8) * kGroupBytes, kGroupBytes);
-          if (elect_one()) {
+            const uint64_t da = k_channels + b * (2 * kGroupBytes >> 4);
+            const uint64_t db = k_channels + (b == 1 ? 0 : b == 3 ? 1 : 8) * (kGroupBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (uint32_t s = 0; s < 8; ++s)
-              mma_bf16(tmem + b * NH, da + s * 128, db + s * 128, kIdO, s != 0 || !fresh);
-            mma_commit(bar(kBarPV + b));
+              for (uint32_t s = 0; s < 8; ++s) mma_bf16(tmem + b * NH, da + s * 128, db + s * 128, kIdO, s != 0 || !fresh);
+              mma_commit(bar(kBarPV + b));
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          fresh = false;
+          if (++tile == p.tiles) tile = 0, fresh = true;
         }
-        fresh = false;
-        if (++tile == p.tiles) tile = 0, fresh = true;
+      } else {
+        for (uint32_t n = 0; n < count; ++n) {
+          const uint32_t par = n & 1;
+          ok = ok && warp_wait(bar(kBarFull + 1), par, gave_up);  // (every warp's queries)
+          ok = ok && warp_wait(bar(kBarFull + 2), par, gave_up);
+          issue_s(2);
+          ok = ok && warp_wait(bar(kBarFull + 3), par, gave_up);
+          issue_s(3);
+          ok = ok && warp_wait(bar(kBarFull + 4), par, gave_up);
+          ok = ok && warp_wait(bar(kBarDrained), par, gave_up);   // (block 1's columns have been read)
+          issue_s(4);
+        }
       }
+      const uint32_t end = bar(kBarEnd + (warp == kWarps ? 0 : 1));
       if (elect_one()) {  // every product has ended before the block's TMEM goes
-        mma_commit(bar(kBarEnd));
+        mma_commit(end);
         const unsigned long long t0 = global_ns();
-        while (!mbar_try(bar(kBarEnd), 0) && global_ns() - t0 < 1000000000ull) {}
+        while (!mbar_try(end, 0) && global_ns() - t0 < 1000000000ull) {}
       }
       __syncwarp();
     } else if (warp <= kWarps + kLoaders) {
@@ -483,6 +510,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    if (kCluster) meet();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
     decode<NH>(p, w);
@@ -490,11 +518,11 @@ k_attend(const __grid_constant__ AttendParams p) {
     const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
     const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
     // widening: the first 8 warps do blocks 1 and 0, the others 2 and 3; a lane rows r0,
-    // r0 + 4, ..., 16 channels ch of a block.  (A row's lanes lie so that each quarter of a
-    // warp, which is what a 16-byte access is served by, meets 8 different chunks of the
-    // swizzled rows.)
+    // r0 + 4, ..., 16 channels ch of a block.  16-byte accesses are served by quarters of a
+    // warp: a quarter loads 128 bytes of one row, and stores to 8 different chunks of its
+    // swizzled row, since lanes of the second half store their second chunk first.
     const bool second = warp >= kWarps / 2;
-    const uint32_t r0 = 4 * kSlots * (warp & (kWarps / 2 - 1)) + (lane & 1) + ((lane >> 4) << 1), ch = (lane >> 1) & 7;
+    const uint32_t r0 = 4 * kSlots * (warp & (kWarps / 2 - 1)) + (lane >> 3), ch = lane & 7;
     float *top = reinterpret_cast<float *>(sm + L::top) + grp * HG * 4;
     uint32_t xph = 0;
     auto exchange = [&]() -> bool {  // the four warps of a column group
@@ -528,11 +556,13 @@ k_attend(const __grid_constant__ AttendParams p) {
         const uint32_t r = r0 + 4 * j, x = r & 7;
         const uint4 v = raw[j];
         uint8_t *at = sm + L::k + (2 * b + (ch >> 2)) * kGroupBytes + r * 128;
-        const uint32_t c = 2 * (ch & 3);
+        const bool up = ch & 4;
+        const uint32_t c = 2 * (ch & 3) + (up ? 1 : 0);
+        const uint32_t p0 = up ? v.z : v.x, p1 = up ? v.w : v.y, q0 = up ? v.x : v.z, q1 = up ? v.y : v.w;
         *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
-            make_uint4(codes_to_bf16(v.x), codes_to_bf16(v.x >> 16), codes_to_bf16(v.y), codes_to_bf16(v.y >> 16));
-        *reinterpret_cast<uint4 *>(at + (((c + 1) ^ x) << 4)) =
-            make_uint4(codes_to_bf16(v.z), codes_to_bf16(v.z >> 16), codes_to_bf16(v.w), codes_to_bf16(v.w >> 16));
+            make_uint4(codes_to_bf16(p0), codes_to_bf16(p0 >> 16), codes_to_bf16(p1), codes_to_bf16(p1 >> 16));
+        *reinterpret_cast<uint4 *>(at + ((c ^ 1 ^ x) << 4)) =
+            make_uint4(codes_to_bf16(q0), codes_to_bf16(q0 >> 16), codes_to_bf16(q1), codes_to_bf16(q1 >> 16));
       }
       hand_over(kBarFull + b);
     };
@@ -541,6 +571,18 @@ k_attend(const __grid_constant__ AttendParams p) {
     float sum[HG], ref = -INFINITY;  // this row's sums; lane h: head h's running maximum
     bool start = true;               // the first tile of a piece
     uint32_t first_tile = w.tile;
+    // the queries of w's item
+    auto load_queries = [&]() {
+      const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + w.req * p.a.q_req_stride + w.qi * p.a.q_tok_stride;
+      for (uint32_t i = threadIdx.x; i < NH * 72; i += kWarps * 32) {
+        const uint32_t h = i / 72, c = i - h * 72;
+        const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
+        const bool in = w.h0 + h < p.a.heads;
+        const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
+        copy16(dst, src, in ? 16 : 0);
+      }
+    };
+    load_queries();  // (while the first rows are looked up)
     bool ok = warp_wait(bar(kBarPlace), 0, gave_up);
     if (ok) {
       fetch(raw1, 0, block1, 0, kSlots);
@@ -553,15 +595,7 @@ k_attend(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int h = 0; h < HG; ++h) sum[h] = 0.f;
         ref = -INFINITY;
-        // the item's queries (the products that read the previous item's have ended)
-        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + w.req * p.a.q_req_stride + w.qi * p.a.q_tok_stride;
-        for (uint32_t i = threadIdx.x; i < NH * 72; i += kWarps * 32) {
-          const uint32_t h = i / 72, c = i - h * 72;
-          const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
-          const bool in = w.h0 + h < p.a.heads;
-          const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
-          copy16(dst, src, in ? 16 : 0);
-        }
+        if (n) load_queries();  // (the products that read the previous item's have ended)
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
       // ---- widen the tile, block by block as there is room
@@ -755,45 +789,76 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
       w = next;
     }
+    if (kCluster) {  // (here, since the other warps have fewer registers)
+      tc_fence_before();
+      meet();
+      const uint32_t item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
+      const uint32_t token = item / p.head_tiles, h0 = (item - token * p.head_tiles) * NH;
+      const uint32_t heads = p.a.heads - h0 < NH ? p.a.heads - h0 : NH;
+      // this block's share: query heads [first, last).  The first values are on their way while
+      // each part's weight in a head is worked out.
+      const uint32_t first = rank * heads / p.cluster, last = (rank + 1) * heads / p.cluster;
+      const uint32_t total = (last - first) * 128;
+      float *weight = reinterpret_cast<float *>(sm + L::q);  // [head][part] (no product reads the queries any more)
+      float4 o[kMostCluster];
+      auto load = [&](uint32_t i) {
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k)
+          if (k < p.cluster) {
+            uint32_t at;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sk + first * 2048 + i * 16), "r"(k));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w) : "r"(at) : "memory");
+          }
+      };
+      uint32_t i = threadIdx.x;
+      if (i < total) load(i);
+      if (i < last - first) {
+        const uint32_t h = first + i;
+        float l[kMostCluster], m = -INFINITY, all = 0.f;
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k) {
+          l[k] = -INFINITY;
+          if (k < p.cluster) {
+            uint32_t at;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + L::scale + h * 4), "r"(k));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l[k]) : "r"(at) : "memory");
+          }
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k) m = fmaxf(m, l[k]);
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k) all += l[k] = ex2(l[k] - m);
+        const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k) weight[i * kMostCluster + k] = l[k] * inv;
+        if (p.a.lse) p.a.lse[(uint64_t)token * p.a.heads + h0 + h] = (m + log2f(all)) * 0.693147180559945309f;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+      while (i < total) {
+        const uint32_t h = i >> 7, c = i & 127;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (uint32_t k = 0; k < kMostCluster; ++k)
+          if (k < p.cluster) {
+            const float f = weight[h * kMostCluster + k];
+            acc.x += f * o[k].x, acc.y += f * o[k].y, acc.z += f * o[k].z, acc.w += f * o[k].w;
+          }
+        reinterpret_cast<uint2 *>((__nv_bfloat16 *)p.a.out + ((uint64_t)token * p.a.heads + h0 + first + h) * ULA_ROW_LATENT)[c] =
+            make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+        i += kWarps * 32;
+        if (i < total) load(i);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-  if (kCluster) {
-    // every block of the cluster gets here, also one that has given up
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const uint32_t item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
-    const uint32_t token = item / p.head_tiles, h0 = (item - token * p.head_tiles) * NH;
-    const uint32_t heads = p.a.heads - h0 < NH ? p.a.heads - h0 : NH;
-    // (by the compute warps: the others have fewer registers)
-    const uint32_t last = warp < kWarps ? (rank + 1) * heads * 128 / p.cluster : 0;
-    for (uint32_t i = rank * heads * 128 / p.cluster + threadIdx.x; i < last; i += kWarps * 32) {
-      const uint32_t h = i >> 7, c = i & 127;
-      Joined j;
-      for (uint32_t b = 0; b < p.cluster; b += Joined::kBatch) {
-        float l[Joined::kBatch];
-        float4 o[Joined::kBatch];
-#pragma unroll
-        for (uint32_t k = 0; k < Joined::kBatch; ++k) {
-          l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (b + k < p.cluster) {
-            uint32_t at_l, at_o;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_l) : "r"(base + L::scale + h * 4), "r"(b + k));
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_o) : "r"(sk + h * 2048 + c * 16), "r"(b + k));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l[k]) : "r"(at_l) : "memory");
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w) : "r"(at_o) : "memory");
-          }
-        }
-        j.add(l, o);
-      }
-      j.write(p.a, (uint64_t)token * p.a.heads + h0 + h, c);
-    }
-    // (a block's shared memory stays until the others have read it)
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
+  // (a block's shared memory stays until the others have read it)
+  if (kCluster) meet();
 }
 
 // Joins the partial results of the items that several blocks share: 128 threads per query
@@ -847,7 +912,31 @@ struct Plan {
   uint64_t workspace;
 };
 
-constexpr uint32_t kMostCluster = 8;  // (the portable size)
+
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint32_t smem, uint32_t cluster,
+                   cudaStream_t st, Args... args) {
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <uint32_t NH>
+cudaError_t prepare_attend(bool cluster) {
+  // (idempotent and cheap; a per-device flag would have to know about device resets)
+  auto kernel = cluster ? k_attend<NH, true> : k_attend<NH, false>;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
+}
 
 bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool own, Plan *pl) {
   const uint64_t tokens = (uint64_t)n_req * n_q;
@@ -878,31 +967,11 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   return true;
 }
 
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint32_t smem, uint32_t cluster,
-                   cudaStream_t st, Args... args) {
-  cudaLaunchAttribute at[2]{};
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <uint32_t NH>
 cudaError_t launch_attend(const AttendParams &p, cudaStream_t st) {
-  auto kernel = p.cluster > 1 ? k_attend<NH, true> : k_attend<NH, false>;
-  // (idempotent and cheap; a per-device flag would have to know about device resets)
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
+  const cudaError_t e = prepare_attend<NH>(p.cluster > 1);
   if (e != cudaSuccess) return e;
-  return launch(kernel, p.blocks, kThreads, Shared<NH>::bytes, p.cluster, st, p);
+  return launch(p.cluster > 1 ? k_attend<NH, true> : k_attend<NH, false>, p.blocks, kThreads, Shared<NH>::bytes, p.cluster, st, p);
 }
 
 }  // namespace

@@ -209,8 +209,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // Bound by its bytes.  One warp per token: lane l holds latents 16l..16l+15 (8 lanes share
 // a block's scale) and turns rope pair l; a warp has the next token's loads in flight
 // while it works on one.  kVec: 16-byte loads of the latents (bases and strides that allow
-// them).  The quotient is a product with the scale's reciprocal (two fp32 roundings; 16
-// divisions a lane were half of the instructions).
+// them).  16 divisions a lane were half of the instructions; x / scale is the product with the
+// scale's reciprocal and one correction by the remainder, which a fused multiply-add gives
+// exactly (Markstein, IBM J. Res. Dev. 34, 1990): the correctly rounded quotient, so that a
+// value near the middle of two codes goes to the nearer one.
 template <typename T, bool kHalves, bool kVec>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
   constexpr int V = Vec<T>::n, N = 16 / V;
@@ -252,10 +254,14 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     const float scale = max_nan(__fdiv_rn(amax, 448.f), 0x1p-126f), inv = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float q = v[i] * inv;
+      v[i] = fmaf(fmaf(-q, scale, v[i]), inv, q);
+    }
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     uint8_t *row = p.rows + t * p.row_stride;
     reinterpret_cast<uint4 *>(row)[l] = make_uint4(c[0], c[1], c[2], c[3]);
     if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;

@@ -214,6 +214,26 @@ def test_pack_not_finite():
     assert (rope == 0).all()
 
 
+def test_pack_quotients():
+    """Codes are those of the fp32 quotient x / scale, correctly rounded, for values at and next
+    to the middle of two codes (a quotient one unit off would cross it)."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(11)
+    mids = (E4M3[1:126] + E4M3[2:127]) / 2
+    n = 400
+    top = np.exp(3 * rng.standard_normal((n, 4, 1))).astype(np.float32)
+    scale = np.maximum(top / np.float32(448), np.float32(2.0 ** -126))
+    x = (rng.choice(mids, (n, 4, 128)) * rng.choice([-1, 1], (n, 4, 128)) * scale).astype(np.float32)
+    x = x.view(np.int32) + rng.integers(-2, 3, x.shape).astype(np.int32)
+    x = np.clip(x.view(np.float32), -top, top)
+    x[:, :, 0] = top[:, :, 0]
+    latent = torch.from_numpy(x.reshape(n, 512)).cuda()
+    got = rows.pack(latent, torch.zeros(n, 64, device="cuda"),
+                    torch.zeros(n, dtype=torch.int32, device="cuda"), rows.Rotary([0.0] * 32))
+    want = torch.from_numpy((x / scale).reshape(n, 512)).to(torch.float8_e4m3fn)
+    assert torch.equal(got[:, :512].cpu(), want.view(torch.uint8))
+
+
 def test_pack_strides():
     from serving_step_sparse_gb300 import rows
     rng = np.random.default_rng(5)
@@ -600,3 +620,39 @@ def test_refusals():
     with pytest.raises(ula.UlaError):
         rows.attend(q, store[8:8 + 3 * 656].view(3, 656), entry, SCALE)
     rows.sync()
+
+
+# ------------------------------------------------------------------------------- together
+
+def test_decode_layers_example():
+    """The operators with the cache, as a decode step uses them, against a dense computation in
+    64 bits.  Outputs are averages of latents of unit size (at most 6): rounded to bf16 once
+    for each of two parts and once for the joined result (2^-8 each), with the probabilities'
+    2^-8: off by at most 4 * 2^-8 * 6."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_layers.py")
+    spec = importlib.util.spec_from_file_location("decode_layers", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.run(steps=2, seed=1, check=True) <= 4 * 2.0 ** -8 * 6
+
+
+def test_attend_partitions_of_tp():
+    """TP mode: a rank's local and remote rows, two buffers with entry rows of their own, attended
+    to separately and joined, against one buffer with all of them."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(4, 2, 24, 300, 600, 55, pads=0.05)
+    remote = (torch.arange(600, device="cuda") % 2).bool()
+    index = torch.cumsum(remote, 0).to(torch.int32) - 1
+    other = torch.cumsum(~remote, 0).to(torch.int32) - 1
+    at = entry.clamp_min(0).long()
+    here = torch.where((entry >= 0) & ~remote[at], other[at], -1)
+    there = torch.where((entry >= 0) & remote[at], index[at], -1)
+    a = rows.attend(q, kv[~remote].contiguous(), here, SCALE)
+    b = rows.attend(q, kv[remote].contiguous(), there, SCALE)
+    o, z = rows.join([a[0], b[0]], [a[1], b[1]])
+    out, lse, slack, zslack = attend64(q, kv, entry, SCALE)
+    assert (np.abs(z.double().cpu().numpy() - lse) <= zslack + 2.0 ** -19 * (1 + np.abs(lse))).all()
+    tol = 2.0 ** -8 * 1.01 * np.abs(out) + (2.0 ** -8 + 2.0 ** -8 + np.expm1(2 * zslack[..., None])) * slack
+    assert (np.abs(o.double().cpu().numpy() - out) <= tol).all()

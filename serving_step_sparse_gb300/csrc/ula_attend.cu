@@ -13,8 +13,8 @@
 // both products from one bf16 copy in shared memory (K-major for the first, MN-major for
 // the second).  A code is exact in bf16 and its scale multiplies fp32 accumulators, so the
 // logits are as exact as fp32 sums; the probabilities times the scales enter the second
-// product in bf16 (half a unit 2^-9 relative on each, which averages out over the rows;
-// bf16 and not f16 since scales may span many orders).
+// product in bf16 (up to 2^-8 relative on each, which averages out over the rows; bf16 and not
+// f16 since scales may span many orders).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,10 +27,10 @@ __device__ int g_status;  // the first error that a kernel of this file latched
 constexpr uint32_t kTile = 128;                      // rows per tile
 constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
 constexpr uint32_t kGroups = 9;                      // 8 of latents, 1 of rope
-constexpr uint32_t kWarps = 16;                      // compute warps; then the issuing and the loading one
+constexpr uint32_t kWarps = 8;                       // compute warps; then an issuing one, two loading, an issuing one
 constexpr uint32_t kThreads = (kWarps + 4) * 32;     // (registers move between groups of 4 warps)
-// Launched with 96 registers a thread: 5 * 96 = 4 * 104 + 64.
-constexpr uint32_t kRegsCompute = 104, kRegsIssue = 64;
+// Launched with 168 registers a thread: 3 * 168 = 2 * 216 + 72.
+constexpr uint32_t kRegsCompute = 216, kRegsIssue = 72;
 constexpr uint32_t kLoaders = 2;                     // loading warps, 64 rows each
 constexpr uint32_t kSlots = kTile / (4 * kWarps / 2);  // rows per lane of the widening
 constexpr uint32_t kMostCluster = 8;                  // (the portable size)
@@ -53,12 +53,6 @@ struct AttendParams {
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ unsigned long long global_ns() {
-  unsigned long long v;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(v));
-  return v;
-}
-
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -67,37 +61,26 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+// Bounded: false after 2^20 tries. Each returns at once or after at most about a microsecond (the
+// time given to it), so a wait that is never met ends after 10 ms to 1 s, and any wait that these
+// kernels can meet is shorter than a tenth of a millisecond. The loop is written out because its
+// size matters: the compute warps pass through some 15 waits a tile, their code is longer than
+// the instruction caches nearest to them, and with a clock read and two ways out in each wait
+// the step of 96 tokens, 128 heads, 2,048 rows took 169.4 us, with this form 159.4.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, 0;\n"
+      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra over;\n"
+      " add.u32 i, i, 1;\n setp.lt.u32 p, i, 0x100000;\n @p bra again;\n setp.ne.u32 p, 0, 0;\n"
+      "over:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done;
 }
 
-// Bounded: after 1 s, or once another thread of the block has given up, it returns false.
-__device__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-  const unsigned long long t0 = global_ns();
-  for (;;) {
-    if (mbar_try(bar, parity)) return true;
-    if (*gave_up) return false;
-    if (global_ns() - t0 > 1000000000ull) {
-      *gave_up = 1;
-      atomicCAS(&g_status, 0, (int)ULA_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-  if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, gave_up);
-}
-
 // By a whole warp: the same answer in every lane, so that a warp leaves its work as one.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *gave_up) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, gave_up));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -153,6 +136,10 @@ template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float (&v
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
         "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
         "=f"(v[15]) : "r"(addr) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float (&v)[32]) {
+  tmem_ld<16>(addr, reinterpret_cast<float (&)[16]>(v[0]));
+  tmem_ld<16>(addr + 16, reinterpret_cast<float (&)[16]>(v[16]));
 }
 template <> __device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
@@ -219,11 +206,16 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t *>(&b);
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);  // (their low halves are 0)
 }
 
 // ---------------------------------------------------------------- the kernel
+
+// mbarriers.  Full + b: block b of the tile stands in shared memory (4: the rope); S + b: S_b^T in
+// TMEM; Drained: block 1's S^T has been read; P: P_0, and P_1 to P_3, stand in shared memory; PV + b:
+// O_b^T is up to date and block b's codes are free; X: exchange in a column group; Place: the rows'
+// addresses stand; Scale: their scales; End: a warp's products have ended.
+enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarPlace = 19, kBarScale = 20, kBarEnd = 21, kBars = 24 };
 
 template <uint32_t NH>
 struct Shared {
@@ -233,11 +225,9 @@ struct Shared {
   static constexpr uint32_t place = scale + kTile * 16;       // [2][128] the rows' addresses, 0: no row
   static constexpr uint32_t top = place + 2 * kTile * 8;      // [NH][4] tile maxima (then sums) by quadrant
   static constexpr uint32_t bars = top + NH * 16;
-  static constexpr uint32_t words = bars + 32 * 8;            // TMEM address, gave_up
+  static constexpr uint32_t words = bars + kBars * 8;         // TMEM address
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
-
-enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarPlace = 21, kBarScale = 22, kBarEnd = 23 };
 
 // The tiles of a block, in item order.
 struct Place {
@@ -307,10 +297,18 @@ struct Joined {
 
 // Persistent: one block per SM, block c runs an even share of all tiles, item after item
 // (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
-// joins them).  16 compute warps fetch the rows' codes into registers one tile ahead, widen
+// joins them).  8 compute warps fetch the rows' codes into registers one tile ahead, widen
 // them to bf16 in shared memory and run the softmax; two warps look the rows up and copy
-// their scales and rope channels; one warp issues the products.  Compute warp w reads TMEM
-// lanes (rows) 32 (w % 4).. and the heads of column group w / 4.
+// their scales and rope channels; two issue the products.  Compute warp w reads TMEM lanes
+// (rows) 32 (w % 4).. and the heads of column group w / 4.
+//
+// What bounds it: the one tile in shared memory (queries 72 KB, tile 144 KB at 64 heads) makes
+// widening, S^T, softmax and O^T of a tile follow each other, some 10,000 clocks a tile, of
+// which its 68 products take 3,500 (their operands' bytes from shared memory, not their
+// arithmetic), its loads 2,150 (64 KB at the 30 B a clock that an SM's loads in flight reach)
+// and the conversions 1,600.  96 tokens, 2,048 + 3 rows: 128 heads 154 us (0.36 PFLOP/s), 64
+// heads 87 us, and 17.4 us for 8 tokens of 64 heads.  16 compute warps of half the registers:
+// 166, 92 and 17.8 us.
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
@@ -325,12 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 k_attend(const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NH>;
-  constexpr int HG = NH / 4;  // heads per column group
+  constexpr int HG = NH / (kWarps / 4);  // heads per column group
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
-  volatile uint32_t *gave_up = reinterpret_cast<volatile uint32_t *>(sm + L::words + 4);
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < 5; ++i) {
       mbar_init(bar(kBarFull + i), i < 4 ? kWarps / 2 : kLoaders);
@@ -339,9 +336,9 @@ k_attend(const __grid_constant__ AttendParams p) {
     mbar_init(bar(kBarPlace), kLoaders), mbar_init(bar(kBarScale), kLoaders * 32);
     mbar_init(bar(kBarDrained), kWarps);
     mbar_init(bar(kBarP), kWarps), mbar_init(bar(kBarP + 1), kWarps);
-    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1), mbar_init(bar(kBarX + i), 4);
+    for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1);
+    for (uint32_t i = 0; i < kWarps / 4; ++i) mbar_init(bar(kBarX + i), 4);
     mbar_init(bar(kBarEnd), 1), mbar_init(bar(kBarEnd + 1), 1);
-    *gave_up = 0;
     fence_async_smem();
   }
   // (an address read before its time, after a wait that ran out, is no address)
@@ -378,6 +375,7 @@ k_attend(const __grid_constant__ AttendParams p) {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   };
 
+  bool ok = true;  // false once a wait has run out
   if (warp >= kWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kWarps || warp == kWarps + 1 + kLoaders) {
@@ -391,7 +389,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       // D fp32, A and B bf16; M = 128, N = NH; for O^T both operands are MN-major
       constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((NH >> 3) << 17) | ((kTile >> 4) << 24);
       constexpr uint32_t kIdO = kIdS | (1u << 15) | (1u << 16);
-      const uint64_t k_rows = operand(sk, 16), k_channels = operand(sk, kGroupBytes), q_rows = operand(base + L::q, 16);
+      uint64_t k_rows = operand(sk, 16), k_channels = operand(sk, kGroupBytes), q_rows = operand(base + L::q, 16);
       // S_b^T; the rope's part (4) goes to block 1's columns
       auto issue_s = [&](uint32_t b) {
         tc_fence_after();
@@ -405,23 +403,24 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
         __syncwarp();
       };
-      bool ok = true;
       if (warp == kWarps) {
         uint32_t tile = w.tile;
         bool fresh = true;
         for (uint32_t n = 0; n < count; ++n) {
           const uint32_t par = n & 1;
-          ok = ok && warp_wait(bar(kBarFull + 1), par, gave_up);
-          ok = ok && warp_wait(bar(kBarFull + 2), par, gave_up);  // (every warp's queries)
+          // (new to the compiler in every tile: it would keep 68 descriptors in registers otherwise)
+          asm volatile("" : "+l"(k_rows), "+l"(k_channels), "+l"(q_rows));
+          ok = ok && warp_wait(bar(kBarFull + 1), par);
+          ok = ok && warp_wait(bar(kBarFull + 2), par);  // (every warp's queries)
           issue_s(1);
-          ok = ok && warp_wait(bar(kBarFull), par, gave_up);
+          ok = ok && warp_wait(bar(kBarFull), par);
           issue_s(0);
-          ok = ok && warp_wait(bar(kBarP), par, gave_up);
+          ok = ok && warp_wait(bar(kBarP), par);
           tc_fence_after();
 #pragma unroll
           for (uint32_t b = 0; b < 4; ++b) {  // O_b^T
             if (b == 1) {
-              ok = ok && warp_wait(bar(kBarP + 1), par, gave_up);
+              ok = ok && warp_wait(bar(kBarP + 1), par);
               tc_fence_after();
             }
             const uint64_t da = k_channels + b * (2 * kGroupBytes >> 4);
@@ -439,21 +438,21 @@ k_attend(const __grid_constant__ AttendParams p) {
       } else {
         for (uint32_t n = 0; n < count; ++n) {
           const uint32_t par = n & 1;
-          ok = ok && warp_wait(bar(kBarFull + 1), par, gave_up);  // (every warp's queries)
-          ok = ok && warp_wait(bar(kBarFull + 2), par, gave_up);
+          asm volatile("" : "+l"(k_rows), "+l"(q_rows));
+          ok = ok && warp_wait(bar(kBarFull + 1), par);  // (every warp's queries)
+          ok = ok && warp_wait(bar(kBarFull + 2), par);
           issue_s(2);
-          ok = ok && warp_wait(bar(kBarFull + 3), par, gave_up);
+          ok = ok && warp_wait(bar(kBarFull + 3), par);
           issue_s(3);
-          ok = ok && warp_wait(bar(kBarFull + 4), par, gave_up);
-          ok = ok && warp_wait(bar(kBarDrained), par, gave_up);   // (block 1's columns have been read)
+          ok = ok && warp_wait(bar(kBarFull + 4), par);
+          ok = ok && warp_wait(bar(kBarDrained), par);   // (block 1's columns have been read)
           issue_s(4);
         }
       }
       const uint32_t end = bar(kBarEnd + (warp == kWarps ? 0 : 1));
       if (elect_one()) {  // every product has ended before the block's TMEM goes
         mma_commit(end);
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try(end, 0) && global_ns() - t0 < 1000000000ull) {}
+        mbar_wait(end, 0);
       }
       __syncwarp();
     } else if (warp <= kWarps + kLoaders) {
@@ -482,14 +481,14 @@ k_attend(const __grid_constant__ AttendParams p) {
           step<NH>(p, w);
           fetch_entries();
         }
-        if (n && !warp_wait(bar(kBarPV + 1), prev, gave_up)) break;
+        if (n && !(ok = warp_wait(bar(kBarPV + 1), prev))) break;
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j) {
           const uint64_t row = place[lane + 32 * j];
           copy16(base + L::scale + (r0 + lane + 32 * j) * 16, (const void *)(row ? row + ULA_ROW_LATENT : (uint64_t)p.a.q), row ? 16 : 0);
         }
         copy_arrive(bar(kBarScale));
-        if (n && !warp_wait(bar(kBarPV + 2), prev, gave_up)) break;
+        if (n && !(ok = warp_wait(bar(kBarPV + 2), prev))) break;
 #pragma unroll
         for (uint32_t i = 0; i < 16; ++i) {
           const uint32_t r = r0 + 4 * i + (lane >> 3), ch = lane & 7;
@@ -504,7 +503,8 @@ k_attend(const __grid_constant__ AttendParams p) {
         // The next addresses only once every compute warp has this tile's: a second arrival of
         // one loading warp may not stand for the first of the other.
         if (n + 1 < count) {
-          if (!warp_wait(bar(kBarFull + 1), par, gave_up) || !warp_wait(bar(kBarFull + 2), par, gave_up)) break;
+          ok = warp_wait(bar(kBarFull + 1), par);
+          if (!(ok = ok && warp_wait(bar(kBarFull + 2), par))) break;
           place_rows(prev);
         }
       }
@@ -517,7 +517,7 @@ k_attend(const __grid_constant__ AttendParams p) {
     const uint32_t quad = warp & 3, grp = warp >> 2;
     const uint32_t lanes = tmem + (quad << 21);  // TMEM lane 32 * quad
     const uint32_t mine = 32 * quad + lane;      // this thread's row in the softmax
-    // widening: the first 8 warps do blocks 1 and 0, the others 2 and 3; a lane rows r0,
+    // widening: the first half of the warps does blocks 1 and 0, the other 2 and 3; a lane rows r0,
     // r0 + 4, ..., 16 channels ch of a block.  16-byte accesses are served by quarters of a
     // warp: a quarter loads 128 bytes of one row, and stores to 8 different chunks of its
     // swizzled row, since lanes of the second half store their second chunk first.
@@ -528,9 +528,9 @@ k_attend(const __grid_constant__ AttendParams p) {
     auto exchange = [&]() -> bool {  // the four warps of a column group
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarX + grp));
-      const bool ok = warp_wait(bar(kBarX + grp), xph, gave_up);
+      const bool met = warp_wait(bar(kBarX + grp), xph);
       xph ^= 1;
-      return ok;
+      return met;
     };
     auto hand_over = [&](uint32_t b) {
       fence_async_smem();
@@ -539,12 +539,11 @@ k_attend(const __grid_constant__ AttendParams p) {
       if (lane == 0) mbar_arrive(bar(b));
     };
     const uint32_t block1 = second ? 2 : 1, block2 = second ? 3 : 0;
-    // codes of tile n's rows j0..j1-1, of one block; fetched in pieces between other work, since
-    // a piece's loads hold up what the load/store unit gets behind them
-    auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block, uint32_t j0, uint32_t j1) {
+    // codes of tile n's rows, of one block
+    auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block) {
       const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile;
 #pragma unroll
-      for (uint32_t j = j0; j < j1; ++j) {
+      for (uint32_t j = 0; j < kSlots; ++j) {
         const uint64_t row = place[r0 + 4 * j];
         raw[j] = make_uint4(0, 0, 0, 0);
         if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + block * 128 + ch * 16));
@@ -583,10 +582,10 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
     };
     load_queries();  // (while the first rows are looked up)
-    bool ok = warp_wait(bar(kBarPlace), 0, gave_up);
+    ok = warp_wait(bar(kBarPlace), 0);
     if (ok) {
-      fetch(raw1, 0, block1, 0, kSlots);
-      fetch(raw2, 0, block2, 0, kSlots);
+      fetch(raw1, 0, block1);
+      fetch(raw2, 0, block2);
     }
     for (uint32_t n = 0; n < count && ok; ++n) {
       const uint32_t par = n & 1;
@@ -598,13 +597,18 @@ k_attend(const __grid_constant__ AttendParams p) {
         if (n) load_queries();  // (the products that read the previous item's have ended)
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
-      // ---- widen the tile, block by block as there is room
-      if (n && !(ok = warp_wait(bar(kBarPV + block1), par ^ 1, gave_up))) break;
-      widen(raw1, block1);
-      if (n && !(ok = warp_wait(bar(kBarPV + 3), par ^ 1, gave_up))) break;
-      widen(raw2, block2);
+      // ---- widen the tile, block by block as there is room (in a loop, since two copies of this
+      // code fall out of the instruction caches: 158.5 us instead of 154.1)
+#pragma unroll 1
+      for (uint32_t half = 0; half < 2; ++half) {
+        if (n && !(ok = warp_wait(bar(kBarPV + (half ? 3 : block1)), par ^ 1))) break;
+        widen(raw1, half ? block2 : block1);
+#pragma unroll
+        for (uint32_t j = 0; j < kSlots; ++j) raw1[j] = raw2[j];
+      }
+      if (!ok) break;
       // this row's scales; a row without an entry (its codes are zeros) gets logits of -inf
-      if (!(ok = warp_wait(bar(kBarScale), par, gave_up))) break;
+      if (!(ok = warp_wait(bar(kBarScale), par))) break;
       const float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
       const float off = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] ? 0.f : -INFINITY;
       const bool more = n + 1 < count;
@@ -614,7 +618,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       float z[HG];
       {
         float v[HG];
-        if (!(ok = warp_wait(bar(kBarS + 1), par, gave_up))) break;
+        if (!(ok = warp_wait(bar(kBarS + 1), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, v);
         tc_wait_ld();
@@ -625,11 +629,15 @@ k_attend(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
-      if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1, gave_up))) break;
+      if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1))) break;
+      if (more) {
+        fetch(raw1, n + 1, block1);
+        fetch(raw2, n + 1, block2);
+      }
       {
         float v[HG], x[HG];
-        ok = warp_wait(bar(kBarS + 2), par, gave_up);
-        if (!(ok = ok && warp_wait(bar(kBarS), par, gave_up))) break;
+        ok = warp_wait(bar(kBarS + 2), par);
+        if (!(ok = ok && warp_wait(bar(kBarS), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + 2 * NH + grp * HG, v);
         tmem_ld<HG>(lanes + kColS + grp * HG, x);
@@ -640,9 +648,8 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
-        if (more) fetch(raw1, n + 1, block1, 0, kSlots / 2);
-        ok = warp_wait(bar(kBarS + 3), par, gave_up);
-        if (!(ok = ok && warp_wait(bar(kBarS + 4), par, gave_up))) break;
+        ok = warp_wait(bar(kBarS + 3), par);
+        if (!(ok = ok && warp_wait(bar(kBarS + 4), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + 3 * NH + grp * HG, v);
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, x);
@@ -654,8 +661,6 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
       }
-
-      if (more) fetch(raw1, n + 1, block1, kSlots / 2, kSlots);
 
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
       // above it, so that O^T is seldom rescaled; p stays below 2^8.  Lane h keeps head h's.
@@ -714,21 +719,15 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
         uint8_t *at = sm + L::k + group * kGroupBytes + mine * 128;
         const uint32_t x = mine & 7;
-        if constexpr (HG == 16) {
-          *reinterpret_cast<uint4 *>(at + (((2 * grp) ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-          *reinterpret_cast<uint4 *>(at + (((2 * grp + 1) ^ x) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
-        } else if constexpr (HG == 8) {
-          *reinterpret_cast<uint4 *>(at + ((grp ^ x) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
-          *reinterpret_cast<uint2 *>(at + (((grp >> 1) ^ x) << 4) + (grp & 1) * 8) = make_uint2(u[0], u[1]);
-        }
+#pragma unroll
+        for (uint32_t c = 0; c < HG / 8; ++c)
+          *reinterpret_cast<uint4 *>(at + (((HG / 8 * grp + c) ^ x) << 4)) = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
       };
       put(scale.x, 8);
       hand_over(kBarP);
-      if (more) fetch(raw2, n + 1, block2, 0, kSlots);
       Place next = w;
       step<NH>(p, next);
-      if (!(ok = warp_wait(bar(kBarPV), par, gave_up))) break;
+      if (!(ok = warp_wait(bar(kBarPV), par))) break;
       put(scale.y, 0);
       put(scale.z, 8);
       put(scale.w, 1);
@@ -762,10 +761,10 @@ k_attend(const __grid_constant__ AttendParams p) {
         __nv_bfloat16 *out = (__nv_bfloat16 *)p.a.out + ((uint64_t)w.token * p.a.heads + h0) * ULA_ROW_LATENT + mine;
         float *part = p.part_out + ((uint64_t)slot * NH + grp * HG) * ULA_ROW_LATENT + mine;
         // (a cluster's results lie across the whole tile's room: no product may read it any more)
-        if (kCluster && !(ok = warp_wait(bar(kBarPV + 3), par, gave_up))) break;
+        if (kCluster && !(ok = warp_wait(bar(kBarPV + 3), par))) break;
 #pragma unroll 1
         for (uint32_t b = 0; b < 4; ++b) {
-          if (!(ok = warp_wait(bar(kBarPV + b), par, gave_up))) break;
+          if (!(ok = warp_wait(bar(kBarPV + b), par))) break;
           tc_fence_after();
           float o[HG];
           tmem_ld<HG>(lanes + b * NH + grp * HG, o);
@@ -852,6 +851,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
     }
   }
+  if (!ok && lane == 0) atomicCAS(&g_status, 0, (int)ULA_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -912,7 +912,6 @@ struct Plan {
   uint64_t workspace;
 };
 
-
 template <typename... Args>
 cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint32_t smem, uint32_t cluster,
                    cudaStream_t st, Args... args) {
@@ -945,6 +944,10 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
     return false;
   pl->keys = k + (own ? n_q : 0);
   pl->tiles = pl->keys ? (pl->keys + kTile - 1) / kTile : 1;
+  // Heads per item: the fewest that hold them all, up to 64 (TMEM's columns).  The rows are widened
+  // once an item, so heads are not split further: 96 tokens x 2,048 rows, 64 heads, 89 us with 64
+  // and 115 with 32.  Rounding 32 heads up to 64 costs 10.7 -> 13.1 us (one token, 256 rows), 16 up
+  // to 32 73 -> 78 us (128 tokens, 2,048 rows).
   pl->nh = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   pl->head_tiles = (heads + pl->nh - 1) / pl->nh;
   const uint64_t items = tokens * pl->head_tiles;
@@ -952,8 +955,17 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->total = items * pl->tiles;
   const int sms = sm_count();
   if (sms < 1 || pl->total > (1ull << 48)) return false;
+  // An item's tiles on a cluster, when there is one tile per block.  A cluster's join is shared
+  // by its blocks alone, where the second kernel's is by all SMs: it takes blocks enough that the
+  // trip of all partial results through L2 is what counts, and fewer blocks for its wider results
+  // (us with clusters, without; heads, tiles, query tokens):
+  //   32 heads  7 x 5: 10.3, 10.2    7 x 15: 10.3, 12.3    2 x 19: 10.2, 10.3    2 x 57: 10.3, 12.3
+  //   64 heads  4 x 1: 14.3, 12.3    4 x 28: 14.4, 16.4    8 x 14: 16.4, 14.4    2 x 76: 16.2, 20.8
+  // Clusters of more than 2 cannot use every SM (a cluster lies within one group of SMs), and those
+  // that find no place run behind the others: 32 heads 4 x 28: 10.3, 12.3, but 4 x 38: 20.5, 12.3.
   pl->cluster = 1;
-  if (pl->tiles > 1 && pl->tiles <= kMostCluster && pl->total <= (unsigned)sms) {
+  if (pl->tiles > 1 && pl->tiles <= (pl->nh == 64 ? kMostCluster / 2 : kMostCluster) &&
+      pl->total >= (unsigned)sms * 2 / 5 && pl->total <= (unsigned)(pl->tiles == 2 ? sms : sms * 3 / 4)) {
     pl->cluster = pl->tiles;
     pl->blocks = (uint32_t)pl->total;
     pl->parts = false;

@@ -448,6 +448,32 @@ def test_attend_strides():
     assert got[0] is out and got[1] is lse and torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("R,Q,H,K,own", [
+    (12, 1, 16, 1024, False), (5, 2, 20, 777, True), (16, 1, 32, 600, False), (38, 2, 64, 129, True),
+    (20, 1, 40, 512, False), (37, 1, 64, 300, False), (9, 4, 130, 200, False), (38, 1, 1, 380, True)])
+def test_attend_few_tiles(R, Q, H, K, own):
+    """Numbers of tiles about as large as the GPU: items of two to eight tiles in as many blocks.
+    Parts without rows, a query token without rows, one with a single row in its last tile."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(R, Q, H, K, 500, R + K, pads=0.1, own=own)
+    entry[0, 0, :] = -1
+    entry[1, 0, :128] = -1
+    entry[2, 0, 128:] = -1
+    entry[3, -1, :K - 1] = -1
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(got, attend64(q, kv, entry, SCALE, own_rows))
+    bad = kv.clone()
+    bad[499, 512:528] = torch.tensor([math.nan] * 4).view(torch.uint8).cuda()
+    entry = torch.where(entry == 499, 498, entry)
+    clean = rows.attend(q, bad, entry, SCALE, own_rows=own_rows)
+    entry[4, 0, K - 1] = 499
+    out, lse = rows.attend(q, bad, entry, SCALE, own_rows=own_rows)
+    assert torch.isnan(out[4, 0]).all() and torch.isnan(lse[4, 0]).all()
+    out[4, 0], lse[4, 0] = clean[0][4, 0], clean[1][4, 0]
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    rows.sync()
+
+
 def test_attend_far_rows():
     """A gathered buffer past 2^32 bytes."""
     from serving_step_sparse_gb300 import rows

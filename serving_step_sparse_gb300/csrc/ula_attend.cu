@@ -270,18 +270,18 @@ __device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &a
 // The join of partial results of one query head: 4 channels, a running maximum over batches
 // of parts (whose loads are all in flight together).
 struct Joined {
-  static constexpr uint32_t kBatch = 8;
   float m = -INFINITY, total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(const float (&l)[kBatch], const float4 (&o)[kBatch]) {
+  template <uint32_t N>
+  __device__ __forceinline__ void add(const float (&l)[N], const float4 (&o)[N]) {
     float top = m;
 #pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) top = fmaxf(top, l[k]);
+    for (uint32_t k = 0; k < N; ++k) top = fmaxf(top, l[k]);
     const float ref = top == -INFINITY ? 0.f : top, old = ex2(m - ref);
     m = top;
     total *= old, acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
 #pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) {
+    for (uint32_t k = 0; k < N; ++k) {
       const float f = ex2(l[k] - ref);
       total += f;
       acc.x += f * o[k].x, acc.y += f * o[k].y, acc.z += f * o[k].z, acc.w += f * o[k].w;
@@ -306,9 +306,9 @@ struct Joined {
 // widening, S^T, softmax and O^T of a tile follow each other, some 10,000 clocks a tile, of
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its loads 2,150 (64 KB at the 30 B a clock that an SM's loads in flight reach)
-// and the conversions 1,600.  96 tokens, 2,048 + 3 rows: 128 heads 154 us (0.36 PFLOP/s), 64
-// heads 87 us, and 17.4 us for 8 tokens of 64 heads.  16 compute warps of half the registers:
-// 166, 92 and 17.8 us.
+// and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads 144 us (0.38 PFLOP/s),
+// 64 heads 84 us, and 17.6 us for 8 tokens of 64 heads.  16 compute warps of half the registers:
+// 12, 5 and 0.4 us more.
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
@@ -862,37 +862,51 @@ k_attend(const __grid_constant__ AttendParams p) {
 }
 
 // Joins the partial results of the items that several blocks share: 128 threads per query
-// token and head, 4 channels each.
-__global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh) {
-  const uint32_t i = blockIdx.x * 2 + (threadIdx.x >> 7), c = threadIdx.x & 127;
+// token and head, 4 channels each; a block's `heads` heads (blockIdx.y) are of one item.
+// Bound by what an SM can have in flight of the parts' bytes (in L2): 16.8 MB, 16 parts of
+// 512 heads, some 4 us.
+__global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh, uint32_t heads) {
+  const uint32_t item = blockIdx.x, c = threadIdx.x & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint32_t token = i / p.a.heads, head = i - token * p.a.heads;
-  if (token >= p.a.n_req * p.a.n_q) return;
-  const unsigned long long s = ((unsigned long long)token * p.head_tiles + head / nh) * p.tiles;
+  const uint32_t token = item / p.head_tiles, h0 = (item - token * p.head_tiles) * nh;
+  const unsigned long long s = (unsigned long long)item * p.tiles;
   auto owner = [&](unsigned long long tile) -> uint32_t {  // (64-bit divisions only where they have to be)
     const unsigned long long x = (tile + 1) * p.blocks - 1;
     return (x | p.total) >> 32 ? (uint32_t)(x / p.total) : (uint32_t)x / (uint32_t)p.total;
   };
   const uint32_t b0 = owner(s), b1 = owner(s + p.tiles - 1);
   if (b0 == b1) return;  // written whole
-  const uint32_t h = head % nh;
-  Joined j;
-  for (uint32_t b = b0; b <= b1; b += Joined::kBatch) {
-    float l[Joined::kBatch];
-    float4 o[Joined::kBatch];
+  uint32_t last = (blockIdx.y + 1) * heads;
+  if (last > p.a.heads - h0) last = p.a.heads - h0;
+  for (uint32_t h = blockIdx.y * heads + (threadIdx.x >> 7); h < last; h += 2) {
+    Joined j;
+    uint32_t b = b0;
+    auto take = [&](auto &l, auto &o) {
 #pragma unroll
-    for (uint32_t k = 0; k < Joined::kBatch; ++k) {
-      l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (b + k <= b1) {
-        const uint64_t row = ((uint64_t)2 * (b + k) + (b + k == b0 ? 1 : 0)) * nh + h;
-        l[k] = __ldcs(p.part_lse + row);
-        o[k] = __ldcs(reinterpret_cast<const float4 *>(p.part_out + row * ULA_ROW_LATENT) + c);
+      for (uint32_t k = 0; k < sizeof l / sizeof *l; ++k) {
+        l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b + k <= b1) {
+          const uint64_t row = ((uint64_t)2 * (b + k) + (b + k == b0 ? 1 : 0)) * nh + h;
+          l[k] = __ldcs(p.part_lse + row);
+          o[k] = __ldcs(reinterpret_cast<const float4 *>(p.part_out + row * ULA_ROW_LATENT) + c);
+        }
+      }
+      j.add(l, o);
+    };
+    if (b1 - b0 == 1) {  // (an item shorter than a block's share: nothing worked out for absent parts)
+      float l[2];
+      float4 o[2];
+      take(l, o);
+    } else {
+      for (; b <= b1; b += 8) {
+        float l[8];
+        float4 o[8];
+        take(l, o);
       }
     }
-    j.add(l, o);
+    j.write(p.a, (uint64_t)token * p.a.heads + h0 + h, c);
   }
-  j.write(p.a, i, c);
 }
 
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -906,14 +920,14 @@ int sm_count() {
 }
 
 struct Plan {
-  uint32_t nh, head_tiles, tiles, keys, blocks, cluster;
+  uint32_t sms, nh, head_tiles, tiles, keys, blocks, cluster;
   unsigned long long total;
   bool parts;  // some item's tiles lie in several blocks that are no cluster
   uint64_t workspace;
 };
 
 template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint32_t smem, uint32_t cluster,
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, uint32_t block, uint32_t smem, uint32_t cluster,
                    cudaStream_t st, Args... args) {
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -921,7 +935,7 @@ cudaError_t launch(void (*kernel)(Args...), uint32_t grid, uint32_t block, uint3
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = cluster, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -955,6 +969,7 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->total = items * pl->tiles;
   const int sms = sm_count();
   if (sms < 1 || pl->total > (1ull << 48)) return false;
+  pl->sms = (uint32_t)sms;
   // An item's tiles on a cluster, when there is one tile per block.  A cluster's join is shared
   // by its blocks alone, where the second kernel's is by all SMs: it takes blocks enough that the
   // trip of all partial results through L2 is what counts, and fewer blocks for its wider results
@@ -1018,8 +1033,14 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = pl.nh == 16 ? launch_attend<16>(p, st) : pl.nh == 32 ? launch_attend<32>(p, st) : launch_attend<64>(p, st);
   if (e != cudaSuccess) return ULA_ERR_CUDA;
-  if (pl.parts)
-    e = launch(k_join_parts, (uint32_t)(((uint64_t)a.n_req * a.n_q * a.heads + 1) / 2), 256, 0, 1, st, p, pl.nh);
+  if (pl.parts) {
+    // Heads per block of the join: 4 share the work on a block's place once every SM has several
+    // blocks (96 tokens x 2,048 rows, 128 heads, both kernels 144.5 us; 146.3 with 2), and 2 keep
+    // the loads of few items on more SMs (8 tokens, 64 heads: 17.6 us; 21.2 with 4).
+    const uint64_t items = pl.total / pl.tiles;
+    const uint32_t join_heads = items * pl.nh / 4 >= 4ull * pl.sms ? 4 : 2;
+    e = launch(k_join_parts, dim3((uint32_t)items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
+  }
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 

@@ -113,6 +113,11 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Brings bytes (a multiple of 16, as the address is) into L2.
+__device__ __forceinline__ void prefetch(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -305,8 +310,8 @@ struct Joined {
 // What bounds it: the one tile in shared memory (queries 72 KB, tile 144 KB at 64 heads) makes
 // widening, S^T, softmax and O^T of a tile follow each other, some 10,000 clocks a tile, of
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
-// arithmetic), its loads 2,150 (64 KB at the 30 B a clock that an SM's loads in flight reach)
-// and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads 144 us (0.38 PFLOP/s),
+// arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
+// direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads 144 us (0.38 PFLOP/s),
 // 64 heads 84 us, and 17.6 us for 8 tokens of 64 heads.  16 compute warps of half the registers:
 // 12, 5 and 0.4 us more.
 //
@@ -506,6 +511,12 @@ k_attend(const __grid_constant__ AttendParams p) {
           ok = warp_wait(bar(kBarFull + 1), par);
           if (!(ok = ok && warp_wait(bar(kBarFull + 2), par))) break;
           place_rows(prev);
+          // into L2 ahead of the loads, a tile's time before they are issued (the first tile's
+          // loads follow at once, and a row's prefetch takes longer to issue than its load)
+          const uint64_t *ahead = reinterpret_cast<const uint64_t *>(sm + L::place) + prev * kTile + r0;
+#pragma unroll
+          for (uint32_t j = 0; j < 2; ++j)
+            if (ahead[lane + 32 * j]) prefetch((const void *)ahead[lane + 32 * j], ULA_ROW_BYTES);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -863,8 +874,9 @@ k_attend(const __grid_constant__ AttendParams p) {
 
 // Joins the partial results of the items that several blocks share: 128 threads per query
 // token and head, 4 channels each; a block's `heads` heads (blockIdx.y) are of one item.
-// Bound by what an SM can have in flight of the parts' bytes (in L2): 16.8 MB, 16 parts of
-// 512 heads, some 4 us.
+// Bound by the parts' bytes, which each SM reads from L2 at some 30 B a clock: 16.8 MB, 16 parts
+// of 512 heads, 2 us and the loads' latency.
+template <uint32_t kBatch>
 __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh, uint32_t heads) {
   const uint32_t item = blockIdx.x, c = threadIdx.x & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
@@ -881,10 +893,11 @@ __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ Atte
   if (last > p.a.heads - h0) last = p.a.heads - h0;
   for (uint32_t h = blockIdx.y * heads + (threadIdx.x >> 7); h < last; h += 2) {
     Joined j;
-    uint32_t b = b0;
-    auto take = [&](auto &l, auto &o) {
+    for (uint32_t b = b0; b <= b1; b += kBatch) {
+      float l[kBatch];
+      float4 o[kBatch];
 #pragma unroll
-      for (uint32_t k = 0; k < sizeof l / sizeof *l; ++k) {
+      for (uint32_t k = 0; k < kBatch; ++k) {
         l[k] = -INFINITY, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (b + k <= b1) {
           const uint64_t row = ((uint64_t)2 * (b + k) + (b + k == b0 ? 1 : 0)) * nh + h;
@@ -893,17 +906,6 @@ __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ Atte
         }
       }
       j.add(l, o);
-    };
-    if (b1 - b0 == 1) {  // (an item shorter than a block's share: nothing worked out for absent parts)
-      float l[2];
-      float4 o[2];
-      take(l, o);
-    } else {
-      for (; b <= b1; b += 8) {
-        float l[8];
-        float4 o[8];
-        take(l, o);
-      }
     }
     j.write(p.a, (uint64_t)token * p.a.heads + h0 + h, c);
   }
@@ -1037,9 +1039,15 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
     // Heads per block of the join: 4 share the work on a block's place once every SM has several
     // blocks (96 tokens x 2,048 rows, 128 heads, both kernels 144.5 us; 146.3 with 2), and 2 keep
     // the loads of few items on more SMs (8 tokens, 64 heads: 17.6 us; 21.2 with 4).
+    // Parts in flight per thread: 2 where an item has no more; else 16 while there is a place for
+    // every block at that many registers (8 tokens, 64 heads: 15.6 us; 17.6 with 8), then 8 (20
+    // tokens: 24.7 us; 26.7 with 16. 96 tokens of 128 heads, two parts: 141.1 us with 2, 142.8
+    // with 8, 148.3 with 16).
     const uint64_t items = pl.total / pl.tiles;
     const uint32_t join_heads = items * pl.nh / 4 >= 4ull * pl.sms ? 4 : 2;
-    e = launch(k_join_parts, dim3((uint32_t)items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
+    const bool two = pl.tiles <= 2 || pl.total / pl.blocks >= pl.tiles, few = items * pl.nh / join_heads <= 2ull * pl.sms;
+    e = launch(two ? k_join_parts<2> : few ? k_join_parts<16> : k_join_parts<8>,
+               dim3((uint32_t)items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
   }
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }

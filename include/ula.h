@@ -411,7 +411,9 @@ int ula_dedup_noalloc(const uint32_t *d_sel, uint32_t n, uint32_t *d_uniq,
  * These calls need no context.  Every one is asynchronous on `stream`, launches on the
  * current device, and returns ULA_ERR_INVALID_ARG with nothing launched for bad
  * arguments (NULL buffers with work to do, misaligned buffers or strides, sizes out of
- * range).  They allocate nothing and keep nothing between calls.
+ * range).  They allocate nothing and keep nothing between calls.  A kernel's launch and
+ * setup overlap the end of the one before it on the stream; none touches the buffers
+ * before that one has ended.
  */
 #define ULA_ROW_BYTES 656u
 #define ULA_ROW_LATENT 512u

@@ -311,9 +311,9 @@ struct Joined {
 // widening, S^T, softmax and O^T of a tile follow each other, some 10,000 clocks a tile, of
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
-// direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads 144 us (0.38 PFLOP/s),
-// 64 heads 84 us, and 17.6 us for 8 tokens of 64 heads.  16 compute warps of half the registers:
-// 12, 5 and 0.4 us more.
+// direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads
+// 141 us (0.39 PFLOP/s), 64 heads 82 us, and 15.7 us for 8 tokens of 64 heads.  16 compute warps
+// of half the registers took 12, 5 and 0.4 us more.
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
@@ -511,8 +511,8 @@ k_attend(const __grid_constant__ AttendParams p) {
           ok = warp_wait(bar(kBarFull + 1), par);
           if (!(ok = ok && warp_wait(bar(kBarFull + 2), par))) break;
           place_rows(prev);
-          // into L2 ahead of the loads, a tile's time before they are issued (the first tile's
-          // loads follow at once, and a row's prefetch takes longer to issue than its load)
+          // into L2 ahead of the loads: 128 heads 142.7 us instead of 145.2.  (Not for a block's first
+          // tile, whose loads follow at once: one request 10.8 us instead of 9.6.)
           const uint64_t *ahead = reinterpret_cast<const uint64_t *>(sm + L::place) + prev * kTile + r0;
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j)

@@ -308,12 +308,12 @@ struct Joined {
 // (rows) 32 (w % 4).. and the heads of column group w / 4.
 //
 // What bounds it: the one tile in shared memory (queries 72 KB, tile 144 KB at 64 heads) makes
-// widening, S^T, softmax and O^T of a tile follow each other, some 10,000 clocks a tile, of
+// widening, S^T, softmax and O^T of a tile follow each other, some 9,000 clocks a tile, of
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
 // direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads
-// 141 us (0.39 PFLOP/s), 64 heads 82 us, and 15.7 us for 8 tokens of 64 heads.  16 compute warps
-// of half the registers took 12, 5 and 0.4 us more.
+// 125 us (0.44 PFLOP/s), 64 heads 76 us, and 15.9 us for 8 tokens of 64 heads.  (16 compute
+// warps of half the registers took 12, 5 and 0.4 us more than 8, before the loads were spread.)
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
@@ -511,7 +511,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           ok = warp_wait(bar(kBarFull + 1), par);
           if (!(ok = ok && warp_wait(bar(kBarFull + 2), par))) break;
           place_rows(prev);
-          // into L2 ahead of the loads: 128 heads 142.7 us instead of 145.2.  (Not for a block's first
+          // into L2 ahead of the loads: 128 heads 125.0 us instead of 127.5.  (Not for a block's first
           // tile, whose loads follow at once: one request 10.8 us instead of 9.6.)
           const uint64_t *ahead = reinterpret_cast<const uint64_t *>(sm + L::place) + prev * kTile + r0;
 #pragma unroll
@@ -550,11 +550,14 @@ k_attend(const __grid_constant__ AttendParams p) {
       if (lane == 0) mbar_arrive(bar(b));
     };
     const uint32_t block1 = second ? 2 : 1, block2 = second ? 3 : 0;
-    // codes of tile n's rows, of one block
-    auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block) {
+    // Half of this thread's codes of one block, of tile n's rows.  The next tile's come in four such
+    // pieces of 16 KB, apart from each other: more than some 28 KB of loads in flight stop the
+    // load/store unit for the shared memory's accesses as well (128 heads, 2,048 rows: 125 us; 135
+    // in pieces of 24, 24 and 16 KB, 141 in one of 64).
+    auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block, uint32_t half) {
       const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile;
 #pragma unroll
-      for (uint32_t j = 0; j < kSlots; ++j) {
+      for (uint32_t j = half * (kSlots / 2); j < (half + 1) * (kSlots / 2); ++j) {
         const uint64_t row = place[r0 + 4 * j];
         raw[j] = make_uint4(0, 0, 0, 0);
         if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + block * 128 + ch * 16));
@@ -595,8 +598,8 @@ k_attend(const __grid_constant__ AttendParams p) {
     load_queries();  // (while the first rows are looked up)
     ok = warp_wait(bar(kBarPlace), 0);
     if (ok) {
-      fetch(raw1, 0, block1);
-      fetch(raw2, 0, block2);
+      fetch(raw1, 0, block1, 0), fetch(raw1, 0, block1, 1);
+      fetch(raw2, 0, block2, 0), fetch(raw2, 0, block2, 1);
     }
     for (uint32_t n = 0; n < count && ok; ++n) {
       const uint32_t par = n & 1;
@@ -641,10 +644,7 @@ k_attend(const __grid_constant__ AttendParams p) {
         for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
       if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1))) break;
-      if (more) {
-        fetch(raw1, n + 1, block1);
-        fetch(raw2, n + 1, block2);
-      }
+      if (more) fetch(raw1, n + 1, block1, 0);
       {
         float v[HG], x[HG];
         ok = warp_wait(bar(kBarS + 2), par);
@@ -673,6 +673,7 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
       }
 
+      if (more) fetch(raw1, n + 1, block1, 1);
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
       // above it, so that O^T is seldom rescaled; p stays below 2^8.  Lane h keeps head h's.
       {
@@ -738,12 +739,14 @@ k_attend(const __grid_constant__ AttendParams p) {
       hand_over(kBarP);
       Place next = w;
       step<NH>(p, next);
+      if (more) fetch(raw2, n + 1, block2, 0);
       if (!(ok = warp_wait(bar(kBarPV), par))) break;
       put(scale.y, 0);
       put(scale.z, 8);
       put(scale.w, 1);
       hand_over(kBarP + 1);
       start = false;
+      if (more) fetch(raw2, n + 1, block2, 1);
 
       // ---- the end of a piece: normalise and write (a warp's 32 lanes: 32 channels of a head)
       const bool item_ends = w.tile + 1 == p.tiles;

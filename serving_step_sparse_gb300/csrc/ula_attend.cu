@@ -38,8 +38,11 @@ constexpr uint32_t kColS = 256;                      // TMEM: O^T in columns 0..
 
 struct AttendParams {
   ula_attend_args a;
-  unsigned long long total;  // tiles of all items (an item: a query token and a tile of heads)
-  uint32_t blocks;           // block c takes tiles [c * total / blocks, (c + 1) * total / blocks)
+  // An item is a query token and a tile of heads.  Block c takes items c, c + blocks, ... whole, as
+  // many rounds as there are for all blocks; of the remaining items' tiles the first `sharers`
+  // blocks (all, or as many as there are tiles) take [c * rest / sharers, (c + 1) * rest / sharers).
+  unsigned long long rest;   // tiles of the remaining items
+  uint32_t blocks, rounds, sharers;
   uint32_t tiles;            // tiles per item
   uint32_t head_tiles;
   uint32_t keys;             // entries per query token, own rows included
@@ -230,7 +233,7 @@ struct Shared {
   static constexpr uint32_t place = scale + kTile * 16;       // [2][128] the rows' addresses, 0: no row
   static constexpr uint32_t top = place + 2 * kTile * 8;      // [NH][4] tile maxima (then sums) by quadrant
   static constexpr uint32_t bars = top + NH * 16;
-  static constexpr uint32_t words = bars + kBars * 8;         // TMEM address
+  static constexpr uint32_t words = bars + kBars * 8;         // TMEM address; first remaining item, its tile; tiles in all
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
 
@@ -249,10 +252,15 @@ __device__ __forceinline__ void decode(const AttendParams &p, Place &w) {
 }
 
 template <uint32_t NH>
-__device__ __forceinline__ void step(const AttendParams &p, Place &w) {
+__device__ __forceinline__ void step(const AttendParams &p, Place &w, const volatile uint32_t *words) {
   if (++w.tile == p.tiles) {
     w.tile = 0;
-    ++w.item;
+    const uint32_t whole = p.rounds * p.blocks;  // items
+    if (w.item >= whole) {
+      ++w.item;
+    } else if ((w.item += p.blocks) >= whole) {
+      w.item = words[1], w.tile = words[2];
+    }
     decode<NH>(p, w);
   }
 }
@@ -300,9 +308,9 @@ struct Joined {
   }
 };
 
-// Persistent: one block per SM, block c runs an even share of all tiles, item after item
-// (an item whose tiles end up in several blocks leaves one partial result in each; k_join_parts
-// joins them).  8 compute warps fetch the rows' codes into registers one tile ahead, widen
+// Persistent: one block per SM, which runs whole items first, then an even share of the rest's
+// tiles (an item whose tiles end up in several blocks leaves one partial result in each;
+// k_join_parts joins them).  8 compute warps fetch the rows' codes into registers one tile ahead, widen
 // them to bf16 in shared memory and run the softmax; two warps look the rows up and copy
 // their scales and rope channels; two issue the products.  Compute warp w reads TMEM lanes
 // (rows) 32 (w % 4).. and the heads of column group w / 4.
@@ -312,7 +320,7 @@ struct Joined {
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
 // direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads
-// 125 us (0.44 PFLOP/s), 64 heads 76 us, and 15.9 us for 8 tokens of 64 heads.  (16 compute
+// 120 us (0.46 PFLOP/s), 64 heads 73 us, and 15.5 us for 8 tokens of 64 heads.  (16 compute
 // warps of half the registers took 12, 5 and 0.4 us more than 8, before the loads were spread.)
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
@@ -352,27 +360,34 @@ k_attend(const __grid_constant__ AttendParams p) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::words) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(sm + L::words);
+  if (threadIdx.x == 32) {  // where its share of the remaining items (a cluster's: of its item) starts, and its tiles in all
+    uint32_t item, tile, count;
+    if (kCluster) {
+      item = blockIdx.x / p.cluster;
+      const uint32_t rank = blockIdx.x - item * p.cluster;
+      tile = rank * p.tiles / p.cluster;
+      count = (rank + 1) * p.tiles / p.cluster - tile;
+    } else {
+      const unsigned long long first = p.rest * blockIdx.x / p.sharers;
+      item = (uint32_t)(first / p.tiles), tile = (uint32_t)(first - (unsigned long long)item * p.tiles);
+      item += p.rounds * p.blocks;
+      count = p.rounds * p.tiles;
+      if (blockIdx.x < p.sharers) count += (uint32_t)(p.rest * (blockIdx.x + 1) / p.sharers - first);
+    }
+    words[1] = item, words[2] = tile, words[3] = count;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(sm + L::words), 0);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
   // (launched while the kernel before it ends: nothing above touches memory that it may write)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Place w;
-  uint32_t count;
-  if (kCluster) {
-    w.item = blockIdx.x / p.cluster;
-    const uint32_t rank = blockIdx.x - w.item * p.cluster;
-    w.tile = rank * p.tiles / p.cluster;
-    count = (rank + 1) * p.tiles / p.cluster - w.tile;
-  } else {
-    const unsigned long long first = p.total * blockIdx.x / p.blocks;
-    count = (uint32_t)(p.total * (blockIdx.x + 1) / p.blocks - first);
-    w.item = (uint32_t)(first / p.tiles);
-    w.tile = (uint32_t)(first - (unsigned long long)w.item * p.tiles);
-  }
+  w.item = p.rounds ? blockIdx.x : words[1], w.tile = p.rounds ? 0 : words[2];
+  const uint32_t count = words[3];
   const uint32_t sk = base + L::k;
   // all threads of the cluster; those that have given up on a wait as well
   auto meet = [] {
@@ -438,7 +453,7 @@ k_attend(const __grid_constant__ AttendParams p) {
             __syncwarp();
           }
           fresh = false;
-          if (++tile == p.tiles) tile = 0, fresh = true;
+          if (++tile == p.tiles) tile = n + 1 == p.rounds * p.tiles ? words[2] : 0, fresh = true;
         }
       } else {
         for (uint32_t n = 0; n < count; ++n) {
@@ -483,7 +498,7 @@ k_attend(const __grid_constant__ AttendParams p) {
         const uint32_t par = n & 1, prev = par ^ 1;
         const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile + r0;
         if (n + 1 < count) {
-          step<NH>(p, w);
+          step<NH>(p, w, words);
           fetch_entries();
         }
         if (n && !(ok = warp_wait(bar(kBarPV + 1), prev))) break;
@@ -738,7 +753,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       put(scale.x, 8);
       hand_over(kBarP);
       Place next = w;
-      step<NH>(p, next);
+      step<NH>(p, next, words);
       if (more) fetch(raw2, n + 1, block2, 0);
       if (!(ok = warp_wait(bar(kBarPV), par))) break;
       put(scale.y, 0);
@@ -881,14 +896,14 @@ k_attend(const __grid_constant__ AttendParams p) {
 // of 512 heads, 2 us and the loads' latency.
 template <uint32_t kBatch>
 __global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttendParams p, uint32_t nh, uint32_t heads) {
-  const uint32_t item = blockIdx.x, c = threadIdx.x & 127;
+  const uint32_t item = p.rounds * p.blocks + blockIdx.x, c = threadIdx.x & 127;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the next kernel follows both)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t token = item / p.head_tiles, h0 = (item - token * p.head_tiles) * nh;
-  const unsigned long long s = (unsigned long long)item * p.tiles;
+  const unsigned long long s = (unsigned long long)blockIdx.x * p.tiles;
   auto owner = [&](unsigned long long tile) -> uint32_t {  // (64-bit divisions only where they have to be)
-    const unsigned long long x = (tile + 1) * p.blocks - 1;
-    return (x | p.total) >> 32 ? (uint32_t)(x / p.total) : (uint32_t)x / (uint32_t)p.total;
+    const unsigned long long x = (tile + 1) * p.sharers - 1;
+    return (x | p.rest) >> 32 ? (uint32_t)(x / p.rest) : (uint32_t)x / (uint32_t)p.rest;
   };
   const uint32_t b0 = owner(s), b1 = owner(s + p.tiles - 1);
   if (b0 == b1) return;  // written whole
@@ -925,8 +940,8 @@ int sm_count() {
 }
 
 struct Plan {
-  uint32_t sms, nh, head_tiles, tiles, keys, blocks, cluster;
-  unsigned long long total;
+  uint32_t sms, nh, head_tiles, tiles, keys, blocks, rounds, sharers, cluster;
+  unsigned long long rest;
   bool parts;  // some item's tiles lie in several blocks that are no cluster
   uint64_t workspace;
 };
@@ -971,9 +986,9 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->head_tiles = (heads + pl->nh - 1) / pl->nh;
   const uint64_t items = tokens * pl->head_tiles;
   if (items > 0x7fffffffull || tokens * heads > 0x7fffffffull) return false;
-  pl->total = items * pl->tiles;
+  const uint64_t total = items * pl->tiles;
   const int sms = sm_count();
-  if (sms < 1 || pl->total > (1ull << 48)) return false;
+  if (sms < 1 || total > (1ull << 48)) return false;
   pl->sms = (uint32_t)sms;
   // An item's tiles on a cluster, when there is one tile per block.  A cluster's join is shared
   // by its blocks alone, where the second kernel's is by all SMs: it takes blocks enough that the
@@ -985,16 +1000,21 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   // that find no place run behind the others: 32 heads 4 x 28: 10.3, 12.3, but 4 x 38: 20.5, 12.3.
   pl->cluster = 1;
   if (pl->tiles > 1 && pl->tiles <= (pl->nh == 64 ? kMostCluster / 2 : kMostCluster) &&
-      pl->total >= (unsigned)sms * 2 / 5 && pl->total <= (unsigned)(pl->tiles == 2 ? sms : sms * 3 / 4)) {
+      total >= (unsigned)sms * 2 / 5 && total <= (unsigned)(pl->tiles == 2 ? sms : sms * 3 / 4)) {
     pl->cluster = pl->tiles;
-    pl->blocks = (uint32_t)pl->total;
+    pl->blocks = (uint32_t)total, pl->rounds = 0, pl->rest = 0, pl->sharers = 1;
     pl->parts = false;
     pl->workspace = 0;
     return true;
   }
-  pl->blocks = pl->total < (unsigned)sms ? (uint32_t)pl->total : (uint32_t)sms;
-  if (pl->total / (pl->blocks ? pl->blocks : 1) > 0x7fffffffull) return false;
-  pl->parts = pl->blocks && !(pl->total % pl->blocks == 0 && (pl->total / pl->blocks) % pl->tiles == 0);
+  pl->blocks = total == 0 ? 1 : total < (unsigned)sms ? (uint32_t)total : (uint32_t)sms;
+  if (total / pl->blocks > 0x7fffffffull) return false;
+  // Whole items first: their results need no join (192 items of 17 tiles: 120.0 us, with even
+  // shares of all tiles 125.0).
+  pl->rounds = (uint32_t)(items / pl->blocks);
+  pl->rest = (items - (uint64_t)pl->rounds * pl->blocks) * pl->tiles;
+  pl->sharers = pl->rest && pl->rest < pl->blocks ? (uint32_t)pl->rest : pl->blocks;
+  pl->parts = pl->rest && pl->tiles > 1;
   pl->workspace = pl->parts ? (uint64_t)2 * pl->blocks * pl->nh * (ULA_ROW_LATENT + 1) * 4 : 0;
   return true;
 }
@@ -1030,7 +1050,7 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   if (pl.workspace && (!a.workspace || a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
   AttendParams p{};
   p.a = a;
-  p.total = pl.total, p.blocks = pl.blocks, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
+  p.rest = pl.rest, p.blocks = pl.blocks, p.rounds = pl.rounds, p.sharers = pl.sharers, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
   p.cluster = pl.cluster;
   p.c0 = a.softmax_scale * 1.44269504088896341f;
   p.part_out = (float *)a.workspace;
@@ -1046,11 +1066,18 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
     // every block at that many registers (8 tokens, 64 heads: 15.6 us; 17.6 with 8), then 8 (20
     // tokens: 24.7 us; 26.7 with 16. 96 tokens of 128 heads, two parts: 141.1 us with 2, 142.8
     // with 8, 148.3 with 16).
-    const uint64_t items = pl.total / pl.tiles;
-    const uint32_t join_heads = items * pl.nh / 4 >= 4ull * pl.sms ? 4 : 2;
-    const bool two = pl.tiles <= 2 || pl.total / pl.blocks >= pl.tiles, few = items * pl.nh / join_heads <= 2ull * pl.sms;
-    e = launch(two ? k_join_parts<2> : few ? k_join_parts<16> : k_join_parts<8>,
-               dim3((uint32_t)items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
+    // Heads per block of the join: 4 share the work on a block's place once every SM has several
+    // blocks (96 tokens x 2,051 rows, 64 heads, both kernels: 72.9 us; 73.9 with 2), and 2 keep the
+    // loads of few items on more SMs (8 tokens: 17.6 us; 21.2 with 4).
+    // Parts in flight per thread: what an item can have up to 4 (one token, 2 parts: 9.4 us with
+    // room for 2, 9.8 with 8; 96 tokens, 2 or 3: 72.9 us with 4, 76.3 with 8), else 16 while
+    // there is a place for every block at that many registers (8 tokens, 16 parts: 15.6 us; 17.6
+    // with 8), then 8 (20 tokens, 9 parts: 24.7 us; 26.7 with 16).
+    const uint32_t items = (uint32_t)(pl.rest / pl.tiles), most = pl.sharers / items + 2;
+    const uint32_t join_heads = (uint64_t)items * pl.nh / 4 >= 4ull * pl.sms ? 4 : 2;
+    const bool few = (uint64_t)items * pl.nh / join_heads <= 2ull * pl.sms;
+    e = launch(pl.tiles <= 2 ? k_join_parts<2> : pl.tiles <= 4 || most <= 4 ? k_join_parts<4> : few ? k_join_parts<16> : k_join_parts<8>,
+               dim3(items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
   }
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }

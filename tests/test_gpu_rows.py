@@ -510,6 +510,21 @@ def test_attend_many_items(R, Q, H, K):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("R,Q,H,K", [
+    (161, 1, 64, 700), (200, 1, 24, 1100), (153, 1, 16, 2000), (155, 2, 8, 260), (77, 2, 128, 150)])
+def test_attend_whole_and_shared_items(R, Q, H, K):
+    """Somewhat more query tokens (times 64 heads) than blocks: some are worked on whole, the rest
+    by several blocks each, fewer than there are, or all."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(R, Q, H, K, 700, R + K, pads=0.05)
+    got = rows.attend(q, kv, entry, SCALE)
+    check_attend(got, attend64(q, kv, entry, SCALE))
+    for _ in range(20):
+        again = rows.attend(q, kv, entry, SCALE)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    rows.sync()
+
+
 def test_attend_other_stream():
     """Calls on streams of their own: inputs and temporaries are held until they have run."""
     from serving_step_sparse_gb300 import rows

@@ -1,0 +1,81 @@
+"""The operators on rows without a GPU: the binding against the header, and refusals that are
+made on the host."""
+import ctypes as C
+import math
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "ula.h")
+
+
+@pytest.fixture(scope="module")
+def ula():
+    from serving_step_sparse_gb300.build import build
+    build()
+    from serving_step_sparse_gb300 import ula
+    return ula
+
+
+def test_constants_match_header(ula):
+    src = open(HEADER).read()
+    for name, val in (("ULA_ROW_BYTES", 656), ("ULA_ROW_LATENT", 512), ("ULA_ROW_ROPE", 64),
+                      ("ULA_ROW_BLOCK", 128), ("ULA_ROPE_PAIRS", ula.ROPE_PAIRS), ("ULA_MAX_AXES", ula.MAX_AXES)):
+        m = re.search(rf"#define {name} (\d+)u", src)
+        assert m and int(m.group(1)) == val, name
+    for name, val in (("ULA_PAIR_ADJACENT", ula.PAIR_ADJACENT), ("ULA_PAIR_HALVES", ula.PAIR_HALVES)):
+        assert re.search(rf"{name}\s*=\s*{val}\b", src), name
+
+
+def test_rotary_layout_matches_header(ula, tmp_path):
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "ula.h"\n'
+                   "int main(void) { printf(\"%zu %zu %zu %zu %zu\\n\", sizeof(ula_rotary), "
+                   "offsetof(ula_rotary, n_axes), offsetof(ula_rotary, pairing), "
+                   "offsetof(ula_rotary, freq), offsetof(ula_rotary, axis)); return 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.dirname(HEADER), str(src), "-o", str(exe)], check=True)
+    want = [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+    r = ula.ula_rotary
+    assert want == [C.sizeof(r), r.n_axes.offset, r.pairing.offset, r.freq.offset, r.axis.offset]
+
+
+def test_calls_refuse_null(ula):
+    none, u32, u64 = C.c_void_p(), C.c_uint32, C.c_uint64
+    lib = ula.lib
+    assert lib.ula_rows_attend(none, none) == ula.ERR_INVALID_ARG
+    assert lib.ula_rows_rotate(none, u32(0), none, u64(0), u32(1), u32(1), u32(0), none, u64(0), u64(0),
+                               none, u64(0), u64(0), none) == ula.ERR_INVALID_ARG
+    assert lib.ula_rows_pack(none, none, u64(0), u32(1), u32(0), none, u64(0), none, u64(0), none, u64(656),
+                             none) == ula.ERR_INVALID_ARG
+    assert lib.ula_rows_join(none, none, u32(1), u64(1), none, none, none) == ula.ERR_INVALID_ARG
+
+
+def test_rotary_refusals(ula):
+    from serving_step_sparse_gb300 import rows
+    freq = [1.0] * 32
+    assert rows.Rotary(freq).n_axes == 1
+    assert rows.Rotary(freq, [0, 1, 2, 0] * 8).n_axes == 3
+    for bad in (dict(freq=freq[:31]), dict(freq=freq, axis=[0] * 31), dict(freq=freq, axis=[ula.MAX_AXES] + [0] * 31),
+                dict(freq=freq, axis=[-1] + [0] * 31), dict(freq=freq, pairing="thirds")):
+        with pytest.raises(ValueError):
+            rows.Rotary(**bad)
+
+
+def test_host_tensors_are_refused(ula):
+    from serving_step_sparse_gb300 import rows
+    rot = rows.Rotary([1.0 / (j + 1) for j in range(32)])
+    pos = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        rows.rotate(torch.zeros(2, 64), pos, rot)
+    with pytest.raises(ValueError):
+        rows.pack(torch.zeros(2, 512), torch.zeros(2, 64), pos, rot)
+    with pytest.raises(ValueError):
+        rows.attend(torch.zeros(1, 1, 1, 576, dtype=torch.bfloat16), torch.zeros(4, 656, dtype=torch.uint8),
+                    torch.zeros(1, 1, 4, dtype=torch.int32), math.sqrt(1 / 576))
+    with pytest.raises(ValueError):
+        rows.join([torch.zeros(1, 512, dtype=torch.bfloat16)], [torch.zeros(1)])

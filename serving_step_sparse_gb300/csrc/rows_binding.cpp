@@ -10,6 +10,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
+
 #include "ula.h"
 
 namespace {
@@ -38,10 +40,17 @@ const at::Tensor &tensor(PyObject *o) {
 }
 bool given(PyObject *o) { return o != Py_None; }
 
-int64_t number(PyObject *o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw python_error();
-  return v;
+// The ula_rotary that an object (the ctypes struct) holds, read through its buffer: no address is
+// kept in Python, where a copied or unpickled rotary would bring another object's.
+ula_rotary rotary_of(PyObject *o) {
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw python_error();
+  ula_rotary r;
+  const bool whole = b.len == (Py_ssize_t)sizeof r;
+  if (whole) memcpy(&r, b.buf, sizeof r);
+  PyBuffer_Release(&b);
+  need(whole, "the rotary is a ula_rotary");
+  return r;
 }
 
 int type_of(const at::Tensor &t) {
@@ -74,11 +83,11 @@ struct Positions {
   at::Tensor held;
   const int32_t *data;
   uint64_t stride;
-  Positions(const On &on, const at::Tensor &t, const ula_rotary *rotary, int64_t n) : held(t) {
+  Positions(const On &on, const at::Tensor &t, const ula_rotary &rotary, int64_t n) : held(t) {
     need(t.scalar_type() == at::kInt, "positions are int32");
     on.same(t);
     const bool one = t.dim() == 1;
-    need((one || t.dim() == 2) && (one ? 1 : t.size(0)) >= rotary->n_axes && t.size(-1) == n,
+    need((one || t.dim() == 2) && (one ? 1 : t.size(0)) >= rotary.n_axes && t.size(-1) == n,
          "positions are [axes][tokens]");
     if (n > 1 && t.stride(-1) != 1) held = t.contiguous();
     data = held.data_ptr<int32_t>();
@@ -104,10 +113,10 @@ PyObject *wrap2(PyObject *oa, const at::Tensor &a, PyObject *ob, const at::Tenso
   return both;
 }
 
-// rotate(x, pos, rotary address, out or None, inverse) -> out
+// rotate(x, pos, rotary, out or None, inverse) -> out
 PyObject *rotate(PyObject *const *a) {
   at::Tensor x = tensor(a[0]);
-  const auto *rotary = reinterpret_cast<const ula_rotary *>(number(a[2]));
+  const ula_rotary rotary = rotary_of(a[2]);
   const int type = type_of(x);
   need((x.dim() == 2 || x.dim() == 3) && x.size(-1) == kRope && type >= 0,
        "x is [tokens][heads][64] of bf16, f16 or f32");
@@ -121,17 +130,17 @@ PyObject *rotate(PyObject *const *a) {
        "out has x's shape and type, and dense channels");
   need(n <= INT32_MAX && heads <= INT32_MAX, "too many tokens or heads");
   if (x.stride(-1) != 1) x = x.contiguous();
-  check(ula_rows_rotate(rotary, a[4] == Py_True ? ULA_ROTATE_INVERSE : 0, pos.data, pos.stride, n, heads, type,
+  check(ula_rows_rotate(&rotary, a[4] == Py_True ? ULA_ROTATE_INVERSE : 0, pos.data, pos.stride, n, heads, type,
                         x.data_ptr(), x.stride(0), three ? x.stride(1) : 0, out.data_ptr(), out.stride(0),
                         three ? out.stride(1) : 0, on.stream()),
         "ula_rows_rotate");
   return wrap(a[3], out);
 }
 
-// pack(latent, rope, pos, rotary address, rows or None) -> rows
+// pack(latent, rope, pos, rotary, rows or None) -> rows
 PyObject *pack(PyObject *const *a) {
   at::Tensor latent = tensor(a[0]), rope = tensor(a[1]);
-  const auto *rotary = reinterpret_cast<const ula_rotary *>(number(a[3]));
+  const ula_rotary rotary = rotary_of(a[3]);
   const int type = type_of(latent);
   need(latent.dim() == 2 && latent.size(1) == kLatent && type >= 0, "latent is [tokens][512] of bf16, f16 or f32");
   const On on(latent);
@@ -148,7 +157,7 @@ PyObject *pack(PyObject *const *a) {
   need(n <= INT32_MAX, "too many tokens");
   if (latent.stride(1) != 1) latent = latent.contiguous();
   if (rope.stride(1) != 1) rope = rope.contiguous();
-  check(ula_rows_pack(rotary, pos.data, pos.stride, n, type, latent.data_ptr(), latent.stride(0), rope.data_ptr(),
+  check(ula_rows_pack(&rotary, pos.data, pos.stride, n, type, latent.data_ptr(), latent.stride(0), rope.data_ptr(),
                       rope.stride(0), rows.data_ptr(), n > 1 ? rows.stride(0) : kRow, on.stream()),
         "ula_rows_pack");
   return wrap(a[4], rows);

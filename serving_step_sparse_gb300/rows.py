@@ -13,7 +13,6 @@ Wrong shapes, types or devices raise ValueError, errors of the C ABI ``ula.UlaEr
 """
 from __future__ import annotations
 
-import ctypes as C
 import importlib.machinery
 import importlib.util
 import os
@@ -80,7 +79,6 @@ class Rotary:
         self.config.n_axes, self.config.pairing = self.n_axes, _PAIRINGS[pairing]
         self.config.freq[:] = freq
         self.config.axis[:] = axis
-        self._address = C.addressof(self.config)
 
 
 def rotate(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *, out: torch.Tensor | None = None,
@@ -92,8 +90,8 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *, out: torch.Ten
     inverse turns back; it is also the gradient.
     """
     if stream is not None:
-        return _on(stream, _rows.rotate, x, pos, rotary._address, out, bool(inverse))
-    return _rows.rotate(x, pos, rotary._address, out, bool(inverse))
+        return _on(stream, _rows.rotate, x, pos, rotary.config, out, bool(inverse))
+    return _rows.rotate(x, pos, rotary.config, out, bool(inverse))
 
 
 def pack(latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor, rotary: Rotary,
@@ -106,8 +104,8 @@ def pack(latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor, rotary: Ro
     [n][L][656] that ``UlaCache.alloc`` takes), or None for a new tensor.  Returns rows.
     """
     if stream is not None:
-        return _on(stream, _rows.pack, latent, rope, pos, rotary._address, rows)
-    return _rows.pack(latent, rope, pos, rotary._address, rows)
+        return _on(stream, _rows.pack, latent, rope, pos, rotary.config, rows)
+    return _rows.pack(latent, rope, pos, rotary.config, rows)
 
 
 def attend(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax_scale: float, *,

@@ -697,3 +697,19 @@ def test_attend_partitions_of_tp():
     assert (np.abs(z.double().cpu().numpy() - lse) <= zslack + 2.0 ** -19 * (1 + np.abs(lse))).all()
     tol = 2.0 ** -8 * 1.01 * np.abs(out) + (2.0 ** -8 + 2.0 ** -8 + np.expm1(2 * zslack[..., None])) * slack
     assert (np.abs(o.double().cpu().numpy() - out) <= tol).all()
+
+
+def test_rotary_copies():
+    """A rotary that was copied or pickled turns by its own frequencies."""
+    import copy
+    import pickle
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(61)
+    x = torch.from_numpy(rng.standard_normal((9, 4, 64))).float().cuda()
+    pos = torch.from_numpy(positions(rng, 3, 9)).cuda()
+    rot, _, _ = make_rotary(rng, 3, "halves")
+    want = rows.rotate(x, pos, rot)
+    others = [copy.deepcopy(rot), pickle.loads(pickle.dumps(rot))]
+    rot.config.freq[:] = [0.0] * 32
+    for other in others:
+        assert torch.equal(rows.rotate(x, pos, other), want)

@@ -79,3 +79,38 @@ def test_host_tensors_are_refused(ula):
                     torch.zeros(1, 1, 4, dtype=torch.int32), math.sqrt(1 / 576))
     with pytest.raises(ValueError):
         rows.join([torch.zeros(1, 512, dtype=torch.bfloat16)], [torch.zeros(1)])
+
+
+def test_rotary_copies_own_their_memory(ula, monkeypatch):
+    """A copied or unpickled rotary is read from its own memory, whatever became of the first."""
+    import copy
+    import gc
+    import pickle
+    import types
+    from serving_step_sparse_gb300 import rows
+    freq = [1.0 / (j + 1) for j in range(32)]
+    first, second = rows.Rotary(freq, [0, 1] * 16, "halves"), rows.Rotary(freq, [0, 1] * 16, "halves")
+    assert pickle.dumps(first) == pickle.dumps(second)      # what it says, not where it stands
+    read = []
+
+    def call(x, pos, rotary, *rest):
+        read.append(rotary if isinstance(rotary, int) else C.addressof(rotary))
+
+    monkeypatch.setattr(rows, "_rows", types.SimpleNamespace(rotate=call, pack=call))
+    for make in (copy.copy, copy.deepcopy, lambda r: pickle.loads(pickle.dumps(r))):
+        first = rows.Rotary(freq, [0, 1] * 16, "halves")
+        other = make(first)
+        del first
+        gc.collect()
+        rows.rotate(None, None, other)
+        assert read[-1] == C.addressof(other.config)
+        assert bytes(other.config) == bytes(second.config) and other.n_axes == 2
+
+
+def test_binding_refuses_a_rotary_of_another_size(ula):
+    from serving_step_sparse_gb300 import rows
+    for bad in (bytes(8), (C.c_char * 1024)()):
+        with pytest.raises(ValueError):
+            rows._rows.rotate(torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), bad, None, False)
+    with pytest.raises(TypeError):
+        rows._rows.rotate(torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), 8, None, False)

@@ -483,7 +483,7 @@ int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_a
  *   z[e]  = softmax_scale * <q[r][i][h], (latent(e), rope(e))>
  *   out   = sum_e softmax(z)[e] * latent(e)          (bf16, [n_req][n_q][heads][512])
  *   lse   = ln sum_e exp z[e]                        (fp32, [n_req][n_q][heads])
- * A query token that selects nothing gets out = 0 and lse = -inf.
+ * A query token that selects nothing gets out = 0 and lse = -inf, whatever its q holds.
  * Logits, maxima and sums are held in fp32; the probabilities enter the second product
  * in 16 bits.
  *   q         : device bf16, 576 channels (512 latent, 64 rope, already turned) at

@@ -636,10 +636,10 @@ k_attend(const __grid_constant__ AttendParams p) {
         for (uint32_t j = 0; j < kSlots; ++j) raw1[j] = raw2[j];
       }
       if (!ok) break;
-      // this row's scales; a row without an entry (its codes are zeros) gets logits of -inf
+      // this row's scales, and whether there is a row
       if (!(ok = warp_wait(bar(kBarScale), par))) break;
       const float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
-      const float off = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] ? 0.f : -INFINITY;
+      const bool present = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] != 0;
       const bool more = n + 1 < count;
 
       // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0.
@@ -656,7 +656,7 @@ k_attend(const __grid_constant__ AttendParams p) {
         if (lane == 0) mbar_arrive(bar(kBarDrained));
         const float s = scale.y * p.c0;
 #pragma unroll
-        for (int h = 0; h < HG; h += 2) z[h] = z[h + 1] = off, fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
+        for (int h = 0; h < HG; h += 2) mul2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
       if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1))) break;
       if (more) fetch(raw1, n + 1, block1, 0);
@@ -686,6 +686,13 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
+      }
+
+      // A row that is not there gets logits of -inf, whatever the products say: its zeros times a NaN
+      // or an infinity of the query are NaN.
+      if (!__all_sync(0xffffffffu, present)) {
+#pragma unroll
+        for (int h = 0; h < HG; ++h) z[h] = present ? z[h] : -INFINITY;
       }
 
       if (more) fetch(raw1, n + 1, block1, 1);

@@ -713,3 +713,44 @@ def test_rotary_copies():
     rot.config.freq[:] = [0.0] * 32
     for other in others:
         assert torch.equal(rows.rotate(x, pos, other), want)
+
+
+@pytest.mark.parametrize("R,H,K", [
+    (1, 16, 100), (1, 20, 600), (2, 64, 2048), (160, 64, 300), (300, 8, 64),
+    (12, 16, 1024), (16, 32, 600), (20, 40, 512)])        # (the last three: clusters)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_attend_empty_query_not_finite(R, H, K, bad):
+    """A query token that selects nothing gets 0 and -inf whatever its query holds, an unused
+    query slot of a batch for instance; the others keep their bits."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, _ = attend_case(R, 1, H, K, 300, R + H + K, pads=0.1)
+    empty = sorted({0, R - 1})
+    entry[empty] = -1
+    entry[empty, 0, K // 2:] = 300                         # out of range selects nothing either
+    want = rows.attend(q, kv, entry, SCALE)
+    q[empty[0]] = bad
+    q[empty[-1], 0, :, ::97] = bad
+    for e in (entry, entry[:, :, :0]):
+        out, lse = rows.attend(q, kv, e, SCALE)
+        assert (out[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    out, lse = rows.attend(q, kv, entry, SCALE)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    rows.sync()
+
+
+def test_attend_row_not_there_not_finite():
+    """One row among pads: a query of NaN or infinity is that row's answer, not the pads'."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(2, 3, 24, 300, 50, 3, own=True)
+    kv[7, :128] = 0x38                                     # codes of 1 in the block in question
+    kv[7, 512:516] = torch.tensor([1.0]).view(torch.uint8).cuda()
+    entry[:] = -1
+    entry[0, 0, 131] = 7
+    q[0, 0, 5, :128] = -math.inf                           # that row's logit: -inf
+    q[0, 0, 6, 3] = math.inf
+    q[0, 0, 7, 3] = math.nan
+    out, lse = rows.attend(q, kv, entry, SCALE)
+    assert torch.isneginf(lse[0, 0, 5]) and (out[0, 0, 5] == 0).all()
+    assert torch.isnan(out[0, 0, 6]).all() and torch.isnan(out[0, 0, 7]).all()
+    rest = [h for h in range(24) if h not in (5, 6, 7)]
+    check_attend((out[:, :, rest], lse[:, :, rest]), attend64(q[:, :, rest], kv, entry, SCALE))

@@ -536,6 +536,12 @@ int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t pa
  */
 int ula_rows_sync(void *stream);
 
+/* Test hook: in later ula_rows_attend calls of this process, one of the kernel's barriers
+ * (0..ULA_DEBUG_BARRIERS - 1; negative: none, the default) never opens, so that the waits on it
+ * run out (after about a second) on a working GPU and the kernel's way out is taken. */
+#define ULA_DEBUG_BARRIERS 23
+int ula_rows_debug_hold(int barrier);
+
 /*
  * TP mode, emulated on one GPU (§2 "Unified logical addresses", TP paragraph): the
  * pools of P GPUs form one distributed address space in which logical address t

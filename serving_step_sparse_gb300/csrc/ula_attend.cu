@@ -17,6 +17,7 @@
 // f16 since scales may span many orders).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 
 #include "ula.h"
 
@@ -48,6 +49,7 @@ struct AttendParams {
   uint32_t keys;             // entries per query token, own rows included
   uint32_t cluster;          // blocks of a cluster (one item each), or 1
   float c0;
+  uint32_t hold;             // (test hook) an mbarrier whose phases never end; kBars: none
   float *part_out;           // [2 * blocks][NH][512]: unfinished items' results, normalised
   float *part_lse;           // [2 * blocks][NH]: their log2 sums
 };
@@ -64,8 +66,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded: false after 2^20 tries. Each returns at once or after at most about a microsecond (the
-// time given to it), so a wait that is never met ends after 10 ms to 1 s, and any wait that these
+// Bounded: false after 2^18 tries. A try that is not met comes back after 4.0 us on this GPU,
+// whatever time it is given, so a wait that is never met ends after 1.05 s, and any wait that these
 // kernels can meet is shorter than a tenth of a millisecond. The loop is written out because its
 // size matters: the compute warps pass through some 15 waits a tile, their code is longer than
 // the instruction caches nearest to them, and with a clock read and two ways out in each wait
@@ -74,8 +76,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, 0;\n"
-      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n @p bra over;\n"
-      " add.u32 i, i, 1;\n setp.lt.u32 p, i, 0x100000;\n @p bra again;\n setp.ne.u32 p, 0, 0;\n"
+      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra over;\n"
+      " add.u32 i, i, 1;\n setp.lt.u32 p, i, 0x40000;\n @p bra again;\n setp.ne.u32 p, 0, 0;\n"
       "over:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done;
@@ -223,7 +225,10 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
 // TMEM; Drained: block 1's S^T has been read; P: P_0, and P_1 to P_3, stand in shared memory; PV + b:
 // O_b^T is up to date and block b's codes are free; X: exchange in a column group; Place: the rows'
 // addresses stand; Scale: their scales; End: a warp's products have ended.
-enum { kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarPlace = 19, kBarScale = 20, kBarEnd = 21, kBars = 24 };
+enum {
+  kBarFull = 0, kBarS = 5, kBarDrained = 10, kBarP = 11, kBarPV = 13, kBarX = 17, kBarPlace = 19, kBarScale = 20, kBarEnd = 21,
+  kBars = ULA_DEBUG_BARRIERS
+};
 
 template <uint32_t NH>
 struct Shared {
@@ -233,7 +238,7 @@ struct Shared {
   static constexpr uint32_t place = scale + kTile * 16;       // [2][128] the rows' addresses, 0: no row
   static constexpr uint32_t top = place + 2 * kTile * 8;      // [NH][4] tile maxima (then sums) by quadrant
   static constexpr uint32_t bars = top + NH * 16;
-  static constexpr uint32_t words = bars + kBars * 8;         // TMEM address; first remaining item, its tile; tiles in all
+  static constexpr uint32_t words = bars + 24 * 8;            // TMEM address; first remaining item, its tile; tiles in all
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
 };
 
@@ -352,6 +357,10 @@ k_attend(const __grid_constant__ AttendParams p) {
     for (uint32_t i = 0; i < 4; ++i) mbar_init(bar(kBarPV + i), 1);
     for (uint32_t i = 0; i < kWarps / 4; ++i) mbar_init(bar(kBarX + i), 4);
     mbar_init(bar(kBarEnd), 1), mbar_init(bar(kBarEnd + 1), 1);
+    if (p.hold < kBars) {
+      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(p.hold)) : "memory");
+      mbar_init(bar(p.hold), 1u << 19);  // (more arrivals than a launch makes)
+    }
     fence_async_smem();
   }
   // (an address read before its time, after a wait that ran out, is no address)
@@ -470,11 +479,12 @@ k_attend(const __grid_constant__ AttendParams p) {
         }
       }
       const uint32_t end = bar(kBarEnd + (warp == kWarps ? 0 : 1));
+      bool ended = true;
       if (elect_one()) {  // every product has ended before the block's TMEM goes
         mma_commit(end);
-        mbar_wait(end, 0);
+        ended = mbar_wait(end, 0);
       }
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ended) && ok;
     } else if (warp <= kWarps + kLoaders) {
       // ---- this warp's 64 rows of every tile: their addresses, one tile ahead (two a lane),
       // their scales, and their rope channels straight to where the products read them
@@ -946,6 +956,8 @@ int sm_count() {
   return n;
 }
 
+std::atomic<uint32_t> g_hold{kBars};
+
 struct Plan {
   uint32_t sms, nh, head_tiles, tiles, keys, blocks, rounds, sharers, cluster;
   unsigned long long rest;
@@ -1059,6 +1071,7 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   p.a = a;
   p.rest = pl.rest, p.blocks = pl.blocks, p.rounds = pl.rounds, p.sharers = pl.sharers, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
   p.cluster = pl.cluster;
+  p.hold = g_hold.load(std::memory_order_relaxed);
   p.c0 = a.softmax_scale * 1.44269504088896341f;
   p.part_out = (float *)a.workspace;
   p.part_lse = p.part_out + (uint64_t)2 * pl.blocks * pl.nh * ULA_ROW_LATENT;
@@ -1087,6 +1100,12 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
                dim3(items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
   }
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+extern "C" int ula_rows_debug_hold(int barrier) {
+  if (barrier >= (int)kBars) return ULA_ERR_INVALID_ARG;
+  g_hold.store(barrier < 0 ? (uint32_t)kBars : (uint32_t)barrier, std::memory_order_relaxed);
+  return ULA_OK;
 }
 
 extern "C" int ula_rows_sync(void *stream) {

@@ -149,6 +149,8 @@ def _load():
     lib.ula_tp_destroy.restype = i32
     lib.ula_rows_sync.argtypes = [p]
     lib.ula_rows_sync.restype = i32
+    lib.ula_rows_debug_hold.argtypes = [i32]
+    lib.ula_rows_debug_hold.restype = i32
     return lib
 
 
@@ -344,3 +346,8 @@ def ula_dedup_noalloc(d_sel: int, n: int, d_uniq: int, d_entry_row: int, d_n_uni
 
 def ula_rows_sync(stream) -> None:
     _check(lib.ula_rows_sync(stream), "ula_rows_sync")
+
+
+def ula_rows_debug_hold(barrier: int) -> None:
+    """Test hook: one of the attention kernel's barriers never opens (negative: none)."""
+    _check(lib.ula_rows_debug_hold(barrier), "ula_rows_debug_hold")

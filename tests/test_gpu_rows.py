@@ -754,3 +754,38 @@ def test_attend_row_not_there_not_finite():
     assert torch.isnan(out[0, 0, 6]).all() and torch.isnan(out[0, 0, 7]).all()
     rest = [h for h in range(24) if h not in (5, 6, 7)]
     check_attend((out[:, :, rest], lse[:, :, rest]), attend64(q[:, :, rest], kv, entry, SCALE))
+
+
+def gives_up(case, barrier):
+    """A call in which one barrier never opens: it ends, its error is reported once, and the next
+    call is whole."""
+    from serving_step_sparse_gb300 import rows, ula
+    q, kv, entry, own_rows = case
+    want = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    rows.sync()
+    ula.ula_rows_debug_hold(barrier)
+    try:
+        rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    finally:
+        ula.ula_rows_debug_hold(-1)
+    with pytest.raises(ula.UlaError) as e:
+        rows.sync()
+    assert e.value.code == ula.ERR_TIMEOUT
+    rows.sync()
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    rows.sync()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("barrier", range(23))
+def test_attend_gives_up(barrier):
+    """Every barrier, with several tiles in a block and items that blocks share."""
+    gives_up(attend_case(90, 2, 20, 300, 500, barrier, own=True), barrier)
+
+
+@pytest.mark.parametrize("R,Q,H,K", [
+    (1, 1, 64, 100), (12, 1, 16, 1024), (37, 1, 64, 300)])      # (the last two: clusters)
+@pytest.mark.parametrize("barrier", [4, 5, 17, 19, 21])
+def test_attend_gives_up_elsewhere(R, Q, H, K, barrier):
+    """Single tiles, and clusters, whose blocks all have to meet."""
+    gives_up(attend_case(R, Q, H, K, 500, R + H, pads=0.1), barrier)

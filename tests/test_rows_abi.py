@@ -114,3 +114,16 @@ def test_binding_refuses_a_rotary_of_another_size(ula):
             rows._rows.rotate(torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), bad, None, False)
     with pytest.raises(TypeError):
         rows._rows.rotate(torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), 8, None, False)
+
+
+def test_debug_hold_refuses_other_barriers(ula):
+    src = open(HEADER).read()
+    n = int(re.search(r"#define ULA_DEBUG_BARRIERS (\d+)", src).group(1))
+    try:
+        ula.ula_rows_debug_hold(n - 1)
+        for bad in (n, 1 << 30):
+            with pytest.raises(ula.UlaError) as e:
+                ula.ula_rows_debug_hold(bad)
+            assert e.value.code == ula.ERR_INVALID_ARG
+    finally:
+        ula.ula_rows_debug_hold(-1)

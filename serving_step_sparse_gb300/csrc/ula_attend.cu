@@ -834,6 +834,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
       w = next;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (the queries of a warp that gave up before it used them)
     if (kCluster) {  // (here, since the other warps have fewer registers)
       tc_fence_before();
       meet();

@@ -139,4 +139,5 @@ def join(outs, lses, *, out: torch.Tensor | None = None, lse: torch.Tensor | Non
 def sync(stream: torch.cuda.Stream | None = None) -> None:
     """Waits for the stream; raises the first error these operators latched on the device."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    ula.ula_rows_sync(s.cuda_stream)
+    with torch.cuda.device(s.device):
+        ula.ula_rows_sync(s.cuda_stream)

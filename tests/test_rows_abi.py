@@ -127,3 +127,21 @@ def test_debug_hold_refuses_other_barriers(ula):
             assert e.value.code == ula.ERR_INVALID_ARG
     finally:
         ula.ula_rows_debug_hold(-1)
+
+
+def test_sync_is_made_on_the_streams_device(ula, monkeypatch):
+    import contextlib
+    import types
+    from serving_step_sparse_gb300 import rows
+    log = []
+
+    @contextlib.contextmanager
+    def device(d):
+        log.append(("on", d))
+        yield
+        log.append(("off", d))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(ula, "ula_rows_sync", lambda s: log.append(("sync", s)))
+    rows.sync(types.SimpleNamespace(device="cuda:3", cuda_stream=77))
+    assert log == [("on", "cuda:3"), ("sync", 77), ("off", "cuda:3")]

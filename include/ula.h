@@ -411,7 +411,8 @@ int ula_dedup_noalloc(const uint32_t *d_sel, uint32_t n, uint32_t *d_uniq,
  * These calls need no context.  Every one is asynchronous on `stream`, launches on the
  * current device, and returns ULA_ERR_INVALID_ARG with nothing launched for bad
  * arguments (NULL buffers with work to do, misaligned buffers or strides, sizes out of
- * range).  They allocate nothing and keep nothing between calls.  A kernel's launch and
+ * range).  They allocate nothing and keep nothing between calls (ula_rows_sync keeps what
+ * it has reported).  A kernel's launch and
  * setup overlap the end of the one before it on the stream; none touches the buffers
  * before that one has ended.
  */
@@ -530,9 +531,11 @@ int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t pa
                   void *out, float *lse, void *stream);
 
 /*
- * ula_rows_sync -- wait for `stream`, then return and clear the first error that a
- * kernel of these operators latched on the current device (ULA_ERR_TIMEOUT: a bounded
- * wait of ula_rows_attend expired and that call's outputs are not valid), or ULA_OK.
+ * ula_rows_sync -- wait for `stream` (of the current device), then return ULA_OK, or
+ * ULA_ERR_TIMEOUT if a bounded wait of an ula_rows_attend call has expired since the
+ * stream's last ula_rows_sync: the outputs of some call are not valid.  The error is the
+ * device's: every stream's next sync returns it once, whichever stream the call was on
+ * (a stream that waits for another's results, or replays a graph, gets it as well).
  */
 int ula_rows_sync(void *stream);
 

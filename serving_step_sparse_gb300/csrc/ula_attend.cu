@@ -18,12 +18,15 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <atomic>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "ula.h"
 
 namespace {
 
-__device__ int g_status;  // the first error that a kernel of this file latched
+__device__ uint32_t g_late;  // warps whose waits ran out, in all launches so far
 
 constexpr uint32_t kTile = 128;                      // rows per tile
 constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
@@ -898,7 +901,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       }
     }
   }
-  if (!ok && lane == 0) atomicCAS(&g_status, 0, (int)ULA_ERR_TIMEOUT);
+  if (!ok && lane == 0) atomicAdd(&g_late, 1u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1109,16 +1112,25 @@ extern "C" int ula_rows_debug_hold(int barrier) {
   return ULA_OK;
 }
 
+// The count of late warps at each stream's last sync (0 where it stands at none).  Kept per stream,
+// so that no stream's sync takes an error that another's results depend on.
 extern "C" int ula_rows_sync(void *stream) {
+  static std::mutex lock;
+  static std::map<std::pair<int, unsigned long long>, uint32_t> seen;
   cudaStream_t st = (cudaStream_t)stream;
-  int code = ULA_OK;
-  const int none = ULA_OK;
-  if (cudaMemcpyFromSymbolAsync(&code, g_status, sizeof code, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+  uint32_t late = 0;
+  int device = 0;
+  unsigned long long id = 0;
+  if (cudaMemcpyFromSymbolAsync(&late, g_late, sizeof late, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return ULA_ERR_CUDA;
-  if (code != ULA_OK &&
-      (cudaMemcpyToSymbolAsync(g_status, &none, sizeof none, 0, cudaMemcpyHostToDevice, st) != cudaSuccess ||
-       cudaStreamSynchronize(st) != cudaSuccess))
-    return ULA_ERR_CUDA;
-  return code;
+  if (late == 0) return ULA_OK;
+  if (cudaGetDevice(&device) != cudaSuccess || cudaStreamGetId(st, &id) != cudaSuccess) return ULA_ERR_CUDA;
+  try {
+    const std::lock_guard<std::mutex> held(lock);
+    uint32_t &last = seen[{device, id}];
+    return std::exchange(last, late) == late ? ULA_OK : ULA_ERR_TIMEOUT;
+  } catch (...) {  // (no memory for the entry: the error is returned, and again next time)
+    return ULA_ERR_TIMEOUT;
+  }
 }

@@ -137,7 +137,9 @@ def join(outs, lses, *, out: torch.Tensor | None = None, lse: torch.Tensor | Non
 
 
 def sync(stream: torch.cuda.Stream | None = None) -> None:
-    """Waits for the stream; raises the first error these operators latched on the device."""
+    """Waits for the stream (default: the current one).  Raises ``ula.UlaError`` if a bounded wait of
+    an ``attend`` on the stream's device, on this stream or another, has run out since this
+    stream's last sync; the call's outputs are then not valid."""
     s = stream if stream is not None else torch.cuda.current_stream()
     with torch.cuda.device(s.device):
         ula.ula_rows_sync(s.cuda_stream)

@@ -789,3 +789,28 @@ def test_attend_gives_up(barrier):
 def test_attend_gives_up_elsewhere(R, Q, H, K, barrier):
     """Single tiles, and clusters, whose blocks all have to meet."""
     gives_up(attend_case(R, Q, H, K, 500, R + H, pads=0.1), barrier)
+
+
+def test_sync_of_several_streams():
+    """A wait that ran out on one stream is reported by every stream's next sync, once by each."""
+    from serving_step_sparse_gb300 import rows, ula
+    q, kv, entry, _ = attend_case(1, 1, 16, 64, 64, 1)
+    streams = [torch.cuda.Stream() for _ in range(3)] + [torch.cuda.current_stream()]
+    for s in streams:
+        try:
+            rows.sync(s)
+        except ula.UlaError:
+            pass                                            # (an earlier test's)
+    for failing in (1, 3):
+        ula.ula_rows_debug_hold(4)
+        try:
+            rows.attend(q, kv, entry, SCALE, stream=streams[failing])
+        finally:
+            ula.ula_rows_debug_hold(-1)
+        torch.cuda.synchronize()
+        for s in streams:
+            with pytest.raises(ula.UlaError) as e:
+                rows.sync(s)
+            assert e.value.code == ula.ERR_TIMEOUT
+        for s in streams:
+            rows.sync(s)

@@ -451,7 +451,8 @@ typedef struct ula_rotary {
  *   d_x   : device, channel c of head h of token t at
  *           d_x[t * x_token_stride + h * x_head_stride + c] (strides in elements).
  *   d_out : likewise; may be d_x itself with the same strides (in place), and must not
- *           overlap it otherwise.
+ *           overlap it otherwise.  Its own rows of 64 channels may not overlap
+ *           (ULA_ERR_INVALID_ARG).
  *   dtype : ULA_TYPE_* of d_x and d_out.
  */
 int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const int32_t *d_pos,

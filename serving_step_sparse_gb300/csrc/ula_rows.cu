@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cmath>
+#include <utility>
 
 #include "ula.h"
 
@@ -347,6 +348,23 @@ cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t smem, cudaStream_t
 uint32_t type_size(uint32_t dtype) { return dtype == ULA_TYPE_F32 ? 4u : 2u; }
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Whether two of the rows of 64 channels at i * si + j * sj (i < ni, j < nj) share elements.
+bool overlap(uint64_t ni, uint64_t si, uint64_t nj, uint64_t sj) {
+  constexpr uint64_t kRow = ULA_ROW_ROPE;
+  if ((ni > 1 && si < kRow) || (nj > 1 && sj < kRow)) return true;
+  if (ni < 2 || nj < 2) return false;
+  if (si > sj) std::swap(si, sj), std::swap(ni, nj);
+  using wide = unsigned __int128;
+  if (sj >= (wide)(ni - 1) * si + kRow) return false;  // the rows of one j lie before those of the next
+  const bool fewer_i = ni <= nj;                       // interleaved: every distance along the shorter side
+  const uint64_t na = fewer_i ? ni : nj, nb = fewer_i ? nj : ni, sa = fewer_i ? si : sj, sb = fewer_i ? sj : si;
+  for (uint64_t a = 1; a < na; ++a) {
+    const wide at = (wide)a * sa, b = at / sb, below = at - b * sb;
+    if ((b >= 1 && b < nb && below < kRow) || (b + 1 < nb && sb - below < kRow)) return true;
+  }
+  return false;
+}
+
 // Two rows per thread (4 loads in flight) where there are blocks for every SM several times
 // over: 4,096 tokens x 128 heads of bf16, 26.0 us (5.2 TB/s) against 29.3 with one and 27.8
 // with four.  Fewer rows are spread over more blocks of one row per thread, and so are
@@ -394,6 +412,7 @@ extern "C" int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const i
   if (!d_pos || !d_x || !d_out || (work + 7) / 8 > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
   if (!aligned(d_pos, 4) || !aligned(d_x, type_size(dtype)) || !aligned(d_out, type_size(dtype)))
     return ULA_ERR_INVALID_ARG;
+  if (overlap(n, out_token_stride, heads, out_head_stride)) return ULA_ERR_INVALID_ARG;
   p.pos = d_pos, p.pos_axis_stride = pos_axis_stride, p.n = n, p.heads = heads;
   p.x = d_x, p.xt = x_token_stride, p.xh = x_head_stride;
   p.out = d_out, p.ot = out_token_stride, p.oh = out_head_stride;

@@ -86,7 +86,8 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *, out: torch.Ten
     """Turns the rope channels of x [tokens][heads][64] (or [tokens][64]); bf16, f16 or f32.
 
     pos: int32 [axes][tokens] (or [tokens]).  out: x itself (in place) or another tensor of x's
-    shape and type, such as the last 64 channels of the queries that ``attend`` reads.
+    shape and type, such as the last 64 channels of the queries that ``attend`` reads; its tokens
+    and heads may not share memory.
     inverse turns back; it is also the gradient.
     """
     if stream is not None:

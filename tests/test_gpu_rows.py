@@ -814,3 +814,23 @@ def test_sync_of_several_streams():
             assert e.value.code == ula.ERR_TIMEOUT
         for s in streams:
             rows.sync(s)
+
+
+def test_rotate_output_over_itself():
+    """An output whose tokens or heads share memory is refused; one that interleaves is not."""
+    from serving_step_sparse_gb300 import rows, ula
+    rng = np.random.default_rng(8)
+    rot, _, _ = make_rotary(rng, 1, "halves")
+    x = torch.from_numpy(rng.standard_normal((6, 4, 64))).float().cuda()
+    pos = torch.from_numpy(positions(rng, 1, 6)).cuda()
+    want = rows.rotate(x, pos, rot)
+    store = torch.zeros(6 * 4 * 64 + 64, device="cuda")
+    for shape, stride in (((6, 4, 64), (0, 64, 1)), ((6, 4, 64), (256, 0, 1)), ((6, 4, 64), (192, 64, 1)),
+                          ((6, 4, 64), (64, 320, 1)), ((6, 4, 64), (256, 32, 1))):
+        with pytest.raises(ula.UlaError) as e:
+            rows.rotate(x, pos, rot, out=store.as_strided(shape, stride))
+        assert e.value.code == ula.ERR_INVALID_ARG
+    assert not store.any()
+    for stride in ((256, 64, 1), (64, 384, 1)):
+        out = torch.zeros(4 * 384, device="cuda").as_strided((6, 4, 64), stride)
+        assert torch.equal(rows.rotate(x, pos, rot, out=out), want)

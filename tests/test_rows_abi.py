@@ -145,3 +145,20 @@ def test_sync_is_made_on_the_streams_device(ula, monkeypatch):
     monkeypatch.setattr(ula, "ula_rows_sync", lambda s: log.append(("sync", s)))
     rows.sync(types.SimpleNamespace(device="cuda:3", cuda_stream=77))
     assert log == [("on", "cuda:3"), ("sync", 77), ("off", "cuda:3")]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls that are let through would launch on no memory")
+def test_rotate_refuses_an_output_over_itself(ula):
+    """Against every pair of rows, over strides that nest, interleave and collide."""
+    import itertools
+    rot = ula.ula_rotary()
+    rot.n_axes = 1
+    u32, u64, at = C.c_uint32, C.c_uint64, C.c_void_p(1 << 20)
+    strides = [0, 1, 63, 64, 65, 96, 100, 127, 128, 160, 192, 200, 256, 320, 576]
+    for n, heads in ((1, 1), (1, 3), (4, 1), (2, 2), (3, 5), (7, 4)):
+        for st, sh in itertools.product(strides, strides):
+            starts = sorted(t * st + h * sh for t in range(n) for h in range(heads))
+            apart = all(b - a >= 64 for a, b in zip(starts, starts[1:]))
+            code = ula.lib.ula_rows_rotate(C.byref(rot), u32(0), at, u64(0), u32(n), u32(heads), u32(0), at, u64(0),
+                                           u64(0), at, u64(st), u64(sh), None)
+            assert code == (ula.ERR_CUDA if apart else ula.ERR_INVALID_ARG), (n, heads, st, sh)

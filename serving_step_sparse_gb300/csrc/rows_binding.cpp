@@ -4,6 +4,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -33,10 +34,14 @@ void check(int code, const char *what) {
   if (code != ULA_OK) throw Failed{code, what};
 }
 
-// What the objects hold (references, borrowed for the call).
+// What the objects hold (references, borrowed for the call).  The operators record nothing for
+// autograd: a gradient that is expected would be missing without a word.
 const at::Tensor &tensor(PyObject *o) {
   need(THPVariable_Check(o), "the arguments are tensors");
-  return THPVariable_Unpack(o);
+  const at::Tensor &t = THPVariable_Unpack(o);
+  need(!t.requires_grad() || !at::GradMode::is_enabled(),
+       "no gradient is recorded: detach the tensors that require one, or call under torch.no_grad()");
+  return t;
 }
 bool given(PyObject *o) { return o != Py_None; }
 

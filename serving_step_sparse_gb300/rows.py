@@ -9,7 +9,8 @@ joins partial results over disjoint rows (``join``: ``UlaTP``'s local and remote
 Every step runs in the CUDA library through the C ABI; ``_build/_rows.so`` checks and marshals
 the arguments (in C++: a decode step makes four of these calls per layer).  Calls run on
 ``stream`` (default: the current stream of the tensors' device) and return without waiting.
-Wrong shapes, types or devices raise ValueError, errors of the C ABI ``ula.UlaError``.
+Wrong shapes, types or devices raise ValueError, errors of the C ABI ``ula.UlaError``.  Nothing
+is recorded for autograd: tensors that require a gradient are refused outside ``torch.no_grad()``.
 """
 from __future__ import annotations
 
@@ -88,7 +89,7 @@ def rotate(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *, out: torch.Ten
     pos: int32 [axes][tokens] (or [tokens]).  out: x itself (in place) or another tensor of x's
     shape and type, such as the last 64 channels of the queries that ``attend`` reads; its tokens
     and heads may not share memory.
-    inverse turns back; it is also the gradient.
+    inverse turns back; it is also the gradient (for a backward function of the caller's).
     """
     if stream is not None:
         return _on(stream, _rows.rotate, x, pos, rotary.config, out, bool(inverse))

@@ -834,3 +834,18 @@ def test_rotate_output_over_itself():
     for stride in ((256, 64, 1), (64, 384, 1)):
         out = torch.zeros(4 * 384, device="cuda").as_strided((6, 4, 64), stride)
         assert torch.equal(rows.rotate(x, pos, rot, out=out), want)
+
+
+def test_tensors_that_require_a_gradient():
+    """They are refused where a gradient would be recorded."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(17)
+    rot, _, _ = make_rotary(rng, 1, "halves")
+    x = torch.from_numpy(rng.standard_normal((5, 2, 64))).float().cuda()
+    pos = torch.from_numpy(positions(rng, 1, 5)).cuda()
+    want = rows.rotate(x, pos, rot)
+    for args in ((x.clone().requires_grad_(), None), (x, torch.zeros_like(x).requires_grad_() * 1)):
+        with pytest.raises(ValueError, match="gradient"):
+            rows.rotate(args[0], pos, rot, out=args[1])
+        with torch.no_grad():
+            assert torch.equal(rows.rotate(args[0], pos, rot, out=args[1]), want)

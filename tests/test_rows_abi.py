@@ -162,3 +162,20 @@ def test_rotate_refuses_an_output_over_itself(ula):
             code = ula.lib.ula_rows_rotate(C.byref(rot), u32(0), at, u64(0), u32(n), u32(heads), u32(0), at, u64(0),
                                            u64(0), at, u64(st), u64(sh), None)
             assert code == (ula.ERR_CUDA if apart else ula.ERR_INVALID_ARG), (n, heads, st, sh)
+
+
+def test_tensors_that_require_a_gradient_are_refused(ula):
+    from serving_step_sparse_gb300 import rows
+    rot = rows.Rotary([1.0] * 32)
+    pos, x = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 64, requires_grad=True)
+    q = torch.zeros(1, 1, 1, 576, dtype=torch.bfloat16, requires_grad=True)
+    part = torch.zeros(1, 512, dtype=torch.bfloat16, requires_grad=True)
+    calls = [lambda: rows.rotate(x, pos, rot),
+             lambda: rows.pack(torch.zeros(2, 512, requires_grad=True), x.detach(), pos, rot),
+             lambda: rows.attend(q, torch.zeros(4, 656, dtype=torch.uint8), torch.zeros(1, 1, 4, dtype=torch.int32), 1.0),
+             lambda: rows.join([part], [torch.zeros(1)])]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="device"):    # (host tensors)
+            call()

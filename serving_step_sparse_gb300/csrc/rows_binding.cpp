@@ -100,8 +100,10 @@ struct Positions {
   }
 };
 
+// The result: a new tensor, or the caller's, whose version then says that it was written.
 PyObject *wrap(PyObject *as_given, const at::Tensor &t) {
   if (!given(as_given)) return THPVariable_Wrap(t);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   Py_INCREF(as_given);
   return as_given;
 }

@@ -849,3 +849,31 @@ def test_tensors_that_require_a_gradient():
             rows.rotate(args[0], pos, rot, out=args[1])
         with torch.no_grad():
             assert torch.equal(rows.rotate(args[0], pos, rot, out=args[1]), want)
+
+
+def test_outputs_handed_in_count_as_written():
+    """Autograd notices a saved tensor that a call has changed."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(18)
+    rot, _, _ = make_rotary(rng, 1, "halves")
+    x = torch.from_numpy(rng.standard_normal((5, 2, 64))).float().cuda()
+    pos = torch.from_numpy(positions(rng, 1, 5)).cuda()
+    want = rows.rotate(x, pos, rot)
+    w = torch.ones(5, 2, 64, device="cuda", requires_grad=True)
+    y = x.clone()
+    loss = (w * y).sum()                                    # y is saved for w's gradient
+    rows.rotate(y, pos, rot, out=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    q, kv, entry, own_rows = attend_case(1, 2, 8, 20, 20, 5, own=True)
+    o, z = rows.attend(q, kv, entry, SCALE)
+    tensors = (o, z, own_rows, q, kv, entry)
+    before = [t._version for t in tensors]
+    rows.attend(q, kv, entry, SCALE, out=o, lse=z)
+    rows.join([o], [z], out=o, lse=z)
+    rows.pack(torch.zeros(1, 512, device="cuda"), torch.zeros(1, 64, device="cuda"),
+              torch.zeros(1, dtype=torch.int32, device="cuda"), rot, own_rows[0, :1])
+    assert [t._version - b for t, b in zip(tensors, before)] == [2, 2, 1, 0, 0, 0]
+    with torch.inference_mode():
+        y = x.clone()
+        assert torch.equal(rows.rotate(y, pos, rot, out=y), want)

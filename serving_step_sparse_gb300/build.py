@@ -3,10 +3,12 @@ binding of the operators on rows: csrc/rows_binding.cpp -> _build/_rows.so.
 
 Translation units compile in parallel, then link into one shared library that
 exports the C ABI declared in include/ula.h; the binding (a Python extension module
-against torch's headers) links with it.
+against torch's headers) links with it.  The library needs no torch: where that or its headers
+are missing, the library alone is built.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -28,10 +30,21 @@ def _deps():
     return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "ula.h")]
 
 
+def _torch_dir() -> str | None:
+    """Where torch is installed, if it has what the binding is built from (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    for d in (spec.submodule_search_locations or []) if spec else []:
+        if all(os.path.exists(os.path.join(d, *f)) for f in (("include", "ATen", "core", "Tensor.h"),
+                                                             ("lib", "libtorch_cuda.so"))):
+            return d
+    return None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] + ([BINDING] if _torch_dir() else [])
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -75,24 +88,30 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
         objs.append(obj)
-    binding = os.path.join(OUT_DIR, "rows_binding.o")
-    cmd = [CXX, *_binding_flags(), "-c", os.path.join(CSRC, "rows_binding.cpp"), "-o", binding]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    procs.append(("rows_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
+    binding = None
+    if _torch_dir():
+        binding = os.path.join(OUT_DIR, "rows_binding.o")
+        cmd = [CXX, *_binding_flags(), "-c", os.path.join(CSRC, "rows_binding.cpp"), "-o", binding]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append(("rows_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    else:
+        print("torch or its headers not found: the binding of the operators on rows is not built", file=sys.stderr)
+    failed = {}
     for src, p in procs:
         out, _ = p.communicate()
         if p.returncode:
-            failed.append((src, out.decode(errors="replace")))
+            failed[src] = out.decode(errors="replace")
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
+    if not failed.keys() & set(SOURCES):  # the library does not wait for the binding
+        tmp = LIB + f".{os.getpid()}.tmp"
+        subprocess.run([NVCC, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, LIB)
     if failed:
-        raise RuntimeError("compilation failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
-    tmp = LIB + f".{os.getpid()}.tmp"
-    subprocess.run([NVCC, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs], check=True)
-    os.replace(tmp, LIB)
-    _link_binding(binding)
+        raise RuntimeError("compilation failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed.items()))
+    if binding:
+        _link_binding(binding)
     return LIB
 
 

@@ -494,7 +494,8 @@ int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_a
  *   rows      : device [n_rows][656]: one layer of ula_step_group's d_out.
  *   entry_row : device int32 [n_req][n_q][k]: ula_step_group's d_entry_row.
  *   own_rows  : device; row of token i of request r at byte r * own_req_stride +
- *               i * own_tok_stride (multiples of 16), or NULL.
+ *               i * own_tok_stride (multiples of 16), or NULL.  (A stride along one
+ *               request, token or head counts for nothing.)
  *   lse       : may be NULL.
  *   workspace : device, 16-byte aligned, ula_rows_attend_workspace(...) bytes (may be
  *               NULL when that is 0).  Calls that overlap on the GPU need workspaces

@@ -58,6 +58,9 @@ ula_rotary rotary_of(PyObject *o) {
   return r;
 }
 
+// What one step along a dimension adds; a dimension of one element has no steps, whatever its stride.
+int64_t step_of(const at::Tensor &t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+
 int type_of(const at::Tensor &t) {
   switch (t.scalar_type()) {
     case at::kBFloat16: return ULA_TYPE_BF16;
@@ -138,8 +141,8 @@ PyObject *rotate(PyObject *const *a) {
   need(n <= INT32_MAX && heads <= INT32_MAX, "too many tokens or heads");
   if (x.stride(-1) != 1) x = x.contiguous();
   check(ula_rows_rotate(&rotary, a[4] == Py_True ? ULA_ROTATE_INVERSE : 0, pos.data, pos.stride, n, heads, type,
-                        x.data_ptr(), x.stride(0), three ? x.stride(1) : 0, out.data_ptr(), out.stride(0),
-                        three ? out.stride(1) : 0, on.stream()),
+                        x.data_ptr(), step_of(x, 0), three ? step_of(x, 1) : 0, out.data_ptr(), step_of(out, 0),
+                        three ? step_of(out, 1) : 0, on.stream()),
         "ula_rows_rotate");
   return wrap(a[3], out);
 }
@@ -164,8 +167,8 @@ PyObject *pack(PyObject *const *a) {
   need(n <= INT32_MAX, "too many tokens");
   if (latent.stride(1) != 1) latent = latent.contiguous();
   if (rope.stride(1) != 1) rope = rope.contiguous();
-  check(ula_rows_pack(&rotary, pos.data, pos.stride, n, type, latent.data_ptr(), latent.stride(0), rope.data_ptr(),
-                      rope.stride(0), rows.data_ptr(), n > 1 ? rows.stride(0) : kRow, on.stream()),
+  check(ula_rows_pack(&rotary, pos.data, pos.stride, n, type, latent.data_ptr(), step_of(latent, 0), rope.data_ptr(),
+                      step_of(rope, 0), rows.data_ptr(), n > 1 ? rows.stride(0) : kRow, on.stream()),
         "ula_rows_pack");
   return wrap(a[4], rows);
 }
@@ -190,7 +193,7 @@ PyObject *attend(PyObject *const *a) {
   need(R <= INT32_MAX && Q <= INT32_MAX && H <= INT32_MAX && K <= INT32_MAX && rows.size(0) <= INT32_MAX,
        "too many requests, query tokens, heads, entries or rows");
   if (!entry.is_contiguous()) entry = entry.contiguous();
-  if (q.stride(3) != 1 || q.stride(0) % 8 || q.stride(1) % 8 || q.stride(2) % 8 ||
+  if (q.stride(3) != 1 || step_of(q, 0) % 8 || step_of(q, 1) % 8 || step_of(q, 2) % 8 ||
       reinterpret_cast<uintptr_t>(q.data_ptr()) % 16)
     q = q.clone(at::MemoryFormat::Contiguous);
   ula_attend_args args{};
@@ -201,7 +204,7 @@ PyObject *attend(PyObject *const *a) {
          "own_rows is uint8 [requests][query tokens][656]");
     on.same(own);
     args.own_rows = own.data_ptr();
-    args.own_req_stride = own.stride(0), args.own_tok_stride = own.stride(1);
+    args.own_req_stride = step_of(own, 0), args.own_tok_stride = step_of(own, 1);
   }
   const at::Tensor out = given(a[5]) ? tensor(a[5]) : on.empty({R, Q, H, kLatent}, at::kBFloat16);
   if (given(a[5])) {
@@ -224,7 +227,7 @@ PyObject *attend(PyObject *const *a) {
     args.workspace = space.data_ptr();
   }
   args.q = q.data_ptr();
-  args.q_req_stride = q.stride(0), args.q_tok_stride = q.stride(1), args.q_head_stride = q.stride(2);
+  args.q_req_stride = step_of(q, 0), args.q_tok_stride = step_of(q, 1), args.q_head_stride = step_of(q, 2);
   args.rows = rows.data_ptr(), args.n_rows = rows.size(0);
   args.entry_row = entry.data_ptr<int32_t>();
   args.out = out.data_ptr(), args.lse = lse.data_ptr<float>();

@@ -1059,7 +1059,10 @@ extern "C" uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint
 
 extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   if (!args) return ULA_ERR_INVALID_ARG;
-  const ula_attend_args &a = *args;
+  ula_attend_args a = *args;
+  if (a.n_req == 1) a.q_req_stride = a.own_req_stride = 0;  // (no steps: whatever they are)
+  if (a.n_q == 1) a.q_tok_stride = a.own_tok_stride = 0;
+  if (a.heads == 1) a.q_head_stride = 0;
   if (a.n_req == 0 || a.n_q == 0 || a.heads == 0) return ULA_OK;
   if (!a.q || !a.out || (a.k && (!a.entry_row || (!a.rows && a.n_rows)))) return ULA_ERR_INVALID_ARG;
   if (!aligned(a.q, 16) || !aligned(a.rows, 16) || !aligned(a.own_rows, 16) || !aligned(a.out, 16) ||

@@ -877,3 +877,29 @@ def test_outputs_handed_in_count_as_written():
     with torch.inference_mode():
         y = x.clone()
         assert torch.equal(rows.rotate(y, pos, rot, out=y), want)
+
+
+def test_strides_of_single_elements():
+    """The stride of a dimension of one element says nothing: no reason to refuse a call."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(23)
+
+    def odd(t, dims):
+        return t.as_strided(t.shape, [3 if d in dims else s for d, s in enumerate(t.stride())])
+
+    q, kv, entry, own_rows = attend_case(1, 3, 20, 40, 30, 2, own=True)
+    want = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    got = rows.attend(odd(q, [0]), kv, odd(entry, [0]), SCALE, own_rows=odd(own_rows, [0]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q, kv, entry, own_rows = attend_case(3, 1, 1, 40, 30, 2, own=True)
+    want = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    got = rows.attend(odd(q, [1, 2]), kv, odd(entry, [1]), SCALE, own_rows=odd(own_rows, [1]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    rot, _, _ = make_rotary(rng, 1, "halves")
+    x = torch.from_numpy(rng.standard_normal((1, 4, 64))).to(torch.bfloat16).cuda()
+    pos = torch.tensor([[5]], dtype=torch.int32, device="cuda")
+    want = rows.rotate(x, pos, rot)
+    assert torch.equal(rows.rotate(odd(x, [0]), pos, rot, out=odd(torch.zeros_like(x), [0])), want)
+    latent, rope = x.flatten()[None, :].repeat(1, 2)[:, :512], x[:, 0]
+    want = rows.pack(latent, rope, pos, rot)
+    assert torch.equal(rows.pack(odd(latent, [0]), odd(rope, [0]), pos, rot, odd(torch.zeros_like(want), [0])), want)

@@ -44,6 +44,13 @@ __device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos) 
   return make_float2(c, s);
 }
 
+// A pair turned.  Written out, so that the same operations are rounded in every kernel: left to the
+// compiler, which product is fused differed from one to the other.
+__device__ __forceinline__ void turn(float a, float b, float c, float s, float &oa, float &ob) {
+  oa = fmaf(-b, s, __fmul_rn(a, c));
+  ob = fmaf(b, c, __fmul_rn(a, s));
+}
+
 // Every kernel here may be launched while the one before it on the stream ends, and lets the
 // next one do so: it waits before it touches memory.
 __device__ __forceinline__ void after_previous() {
@@ -141,20 +148,20 @@ __global__ void __launch_bounds__(256) k_rotate_vec(const __grid_constant__ Rota
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
         const float4 cs = tb[(c * V + k) / 2];
-        oa[k] = a[k] * cs.x - b[k] * cs.y, ob[k] = a[k] * cs.y + b[k] * cs.x;
-        oa[k + 1] = a[k + 1] * cs.z - b[k + 1] * cs.w, ob[k + 1] = a[k + 1] * cs.w + b[k + 1] * cs.z;
+        turn(a[k], b[k], cs.x, cs.y, oa[k], ob[k]);
+        turn(a[k + 1], b[k + 1], cs.z, cs.w, oa[k + 1], ob[k + 1]);
       }
     } else {  // pair j: channels 2j, 2j + 1
-      auto turn = [&](const float (&v)[V], float (&o)[V], uint32_t pair0) {
+      auto turn_pairs = [&](const float (&v)[V], float (&o)[V], uint32_t pair0) {
 #pragma unroll
         for (int k = 0; k < V; k += 4) {
           const float4 cs = tb[(pair0 + k / 2) / 2];
-          o[k] = v[k] * cs.x - v[k + 1] * cs.y, o[k + 1] = v[k] * cs.y + v[k + 1] * cs.x;
-          o[k + 2] = v[k + 2] * cs.z - v[k + 3] * cs.w, o[k + 3] = v[k + 2] * cs.w + v[k + 3] * cs.z;
+          turn(v[k], v[k + 1], cs.x, cs.y, o[k], o[k + 1]);
+          turn(v[k + 2], v[k + 3], cs.z, cs.w, o[k + 2], o[k + 3]);
         }
       };
-      turn(a, oa, c * (V / 2));
-      turn(b, ob, kPairs / 2 + c * (V / 2));
+      turn_pairs(a, oa, c * (V / 2));
+      turn_pairs(b, ob, kPairs / 2 + c * (V / 2));
     }
     T *o = (T *)p.out + (t0 + tok) * p.ot + (r - tok * p.heads) * p.oh + c * V;
     *reinterpret_cast<uint4 *>(o) = Vec<T>::close(oa);
@@ -174,9 +181,10 @@ __global__ void __launch_bounds__(256) k_rotate_any(const __grid_constant__ Rota
   T *o = (T *)p.out + t * p.ot + h * p.oh;
   const float2 cs = turn_of(p.rot.step[j], p.pos[p.rot.axis[j] * p.pos_axis_stride + t]);
   const uint32_t ia = kHalves ? j : 2 * j, ib = kHalves ? j + kPairs : 2 * j + 1;
-  const float a = to_f(x[ia]), b = to_f(x[ib]), s = cs.y * p.sign;
-  o[ia] = from_f<T>(a * cs.x - b * s);
-  o[ib] = from_f<T>(a * s + b * cs.x);
+  float oa, ob;
+  turn(to_f(x[ia]), to_f(x[ib]), cs.x, cs.y * p.sign, oa, ob);
+  o[ia] = from_f<T>(oa);
+  o[ib] = from_f<T>(ob);
 }
 
 // ---------------------------------------------------------------- pack
@@ -268,7 +276,8 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams
     if ((l & 7) == 0) reinterpret_cast<float *>(row + ULA_ROW_LATENT)[l >> 3] = scale;
     const float2 cs = turn_of(step, pos);
     __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(row + ULA_ROW_LATENT + 16);
-    const float oa = a * cs.x - b * cs.y, ob = a * cs.y + b * cs.x;
+    float oa, ob;
+    turn(a, b, cs.x, cs.y, oa, ob);
     if (kHalves) {
       o[ia] = __float2bfloat16_rn(oa);
       o[ib] = __float2bfloat16_rn(ob);

@@ -903,3 +903,24 @@ def test_strides_of_single_elements():
     latent, rope = x.flatten()[None, :].repeat(1, 2)[:, :512], x[:, 0]
     want = rows.pack(latent, rope, pos, rot)
     assert torch.equal(rows.pack(odd(latent, [0]), odd(rope, [0]), pos, rot, odd(torch.zeros_like(want), [0])), want)
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rotate_same_bits_at_any_alignment(dtype, pairing):
+    """What an output holds does not depend on how its memory lies, nor on the kernel that
+    this chooses; a row's rope channels are the rotation's."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(29)
+    rot, _, _ = make_rotary(rng, 3, pairing)
+    x = torch.from_numpy(rng.standard_normal((501, 9, 64))).to(DT[dtype]).cuda()
+    pos = torch.from_numpy(positions(rng, 3, 501)).cuda()
+    for inverse in (False, True):
+        want = rows.rotate(x, pos, rot, inverse=inverse)
+        for at in (0, 1, 2, 8):
+            odd = torch.zeros(501, 9, 73, dtype=DT[dtype], device="cuda")[..., at:at + 64]
+            assert torch.equal(rows.rotate(x, pos, rot, out=odd, inverse=inverse), want)
+    packed = rows.pack(torch.zeros(501, 512, dtype=DT[dtype], device="cuda"), x[:, 0], pos, rot)
+    if dtype != "f16":                                      # (rows hold bf16, rounded once)
+        assert torch.equal(packed[:, 528:].contiguous().view(torch.bfloat16),
+                           rows.rotate(x[:, 0], pos, rot).to(torch.bfloat16))

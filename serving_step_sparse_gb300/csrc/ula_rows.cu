@@ -357,6 +357,12 @@ cudaError_t launch(void (*kernel)(P), uint64_t grid, uint32_t smem, cudaStream_t
 uint32_t type_size(uint32_t dtype) { return dtype == ULA_TYPE_F32 ? 4u : 2u; }
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+uint32_t sm_count() {
+  int dev = 0, n = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0
+             ? (uint32_t)n : 1u;
+}
+
 // Whether two of the rows of 64 channels at i * si + j * sj (i < ni, j < nj) share elements.
 bool overlap(uint64_t ni, uint64_t si, uint64_t nj, uint64_t sj) {
   constexpr uint64_t kRow = ULA_ROW_ROPE;
@@ -374,15 +380,15 @@ bool overlap(uint64_t ni, uint64_t si, uint64_t nj, uint64_t sj) {
   return false;
 }
 
-// Two rows per thread (4 loads in flight) where there are blocks for every SM several times
-// over: 4,096 tokens x 128 heads of bf16, 26.0 us (5.2 TB/s) against 29.3 with one and 27.8
-// with four.  Fewer rows are spread over more blocks of one row per thread, and so are
-// tokens of few heads, whose sines would need more shared memory.
+// Two rows per thread (4 loads in flight) where that leaves 4 blocks at least for every SM: 4,096
+// tokens x 128 heads of bf16, 26.0 us (5.2 TB/s) against 29.3 with one and 27.8 with four.  Fewer
+// rows are spread over more blocks of one row per thread, and so are tokens of few heads, whose
+// sines would need more shared memory.
 template <typename T, bool kHalves>
 cudaError_t launch_rotate_vec(const RotateParams &p, cudaStream_t st) {
   const uint64_t all = (uint64_t)p.n * p.heads;
   constexpr uint32_t step = 256 / (32 / Vec<T>::n);
-  const bool many = all >= 2ull * step * 608 && p.heads >= 8;
+  const bool many = p.heads >= 8 && all >= 2ull * step * 4 * sm_count();
   const uint32_t rows = step * (many ? 2 : 1);
   const uint32_t tokens = (rows - 1) / p.heads + 2;  // at most, whatever the first row
   return launch(many ? k_rotate_vec<T, kHalves, 2> : k_rotate_vec<T, kHalves, 1>, (all + rows - 1) / rows,
@@ -402,7 +408,7 @@ cudaError_t launch_pack(const PackParams &p, bool halves, bool vec, cudaStream_t
                   : (vec ? k_pack<T, false, true> : k_pack<T, false, false>);
   // a warp takes more than one token once every SM has its 4 resident blocks (131,072 tokens
   // of bf16: 42.6 us, 5.6 TB/s, with 4; 53.6 / 46.3 / 47.5 / 43.5 with 2 / 3 / 6 / 8)
-  const uint64_t blocks = ((uint64_t)p.n + 7) / 8, most = 4ull * 152;
+  const uint64_t blocks = ((uint64_t)p.n + 7) / 8, most = 4ull * sm_count();
   return launch(k, blocks < most ? blocks : most, 0, st, p);
 }
 

@@ -924,3 +924,74 @@ def test_rotate_same_bits_at_any_alignment(dtype, pairing):
     if dtype != "f16":                                      # (rows hold bf16, rounded once)
         assert torch.equal(packed[:, 528:].contiguous().view(torch.bfloat16),
                            rows.rotate(x[:, 0], pos, rot).to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------------------- many rows
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("heads,more", [(8, 1), (37, 5), (129, 700), (3, 0), (1, 3)])
+def test_rotate_many(heads, more, dtype, pairing):
+    """Prompt sizes: from 2 x 4 blocks' rows for every SM on, threads take two rows each (tokens
+    of fewer than 8 heads excepted); the last block has a remainder."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(heads + more)
+    step = 32 if dtype == "f32" else 64                     # rows a block takes at once
+    n = -(-8 * step * sms() // heads) + more
+    rot, freq, axis = make_rotary(rng, 2, pairing)
+    x = torch.from_numpy(rng.standard_normal((n, heads, 64), dtype=np.float32)).to(DT[dtype]).cuda()
+    pos = positions(rng, 2, n)
+    pos_d = torch.from_numpy(pos).cuda()
+    out = rows.rotate(x, pos_d, rot)
+    check_turned(out, x.double().cpu(), pos, freq, axis, pairing, dtype)
+    back = rows.rotate(x, pos_d, rot, inverse=True)
+    check_turned(back, x.double().cpu(), pos, freq, axis, pairing, dtype, sign=-1.0)
+    wide = torch.full((n, heads, 80), 7.0, dtype=DT[dtype], device="cuda")
+    wide[..., 8:72] = x
+    rows.rotate(wide[..., 8:72], pos_d, rot, out=wide[..., 8:72])                  # in place, strided
+    assert torch.equal(wide[..., 8:72], out)
+    assert (wide[..., :8] == 7).all() and (wide[..., 72:] == 7).all()
+    odd = torch.zeros(n, heads, 65, dtype=DT[dtype], device="cuda")                # unaligned rows
+    assert torch.equal(rows.rotate(x, pos_d, rot, out=odd[..., 1:]), out)
+
+
+def check_packed(got, latent, rope, pos, freq, axis, pairing):
+    """As test_pack has it."""
+    n = latent.shape[0]
+    b = got.cpu().numpy()
+    v = latent.double().cpu().numpy().reshape(n, 4, 128)
+    scale = np.ascontiguousarray(b[:, 512:528]).view(np.float32).astype(np.float64)
+    want = np.maximum(np.abs(v).max(-1) / 448, 2.0 ** -126)
+    assert (np.abs(scale - want) <= 2.0 ** -23 * want).all()
+    codes = E4M3[b[:, :512]].reshape(n, 4, 128)
+    y = v / scale[..., None]
+    spacing = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -6))) - 3)
+    assert (np.abs(codes - y) <= spacing / 2 + 2.0 ** -21 * np.abs(y)).all()
+    got_rope = torch.from_numpy(np.ascontiguousarray(b[:, 528:])).view(torch.bfloat16)
+    check_turned(got_rope, rope.double().cpu(), pos, freq, axis, pairing, "bf16")
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rounds,more", [(1, 0), (1, 1), (2, -3), (2, 270), (4, 9)])
+def test_pack_many(rounds, more, dtype, pairing):
+    """Document sizes: a warp takes more than one token past 4 blocks of 8 warps for every SM."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(rounds * 17 + more)
+    n = rounds * 32 * sms() + more
+    rot, freq, axis = make_rotary(rng, 3, pairing)
+    x = rng.standard_normal((n, 576), dtype=np.float32) * np.exp(rng.standard_normal((n, 1), dtype=np.float32))
+    pos = positions(rng, 3, n)
+    pos_d = torch.from_numpy(pos).cuda()
+    both = torch.from_numpy(x).to(DT[dtype]).cuda()
+    dest = torch.full((n, 2, 656), 0xA5, dtype=torch.uint8, device="cuda")
+    got = rows.pack(both[:, :512], both[:, 512:], pos_d, rot, dest[:, 1])
+    assert (dest[:, 0] == 0xA5).all()
+    check_packed(got, both[:, :512], both[:, 512:], pos, freq, axis, pairing)
+    odd = torch.zeros(n, 577, dtype=DT[dtype], device="cuda")                      # unaligned latents
+    odd[:, 1:] = both
+    assert torch.equal(rows.pack(odd[:, 1:513], odd[:, 513:], pos_d, rot), got)

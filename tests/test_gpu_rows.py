@@ -995,3 +995,107 @@ def test_pack_many(rounds, more, dtype, pairing):
     odd = torch.zeros(n, 577, dtype=DT[dtype], device="cuda")                      # unaligned latents
     odd[:, 1:] = both
     assert torch.equal(rows.pack(odd[:, 1:513], odd[:, 513:], pos_d, rot), got)
+
+
+# ------------------------------------------------------------------------------- with the cache
+
+@pytest.mark.parametrize("R,Q,H,K", [(1, 129, 8, 40), (2, 300, 20, 7), (1, 200, 64, 0), (3, 140, 3, 120), (1, 260, 128, 200)])
+def test_attend_own_rows_over_tiles(R, Q, H, K):
+    """A chunk of a prompt: more query tokens than a tile has rows, each of which sees the own
+    rows up to itself, behind lists that end inside a tile."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own_rows = attend_case(R, Q, H, K, 200, R + Q + H, pads=0.1, own=True)
+    got = rows.attend(q, kv, entry, SCALE, own_rows=own_rows)
+    check_attend(got, attend64(q, kv, entry, SCALE, own_rows))
+    bad = own_rows.clone()                                  # a token's row is seen by later ones only
+    bad[0, Q // 2, 512:528] = torch.tensor([math.nan] * 4).view(torch.uint8).cuda()
+    out, lse = rows.attend(q, kv, entry, SCALE, own_rows=bad)
+    assert torch.equal(out[0, :Q // 2], got[0][0, :Q // 2]) and torch.equal(lse[0, :Q // 2], got[1][0, :Q // 2])
+    assert torch.isnan(out[0, Q // 2:]).all() and torch.isnan(lse[0, Q // 2:]).all()
+    rows.sync()
+
+
+def layer_rows(n, layers, rng):
+    """[n][layers][656]: rows for the cache, one group."""
+    return random_rows(n * layers, rng).view(n, layers, 656)
+
+
+def test_attend_after_a_step_with_pads():
+    """Selections with pads, as a request shorter than the top-k has them, through step_group."""
+    from serving_step_sparse_gb300 import rows, ula
+    from serving_step_sparse_gb300.cache import UlaCache
+    rng = np.random.default_rng(41)
+    R, Q, K, L, H, n = 3, 2, 96, 2, 20, 700
+    store = layer_rows(n, L, rng)
+    cache = UlaCache(row_bytes=656, layers_per_group=[L], gpu_slots=n // 2, host_slots=n, ring_buckets=4,
+                     max_logical=n, max_entries=R * Q * K)
+    try:
+        assert cache.alloc(n, store) == 0
+        entry_row = torch.empty(R * Q * K, dtype=torch.int32, device="cuda")
+        req_off = torch.empty(R + 1, dtype=torch.int32, device="cuda")
+        for step in range(3):
+            sel = np.stack([[rng.choice(200, K, replace=False) + 230 * r for _ in range(Q)] for r in range(R)])
+            sel[0, :, 10 + step:] = -1                      # a short request: pads behind
+            sel[1][rng.random((Q, K)) < 0.4] = -1           # pads anywhere
+            sel[2, 1] = -1                                  # a token that selects nothing
+            sel = torch.from_numpy(sel.astype(np.int32)).cuda()
+            assert int(sel.min()) == -1 and ula.ADDR_PAD == 2 ** 32 - 1
+            out = cache.out_buffer(0, R * Q * K)
+            out.fill_(0xFF)                                 # (NaN where nothing is gathered)
+            cache.step_group(0, sel, out, entry_row, req_off)
+            q = attend_case(R, Q, H, 1, 1, 400 + step)[0]
+            for j in range(L):
+                got = rows.attend(q, out[j], entry_row.view(R, Q, K), SCALE)
+                check_attend(got, attend64(q, store[:, j].contiguous(), sel, SCALE))
+        cache.sync()
+        rows.sync()
+    finally:
+        cache.close()
+
+
+@pytest.mark.parametrize("parts", [2, 4])
+def test_attend_after_a_tp_step(parts):
+    """What a UlaTP step leaves each rank, its local rows and the remote ones with an entry list
+    for each, attended to separately and joined, against all rows at once."""
+    from serving_step_sparse_gb300 import rows
+    from serving_step_sparse_gb300.cache import UlaTP
+    rng = np.random.default_rng(43 + parts)
+    R, Q, K, L, H, n = 2, 3, 150, 2, 24, 2400
+    E = R * Q * K
+    store = layer_rows(n, L, rng)
+    tp = UlaTP(row_bytes=656, layers_per_group=[L], parts=parts, gpu_slots=3 * n // (4 * parts), host_slots=n,
+               ring_buckets=4, max_logical=n, max_entries=E, buffer_slots=2 * E)
+    try:
+        assert tp.alloc(n, store) == 0
+        tp.sync()
+        of_rank = lambda size: [torch.empty(size, dtype=torch.int32, device="cuda") for _ in range(parts)]
+        for step in range(2):
+            # recent tokens of one partition only (nothing remote for one rank), pads, an empty token
+            sel = np.stack([[rng.choice(1200, K, replace=False) + 1200 * r for _ in range(Q)] for r in range(R)])
+            sel[0, 0] = parts * rng.choice(n // parts, K, replace=False)
+            sel[1, 1, 40:] = -1
+            sel[1, 2] = -1
+            sel = torch.from_numpy(sel.astype(np.int32)).cuda()
+            local, remote = ([tp.out_buffer(0, E).fill_(0xFF) for _ in range(parts)] for _ in range(2))
+            local_row, remote_row, local_off, remote_off = of_rank(E), of_rank(E), of_rank(R + 1), of_rank(R + 1)
+            tp.step_group(0, sel, local, remote, local_row, local_off, remote_row, remote_off)
+            tp.sync()
+            q = attend_case(R, Q, H, 1, 1, 500 + step)[0]
+            for j in range(L):
+                out, lse, slack, zslack = attend64(q, store[:, j].contiguous(), sel, SCALE)
+                none = np.isneginf(lse)
+                assert none.any() and not none.all()
+                for r in range(parts):
+                    a = rows.attend(q, local[r][j], local_row[r].view(R, Q, K), SCALE)
+                    b = rows.attend(q, remote[r][j], remote_row[r].view(R, Q, K), SCALE)
+                    o, z = rows.join([a[0], b[0]], [a[1], b[1]])
+                    o, z = o.double().cpu().numpy(), z.double().cpu().numpy()
+                    assert np.array_equal(np.isneginf(z), none) and (o[none] == 0).all()
+                    assert (np.abs(z[~none] - lse[~none]) <= (zslack + 2.0 ** -19 * (1 + np.abs(lse)))[~none]).all()
+                    # each part was rounded to bf16 as well
+                    tol = 2.0 ** -8 * 1.01 * np.abs(out) + (2.0 ** -8 + 2.0 ** -8 + np.expm1(2 * zslack[..., None])) * slack
+                    assert (np.abs(o - out) <= tol)[~none].all()
+        tp.sync()
+        rows.sync()
+    finally:
+        tp.close()

@@ -1099,3 +1099,41 @@ def test_attend_after_a_tp_step(parts):
         rows.sync()
     finally:
         tp.close()
+
+
+@pytest.mark.parametrize("R,H,K", [(2, 20, 700), (12, 16, 1024), (160, 64, 150)])
+def test_operators_in_a_graph(R, H, K):
+    """A layer's calls captured once and replayed on new inputs give what the calls give."""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(R)
+    rot, _, _ = make_rotary(rng, 1, "halves")
+    pos = torch.arange(R, dtype=torch.int32, device="cuda")
+    cases = [attend_case(R, 1, H, K, 400, 70 + s, pads=0.1) for s in range(3)]
+    new = [torch.from_numpy(rng.standard_normal((3, R, 576))).to(torch.bfloat16).cuda()[s] for s in range(3)]
+
+    def layer(q, kv, entry, x):
+        turned = q.clone()
+        rope = turned.view(R, H, 576)[..., 512:]
+        rows.rotate(rope, pos, rot, out=rope)
+        own = rows.pack(x[:, :512], x[:, 512:], pos, rot).view(R, 1, 656)
+        a = rows.attend(turned, kv, entry, SCALE, own_rows=own)
+        b = rows.attend(turned, kv, entry.flip(-1)[..., :K // 3].contiguous(), SCALE)
+        return rows.join([a[0], b[0]], [a[1], b[1]])
+
+    want = [layer(*c[:3], x) for c, x in zip(cases, new)]
+    held = [t.clone() for t in (*cases[0][:3], new[0])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(*held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer(*held)
+    for s in (1, 2, 0, 1):
+        for h, t in zip(held, (*cases[s][:3], new[s])):
+            h.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[s][0]) and torch.equal(got[1], want[s][1])
+    rows.sync()

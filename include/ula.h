@@ -445,8 +445,8 @@ typedef struct ula_rotary {
  * t = pos[axis[j]][token] * freq[j], pair (a, b) becomes (a cos t - b sin t,
  * a sin t + b cos t); ULA_ROTATE_INVERSE turns by -t (which is also the gradient:
  * the rotation's transpose).  The angle is taken modulo one turn in 64-bit fixed
- * point, so it is as exact at position 2^30 as at 1; the pair is turned in fp32 and
- * rounded once.
+ * point and off by at most 1e-7 rad + |pos * freq| * 1.5e-16 (1.6e-7 of that at position
+ * 2^30 and freq 1); the pair is turned in fp32 and rounded once.
  *   d_pos : device int32, axis a of token t at d_pos[a * pos_axis_stride + t].
  *   d_x   : device, channel c of head h of token t at
  *           d_x[t * x_token_stride + h * x_head_stride + c] (strides in elements).

@@ -73,8 +73,9 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // whatever time it is given, so a wait that is never met ends after 1.05 s, and any wait that these
 // kernels can meet is shorter than a tenth of a millisecond. The loop is written out because its
 // size matters: the compute warps pass through some 15 waits a tile, their code is longer than
-// the instruction caches nearest to them, and with a clock read and two ways out in each wait
-// the step of 96 tokens, 128 heads, 2,048 rows took 169.4 us, with this form 159.4.
+// the instruction caches nearest to them: with a clock read and two ways out in each wait the step
+// of 96 tokens, 128 heads, 2,051 rows took 6 % more when this form came in, and with a limit that is
+// a kernel argument it takes 125.0 us instead of 120.5.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -328,8 +329,9 @@ struct Joined {
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
 // direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads
-// 120 us (0.46 PFLOP/s), 64 heads 73 us, and 15.5 us for 8 tokens of 64 heads.  (16 compute
-// warps of half the registers took 12, 5 and 0.4 us more than 8, before the loads were spread.)
+// 120 us (0.46 PFLOP/s), 64 heads 73 us, and 15.5 us for 8 tokens of 64 heads.  (When they were
+// compared, before the loads were spread, 16 compute warps of half the registers took 12, 5 and
+// 0.4 us more than 8.)
 //
 // Shared memory holds one tile, and the tile's own parts make room for P (P_b = p * s_b,
 // 16 KB): P_0 takes the rope's place; after O_0 has read block 0's codes, P_1 and P_3 take
@@ -539,8 +541,8 @@ k_attend(const __grid_constant__ AttendParams p) {
           ok = warp_wait(bar(kBarFull + 1), par);
           if (!(ok = ok && warp_wait(bar(kBarFull + 2), par))) break;
           place_rows(prev);
-          // into L2 ahead of the loads: 128 heads 125.0 us instead of 127.5.  (Not for a block's first
-          // tile, whose loads follow at once: one request 10.8 us instead of 9.6.)
+          // into L2 ahead of the loads: 2 % of 128 heads' time when it came in.  (Not for a block's first
+          // tile, whose loads follow at once: that took 1.2 us of one request's 9.6 more.)
           const uint64_t *ahead = reinterpret_cast<const uint64_t *>(sm + L::place) + prev * kTile + r0;
 #pragma unroll
           for (uint32_t j = 0; j < 2; ++j)
@@ -580,8 +582,8 @@ k_attend(const __grid_constant__ AttendParams p) {
     const uint32_t block1 = second ? 2 : 1, block2 = second ? 3 : 0;
     // Half of this thread's codes of one block, of tile n's rows.  The next tile's come in four such
     // pieces of 16 KB, apart from each other: more than some 28 KB of loads in flight stop the
-    // load/store unit for the shared memory's accesses as well (128 heads, 2,048 rows: 125 us; 135
-    // in pieces of 24, 24 and 16 KB, 141 in one of 64).
+    // load/store unit for the shared memory's accesses as well (128 heads, 2,051 rows, when it came in:
+    // 125 us; 135 in pieces of 24, 24 and 16 KB, 141 in one of 64).
     auto fetch = [&](uint4 (&raw)[kSlots], uint32_t n, uint32_t block, uint32_t half) {
       const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile;
 #pragma unroll
@@ -640,7 +642,7 @@ k_attend(const __grid_constant__ AttendParams p) {
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
       // ---- widen the tile, block by block as there is room (in a loop, since two copies of this
-      // code fall out of the instruction caches: 158.5 us instead of 154.1)
+      // code fall out of the instruction caches: 3 % more)
 #pragma unroll 1
       for (uint32_t half = 0; half < 2; ++half) {
         if (n && !(ok = warp_wait(bar(kBarPV + (half ? 3 : block1)), par ^ 1))) break;
@@ -1002,9 +1004,9 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   pl->keys = k + (own ? n_q : 0);
   pl->tiles = pl->keys ? (pl->keys + kTile - 1) / kTile : 1;
   // Heads per item: the fewest that hold them all, up to 64 (TMEM's columns).  The rows are widened
-  // once an item, so heads are not split further: 96 tokens x 2,048 rows, 64 heads, 89 us with 64
-  // and 115 with 32.  Rounding 32 heads up to 64 costs 10.7 -> 13.1 us (one token, 256 rows), 16 up
-  // to 32 73 -> 78 us (128 tokens, 2,048 rows).
+  // once an item, so heads are not split further: 96 tokens x 2,051 rows, 64 heads, 71.6 us with 64
+  // and 95.7 with 32.  Rounding 32 heads up to 64 costs 9.4 -> 11.7 us (one token, 256 rows), 16 up
+  // to 32 63.7 -> 67.9 us (128 tokens, 2,048 rows).
   pl->nh = heads <= 16 ? 16 : heads <= 32 ? 32 : 64;
   pl->head_tiles = (heads + pl->nh - 1) / pl->nh;
   const uint64_t items = tokens * pl->head_tiles;
@@ -1017,10 +1019,12 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   // by its blocks alone, where the second kernel's is by all SMs: it takes blocks enough that the
   // trip of all partial results through L2 is what counts, and fewer blocks for its wider results
   // (us with clusters, without; heads, tiles, query tokens):
-  //   32 heads  7 x 5: 10.3, 10.2    7 x 15: 10.3, 12.3    2 x 19: 10.2, 10.3    2 x 57: 10.3, 12.3
-  //   64 heads  4 x 1: 14.3, 12.3    4 x 28: 14.4, 16.4    8 x 14: 16.4, 14.4    2 x 76: 16.2, 20.8
+  //   32 heads  7 x 5: 10.9, 10.3    7 x 15: 11.4, 11.2    2 x 19: 10.6, 9.9    2 x 57: 11.0, 11.1
+  //             4 x 28: 10.9, 11.9
+  //   64 heads  4 x 1: 14.2, 12.7    4 x 28: 15.2, 15.1    8 x 14: 16.0, 15.6    2 x 76: 15.7, 17.3
+  //   16 heads  8 x 15: 9.3, 10.1    2 x 57: 9.3, 10.1
   // Clusters of more than 2 cannot use every SM (a cluster lies within one group of SMs), and those
-  // that find no place run behind the others: 32 heads 4 x 28: 10.3, 12.3, but 4 x 38: 20.5, 12.3.
+  // that find no place run behind the others: 32 heads 4 x 38: 20.4, 12.0.
   pl->cluster = 1;
   if (pl->tiles > 1 && pl->tiles <= (pl->nh == 64 ? kMostCluster / 2 : kMostCluster) &&
       total >= (unsigned)sms * 2 / 5 && total <= (unsigned)(pl->tiles == 2 ? sms : sms * 3 / 4)) {
@@ -1032,8 +1036,8 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   }
   pl->blocks = total == 0 ? 1 : total < (unsigned)sms ? (uint32_t)total : (uint32_t)sms;
   if (total / pl->blocks > 0x7fffffffull) return false;
-  // Whole items first: their results need no join (192 items of 17 tiles: 120.0 us, with even
-  // shares of all tiles 125.0).
+  // Whole items first: their results need no join (192 items of 17 tiles: 120 us, with even shares
+  // of all tiles 125).
   pl->rounds = (uint32_t)(items / pl->blocks);
   pl->rest = (items - (uint64_t)pl->rounds * pl->blocks) * pl->tiles;
   pl->sharers = pl->rest && pl->rest < pl->blocks ? (uint32_t)pl->rest : pl->blocks;
@@ -1086,13 +1090,6 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
   cudaError_t e = pl.nh == 16 ? launch_attend<16>(p, st) : pl.nh == 32 ? launch_attend<32>(p, st) : launch_attend<64>(p, st);
   if (e != cudaSuccess) return ULA_ERR_CUDA;
   if (pl.parts) {
-    // Heads per block of the join: 4 share the work on a block's place once every SM has several
-    // blocks (96 tokens x 2,048 rows, 128 heads, both kernels 144.5 us; 146.3 with 2), and 2 keep
-    // the loads of few items on more SMs (8 tokens, 64 heads: 17.6 us; 21.2 with 4).
-    // Parts in flight per thread: 2 where an item has no more; else 16 while there is a place for
-    // every block at that many registers (8 tokens, 64 heads: 15.6 us; 17.6 with 8), then 8 (20
-    // tokens: 24.7 us; 26.7 with 16. 96 tokens of 128 heads, two parts: 141.1 us with 2, 142.8
-    // with 8, 148.3 with 16).
     // Heads per block of the join: 4 share the work on a block's place once every SM has several
     // blocks (96 tokens x 2,051 rows, 64 heads, both kernels: 72.9 us; 73.9 with 2), and 2 keep the
     // loads of few items on more SMs (8 tokens: 17.6 us; 21.2 with 4).

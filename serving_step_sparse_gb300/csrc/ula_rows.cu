@@ -12,9 +12,10 @@ namespace {
 constexpr uint32_t kPairs = ULA_ROPE_PAIRS;
 
 // A rotary as the kernels take it: each pair's turns per position in 64-bit fixed point
-// (2^64 = one turn).  position * step modulo 2^64 is then the angle's fraction of a turn
-// in exact integer arithmetic, however far the position (an fp32 product of position and
-// frequency is off by up to 0.004 rad at position 10^5).
+// (2^64 = one turn), from a quotient in double.  position * step modulo 2^64 is then the angle's
+// fraction of a turn in integer arithmetic: off by position * frequency * 1.5e-16 rad, the
+// quotient's roundings (an fp32 product of position and frequency is off by up to 0.004 rad at
+// position 10^5).
 struct RotaryDev {
   unsigned long long step[kPairs];
   uint8_t axis[kPairs];
@@ -35,7 +36,8 @@ bool rotary_to_dev(const ula_rotary *r, RotaryDev *out) {
 }
 
 // (cos, sin) of a pair (of its step) at a position; the top 32 bits of the phase are the signed
-// fraction of a turn (resolution 1.5e-9 rad), sincospi takes half turns.
+// fraction of a turn, sincospi takes half turns in fp32 (24 bits: off by up to 9.4e-8 rad near half
+// a turn, less for smaller angles).
 __device__ __forceinline__ float2 turn_of(unsigned long long step, int32_t pos) {
   const unsigned long long phase = (unsigned long long)(long long)pos * step;
   const float half_turns = (float)(int32_t)(phase >> 32) * 0x1p-31f;
@@ -221,7 +223,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // them).  16 divisions a lane were half of the instructions; x / scale is the product with the
 // scale's reciprocal and one correction by the remainder, which a fused multiply-add gives
 // exactly (Markstein, IBM J. Res. Dev. 34, 1990): the correctly rounded quotient, so that a
-// value near the middle of two codes goes to the nearer one.
+// value near the middle of two codes goes to the nearer one.  (In blocks whose
+// largest value is below about 2^-105 the remainder's last bits fall under the smallest number,
+// and up to one quotient in 800 is off in its last bit.)
 template <typename T, bool kHalves, bool kVec>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
   constexpr int V = Vec<T>::n, N = 16 / V;

@@ -100,8 +100,10 @@ def run(steps: int = 3, seed: int = 0, check: bool = False) -> float:
         # prompts: packed layer by layer, then handed to the cache group by group
         owned = [[] for _ in range(REQ)]     # each request's logical addresses, oldest first
         store = [[] for _ in range(GROUPS)]  # (check) every row ever appended, by address
+        # (the prefix layer by layer: attend takes one layer's rows one after the other)
         prefix = [model.pack_tokens(torch.arange(PREFIX, device="cuda"),
-                                    torch.empty(PREFIX, LAYERS, 656, dtype=torch.uint8, device="cuda"))
+                                    torch.empty(LAYERS, PREFIX, 656, dtype=torch.uint8,
+                                                device="cuda").transpose(0, 1))
                   for _ in range(GROUPS)]
 
         def append(r: int, group_rows):
@@ -139,7 +141,7 @@ def run(steps: int = 3, seed: int = 0, check: bool = False) -> float:
                     q = model.queries(time)
                     own_j = own[:, j].unflatten(0, (REQ, Q))
                     part = rows.attend(q, out[j], entry_row.view(REQ, Q, K), SCALE, own_rows=own_j)
-                    shared = rows.attend(q, prefix[g][:, j].contiguous(), prefix_entries, SCALE)
+                    shared = rows.attend(q, prefix[g][:, j], prefix_entries, SCALE)
                     o, _ = rows.join([part[0], shared[0]], [part[1], shared[1]])
                     if check:
                         every = torch.cat(store[g])[:, j]

@@ -478,6 +478,38 @@ int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_a
                   void *stream);
 
 /*
+ * ula_rows_norm_rotate -- query heads (or keys) normed and turned in one pass: for each of n
+ * tokens' heads, y = x / sqrt(mean(x^2) + eps) * weight over its `width` channels, then the
+ * 64 channels of y from `at` on turned as by ula_rows_rotate.  In fp32, rounded once.
+ *   width    : 64..ULA_MAX_WIDTH; at: 0..width - 64.
+ *   d_x      : channel c of head h of token t at d_x[t * x_token_stride + h * x_head_stride + c].
+ *   d_weight : [width], of dtype or ULA_TYPE_F32 (weight_dtype).
+ *   d_out    : likewise; may be d_x itself with the same strides (in place), and must not
+ *              overlap it otherwise.  Its own rows of `width` channels may not overlap.
+ *   eps      : finite, not negative.
+ */
+#define ULA_MAX_WIDTH 1024u
+int ula_rows_norm_rotate(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride,
+                         uint32_t n, uint32_t heads, uint32_t width, uint32_t at, uint32_t dtype,
+                         const void *d_x, uint64_t x_token_stride, uint64_t x_head_stride,
+                         const void *d_weight, uint32_t weight_dtype, float eps, void *d_out,
+                         uint64_t out_token_stride, uint64_t out_head_stride, void *stream);
+
+/*
+ * ula_rows_pack_norm -- ula_rows_pack with the key's norm in the same pass: the 512 latents
+ * become x / sqrt(mean(x^2) + eps) * latent_weight before they are quantised; with a rope
+ * weight the 64 rope channels become as much before they are turned.
+ *   d_latent_weight, d_rope_weight : [512] and [64], of dtype or ULA_TYPE_F32; the latter
+ *                                    NULL: rope channels are not normed.
+ */
+int ula_rows_pack_norm(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride,
+                       uint32_t n, uint32_t dtype, const void *d_latent, uint64_t latent_stride,
+                       const void *d_rope, uint64_t rope_stride, const void *d_latent_weight,
+                       uint32_t latent_weight_dtype, const void *d_rope_weight,
+                       uint32_t rope_weight_dtype, float eps, void *d_rows, uint64_t row_stride,
+                       void *stream);
+
+/*
  * ula_rows_attend -- attention of a step's query tokens over the rows it selected.
  * For query token (r, i) and head h, over the entries e of entry_row[r][i] with
  * 0 <= entry_row < n_rows (others, such as the -1 of a pad, select nothing) and, with
@@ -520,6 +552,80 @@ typedef struct ula_attend_args {
 uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k,
                                    int own);
 int ula_rows_attend(const ula_attend_args *args, void *stream);
+
+/*
+ * ula_rows_attend_tree -- attention of a tree of drafted tokens: ula_rows_attend with own
+ * rows that a query token sees along its branch.  Query token i of request r is node i of
+ * the request's tree and sees its list's rows and the own rows of i, parent[r][i],
+ * parent[r][parent[r][i]], and so on.  (Node 0 is the token that was accepted last; one
+ * chain, parent i - 1, is ula_rows_attend's order.)
+ *   args   : as for ula_rows_attend; own_rows is needed, n_q at most ULA_MAX_TREE.
+ *   parent : device int32 [n_req][n_q]; a value that is not an earlier node's (negative, i
+ *            or more) stands for none.
+ *   flags  : ULA_TREE_SHARED_LIST: entry_row is [n_req][k], one list for all nodes of a
+ *            request's tree, whose rows are then read once for all their query heads.
+ * An own row with a NaN among its codes or a scale that is not finite gives NaN to the nodes
+ * that see it, and counts for nothing for the others.
+ */
+#define ULA_MAX_TREE 64u
+#define ULA_TREE_SHARED_LIST 1u
+uint64_t ula_rows_attend_tree_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k,
+                                        uint32_t flags);
+int ula_rows_attend_tree(const ula_attend_args *args, const int32_t *parent, uint32_t flags,
+                         void *stream);
+
+/*
+ * ula_rows_score -- accumulate attention weights by logical address, for eviction: over query
+ * tokens (r, i), heads h and entries e of the token's list,
+ *   scores[address[e]] += exp(z[e] - lse[r][i][h])
+ * with the logits z of ula_rows_attend (or its tree's) and the lse that it gave (with own rows, or
+ * joined with other parts: the weights are then those of the whole).  Entries whose row is outside
+ * [0, n_rows) or whose address is outside [0, n_scores) count for nothing, as do query heads whose
+ * lse is -inf; a weight counts as 1 at most, one that is not a number as 0.  An address's weights
+ * are summed as whole numbers (the sum does not depend on an order) and added to its score once, in
+ * fp32.
+ *   q         : as for ula_rows_attend.
+ *   entry_row : device int32 [n_req][n_q][k], or [n_req][k] with ULA_TREE_SHARED_LIST: one list for
+ *               a request's query tokens.
+ *   address   : device int32, entry_row's shape: ula_step_group's d_sel.
+ *   lse       : device fp32 [n_req][n_q][heads].
+ *   scores    : device fp32 [n_scores], updated in place.
+ *   workspace : device, 8-byte aligned, ula_rows_score_workspace(n_scores) bytes.  Calls that
+ *               overlap on the GPU need workspaces of their own; they may share the scores.
+ */
+typedef struct ula_score_args {
+  const void *q;
+  uint64_t q_req_stride, q_tok_stride, q_head_stride;
+  const void *rows;
+  const int32_t *entry_row;
+  const int32_t *address;
+  const float *lse;
+  float *scores;
+  void *workspace;
+  uint64_t workspace_bytes;
+  uint32_t n_rows, n_scores, n_req, n_q, heads, k, flags;
+  float softmax_scale;
+} ula_score_args;
+
+uint64_t ula_rows_score_workspace(uint32_t n_scores);
+int ula_rows_score(const ula_score_args *args, void *stream);
+
+/*
+ * ula_rows_evict -- which of each request's addresses stay.  Of request r's n = length[r]
+ * addresses (0..longest, clamped), oldest first, the first `first` and the last `last` stay, and of
+ * the others those with the largest scores, min(n, budget) in all; where scores are equal the older
+ * ones leave.
+ *   scores  : device fp32 [n_scores], by address (an address outside has the score 0; a NaN is larger
+ *             than every number).
+ *   address : device int32 [n_req][longest]; what stands behind a list's length is not read.
+ *   kept    : device int32 [n_req][budget]: the addresses that stay, in order, then -1.
+ *   dropped : device int32 [n_req][longest - budget] (none if budget >= longest): those that leave, in
+ *             order, then -1: what ula_free takes.
+ *   first + last may not pass budget.  kept and dropped may not overlap the inputs or each other.
+ */
+int ula_rows_evict(const float *scores, uint32_t n_scores, const int32_t *address,
+                   const int32_t *length, uint32_t n_req, uint32_t longest, uint32_t budget,
+                   uint32_t first, uint32_t last, int32_t *kept, int32_t *dropped, void *stream);
 
 /*
  * ula_rows_join -- join `parts` partial results over disjoint rows (1..ULA_MAX_PARTS):

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libula.so")
 BINDING = os.path.join(OUT_DIR, "_rows.so")
-SOURCES = ["ula_kernels.cu", "ula_api.cu", "ula_noalloc.cu", "ula_rows.cu", "ula_attend.cu"]
+SOURCES = ["ula_kernels.cu", "ula_api.cu", "ula_noalloc.cu", "ula_rows.cu", "ula_attend.cu", "ula_score.cu",
+           "ula_evict.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

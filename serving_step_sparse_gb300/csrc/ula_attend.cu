@@ -23,6 +23,9 @@
 #include <utility>
 
 #include "ula.h"
+#include "ula_tc.cuh"
+
+using namespace ula_tc;
 
 namespace {
 
@@ -53,175 +56,14 @@ struct AttendParams {
   uint32_t cluster;          // blocks of a cluster (one item each), or 1
   float c0;
   uint32_t hold;             // (test hook) an mbarrier whose phases never end; kBars: none
+  // A tree (ula_rows_attend_tree): own row j stands for node j of the request's tree.  A list's columns
+  // (a.heads) are one node's query heads or, where the tree shares the list, all nodes'; a.n_q is
+  // the number of lists of a request.
+  const int32_t *parent;     // [n_req][nodes]
+  uint32_t nodes, node_heads;
   float *part_out;           // [2 * blocks][NH][512]: unfinished items' results, normalised
   float *part_lse;           // [2 * blocks][NH]: their log2 sums
 };
-
-// ---------------------------------------------------------------- PTX
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Bounded: false after 2^18 tries. A try that is not met comes back after 4.0 us on this GPU,
-// whatever time it is given, so a wait that is never met ends after 1.05 s, and any wait that these
-// kernels can meet is shorter than a tenth of a millisecond. The loop is written out because its
-// size matters: the compute warps pass through some 15 waits a tile, their code is longer than
-// the instruction caches nearest to them: with a clock read and two ways out in each wait the step
-// of 96 tokens, 128 heads, 2,051 rows took 6 % more when this form came in, and with a limit that is
-// a kernel argument it takes 125.0 us instead of 120.5.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .u32 i;\n mov.u32 i, 0;\n"
-      "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra over;\n"
-      " add.u32 i, i, 1;\n setp.lt.u32 p, i, 0x40000;\n @p bra again;\n setp.ne.u32 p, 0, 0;\n"
-      "over:\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-  return done;
-}
-
-// By a whole warp: the same answer in every lane, so that a warp leaves its work as one.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p;
-}
-
-// One MMA of K = 16: D[128][N] (+)= A B, all operands in shared memory.
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
-}
-
-// 16 bytes to shared memory without passing through registers; zeros where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// This thread's arrival, once its copies so far have landed.
-__device__ __forceinline__ void copy_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Brings bytes (a multiple of 16, as the address is) into L2.
-__device__ __forceinline__ void prefetch(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// N consecutive TMEM columns of this warp's 32 lanes.
-template <int N> __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]);
-template <int N> __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[N]);
-template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t addr, float (&v)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t addr, float (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-                 "=f"(v[7]) : "r"(addr) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t addr, float (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15}, [%16];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
-        "=f"(v[15]) : "r"(addr) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t addr, float (&v)[32]) {
-  tmem_ld<16>(addr, reinterpret_cast<float (&)[16]>(v[0]));
-  tmem_ld<16>(addr + 16, reinterpret_cast<float (&)[16]>(v[16]));
-}
-template <> __device__ __forceinline__ void tmem_st<4>(uint32_t addr, const float (&v)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
-               ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ float warp_max(float v) {  // NaN counts for nothing
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ void fma2(float &x0, float &x1, float s, float v0, float v1) {  // x += s * v
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %2};\n mov.b64 b, {%3, %4};\n mov.b64 c, {%0, %1};\n"
-      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
-      : "+f"(x0), "+f"(x1) : "f"(s), "f"(v0), "f"(v1));
-}
-__device__ __forceinline__ void mul2(float &x0, float &x1, float s, float v0, float v1) {  // x = s * v
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %2};\n mov.b64 b, {%3, %4};\n mul.rn.f32x2 b, a, b;\n"
-      " mov.b64 {%0, %1}, b;\n}\n"
-      : "=f"(x0), "=f"(x1) : "f"(s), "f"(v0), "f"(v1));
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
-// Sums of N values over a warp's lanes: lane h (and h + N, ...) gets the h-th.  Each step
-// sends the half of the values that the other lane will keep.
-template <int N>
-__device__ __forceinline__ float sum_rows(const float (&v)[N], uint32_t lane) {
-  float x[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = v[i];
-#pragma unroll
-  for (int d = N / 2; d; d >>= 1)
-#pragma unroll
-    for (int i = 0; i < d; ++i) {
-      const bool up = lane & d;
-      const float keep = up ? x[i + d] : x[i], send = up ? x[i] : x[i + d];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, d);
-    }
-  float r = x[0];
-#pragma unroll
-  for (int d = N; d < 32; d <<= 1) r += __shfl_xor_sync(0xffffffffu, r, d);
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Shared-memory operand descriptor, 128-byte swizzle (the swizzle XORs bits 4-6 of an
-// address with bits 7-9, so every operand region starts on 1,024 bytes).  K-major: rows of
-// 64 elements, 8 rows in 1,024 bytes (stride); MN-major: 64 elements of M or N in 128
-// bytes, 8 of K in 1,024 bytes (stride), the next 64 of M `lead` bytes on.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// e4m3 codes (two in the low half of `two`) to bf16, exactly.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
-  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);  // (their low halves are 0)
-}
 
 // ---------------------------------------------------------------- the kernel
 
@@ -280,12 +122,14 @@ __device__ __forceinline__ int32_t entry_of(const AttendParams &p, const Place &
   return e < p.a.k ? __ldg(p.a.entry_row + (uint64_t)at.token * p.a.k + e) : 0;
 }
 
-// Its row (0: none).  Entries behind the list stand for the request's own rows.
+// Its row (0: none).  Entries behind the list stand for the request's own rows (of a tree: all of
+// them; which node sees which is masked after the products).
+template <bool kTree>
 __device__ __forceinline__ uint64_t row_of(const AttendParams &p, const Place &at, uint32_t e, int32_t u) {
   if (e < p.a.k)
     return u >= 0 && (uint32_t)u < p.a.n_rows ? (uint64_t)p.a.rows + (uint64_t)u * ULA_ROW_BYTES : 0;
   const uint32_t j = e - p.a.k;
-  if (e >= p.keys || j > at.qi) return 0;
+  if (e >= p.keys || (!kTree && j > at.qi)) return 0;
   return (uint64_t)p.a.own_rows + at.req * p.a.own_req_stride + j * p.a.own_tok_stride;
 }
 
@@ -317,6 +161,72 @@ struct Joined {
   }
 };
 
+// The bits of the ancestors of a tree's nodes, each node's own among them: lane l gets node l's and
+// node (l + 32)'s.  By doubling: after n steps a node has its ancestors up to 2^n - 1 levels up.
+__device__ __forceinline__ void ancestors(const int32_t *parent, uint32_t nodes, uint32_t lane, uint64_t (&seen)[2]) {
+  int32_t up[2];
+#pragma unroll
+  for (uint32_t i = 0; i < 2; ++i) {
+    const int32_t node = (int32_t)(lane + 32 * i);
+    up[i] = (uint32_t)node < nodes ? __ldg(parent + node) : -1;
+    if (up[i] < 0 || up[i] >= node) up[i] = -1;  // (none but an earlier node is a parent)
+    seen[i] = 1ull << node;
+  }
+  for (uint32_t reach = 1; reach < nodes; reach *= 2) {
+    uint64_t more[2];
+    int32_t next[2];
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint64_t s0 = __shfl_sync(0xffffffffu, seen[0], up[i] & 31), s1 = __shfl_sync(0xffffffffu, seen[1], up[i] & 31);
+      const int32_t n0 = __shfl_sync(0xffffffffu, up[0], up[i] & 31), n1 = __shfl_sync(0xffffffffu, up[1], up[i] & 31);
+      more[i] = up[i] < 0 ? 0 : up[i] < 32 ? s0 : s1;
+      next[i] = up[i] < 0 ? -1 : up[i] < 32 ? n0 : n1;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) seen[i] |= more[i], up[i] = next[i];
+  }
+}
+
+// Masks the logits of a tile with own rows of a tree: a column (node and head) sees the rows of its node
+// and of the node's ancestors.  `codes`: the tile's widened codes, `first` the thread's first column.
+// An own row is in the products of the columns that do not see it too, with a probability of 0, so
+// what it holds must be finite: one with a NaN among its codes (all its logits are NaN) or a scale
+// that is not finite gives NaN to the columns that see it here, and goes on with codes and scales that
+// are.  (Both threads of a row may write its codes: the same values.)
+template <int HG>
+__device__ __forceinline__ void see_tree(const AttendParams &p, const Place &w, uint32_t first, uint32_t mine,
+                                         uint8_t *codes, float (&z)[HG], float4 &scale) {
+  uint64_t seen[2];
+  ancestors(p.parent + (uint64_t)w.req * p.nodes, p.nodes, threadIdx.x & 31, seen);
+  const uint32_t e = w.tile * kTile + mine, j = e - p.a.k;
+  const bool own = e >= p.a.k && j < p.nodes;
+  bool bad = own;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) bad = bad && z[h] != z[h];
+  if (own && !(isfinite(scale.x) && isfinite(scale.y) && isfinite(scale.z) && isfinite(scale.w))) bad = true;
+  if (bad) {
+    scale = make_float4(1.f, 1.f, 1.f, 1.f);
+    for (uint32_t i = 0; i < 64; ++i) {  // (any order: the swizzle stays within a row's 128 bytes)
+      uint32_t *at = reinterpret_cast<uint32_t *>(codes + (i >> 3) * kGroupBytes + mine * 128 + (i & 7) * 16);
+      for (uint32_t k = 0; k < 4; ++k) {
+        uint32_t two = at[k];
+        if ((two & 0x7fff0000u) > 0x7f800000u) two &= 0xffffu;
+        if ((two & 0x7fffu) > 0x7f80u) two &= 0xffff0000u;
+        at[k] = two;
+      }
+    }
+  }
+  const uint32_t column = w.h0 + first;
+  uint32_t node = column / p.node_heads, head = column - node * p.node_heads;
+  node += w.qi;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    const uint64_t s0 = __shfl_sync(0xffffffffu, seen[0], node & 31), s1 = __shfl_sync(0xffffffffu, seen[1], node & 31);
+    if (own) z[h] = ((node < 32 ? s0 : s1) >> j & 1) == 0 ? -INFINITY : bad ? __int_as_float(0x7fffffff) : z[h];
+    if (++head == p.node_heads) head = 0, ++node;
+  }
+}
+
 // Persistent: one block per SM, which runs whole items first, then an even share of the rest's
 // tiles (an item whose tiles end up in several blocks leaves one partial result in each;
 // k_join_parts joins them).  8 compute warps fetch the rows' codes into registers one tile ahead, widen
@@ -341,7 +251,8 @@ struct Joined {
 //
 // kCluster: the tiles of one item spread over the blocks of a cluster, which join their
 // results through each other's shared memory (no second kernel, no trip through L2).
-template <uint32_t NH, bool kCluster>
+// kTree: a column is a node and a head, and own rows are masked by the nodes' ancestors (see_tree).
+template <uint32_t NH, bool kCluster, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend(const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw_smem[];
@@ -503,7 +414,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       auto place_rows = [&](uint32_t par) {
         uint64_t *place = reinterpret_cast<uint64_t *>(sm + L::place) + par * kTile + r0;
 #pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) place[lane + 32 * j] = row_of(p, w, w.tile * kTile + r0 + lane + 32 * j, u[j]);
+        for (uint32_t j = 0; j < 2; ++j) place[lane + 32 * j] = row_of<kTree>(p, w, w.tile * kTile + r0 + lane + 32 * j, u[j]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPlace));
       };
@@ -621,7 +532,12 @@ k_attend(const __grid_constant__ AttendParams p) {
         const uint32_t h = i / 72, c = i - h * 72;
         const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
         const bool in = w.h0 + h < p.a.heads;
-        const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
+        uint64_t at = (w.h0 + h) * p.a.q_head_stride;
+        if (kTree) {
+          const uint32_t node = (w.h0 + h) / p.node_heads;
+          at = node * p.a.q_tok_stride + (w.h0 + h - node * p.node_heads) * p.a.q_head_stride;
+        }
+        const __nv_bfloat16 *src = q + (in ? at + c * 8 : 0);
         copy16(dst, src, in ? 16 : 0);
       }
     };
@@ -653,7 +569,7 @@ k_attend(const __grid_constant__ AttendParams p) {
       if (!ok) break;
       // this row's scales, and whether there is a row
       if (!(ok = warp_wait(bar(kBarScale), par))) break;
-      const float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
+      float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
       const bool present = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] != 0;
       const bool more = n + 1 < count;
 
@@ -709,6 +625,8 @@ k_attend(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int h = 0; h < HG; ++h) z[h] = present ? z[h] : -INFINITY;
       }
+      if (kTree && (w.tile + 1) * kTile > p.a.k)  // (the tile holds nodes' rows)
+        see_tree<HG>(p, w, grp * HG, mine, sm + L::k, z, scale);
 
       if (more) fetch(raw1, n + 1, block1, 1);
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)
@@ -989,19 +907,19 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, uint32_t block, uint32_t 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <uint32_t NH>
+template <uint32_t NH, bool kTree>
 cudaError_t prepare_attend(bool cluster) {
   // (idempotent and cheap; a per-device flag would have to know about device resets)
-  auto kernel = cluster ? k_attend<NH, true> : k_attend<NH, false>;
+  auto kernel = cluster ? k_attend<NH, true, kTree> : k_attend<NH, false, kTree>;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NH>::bytes);
 }
 
-bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool own, Plan *pl) {
-  const uint64_t tokens = (uint64_t)n_req * n_q;
-  if (tokens > 0x7fffffffull || heads > 0x7fffffffu || k > 0x7fffffffu - kTile ||
-      (own && n_q > 0x7fffffffu - kTile - k))
+// For lists ("tokens": query tokens, or requests whose tree shares its list) of k entries and own rows
+// behind them, and each list's columns (its query heads, or its nodes' query heads).
+bool make_plan(uint64_t tokens, uint32_t heads, uint32_t k, uint32_t own, Plan *pl) {
+  if (tokens > 0x7fffffffull || heads > 0x7fffffffu || k > 0x7fffffffu - kTile || own > 0x7fffffffu - kTile - k)
     return false;
-  pl->keys = k + (own ? n_q : 0);
+  pl->keys = k + own;
   pl->tiles = pl->keys ? (pl->keys + kTile - 1) / kTile : 1;
   // Heads per item: the fewest that hold them all, up to 64 (TMEM's columns).  The rows are widened
   // once an item, so heads are not split further: 96 tokens x 2,051 rows, 64 heads, 71.6 us with 64
@@ -1046,49 +964,23 @@ bool make_plan(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, bool ow
   return true;
 }
 
-template <uint32_t NH>
+template <uint32_t NH, bool kTree>
 cudaError_t launch_attend(const AttendParams &p, cudaStream_t st) {
-  const cudaError_t e = prepare_attend<NH>(p.cluster > 1);
+  const cudaError_t e = prepare_attend<NH, kTree>(p.cluster > 1);
   if (e != cudaSuccess) return e;
-  return launch(p.cluster > 1 ? k_attend<NH, true> : k_attend<NH, false>, p.blocks, kThreads, Shared<NH>::bytes, p.cluster, st, p);
+  return launch(p.cluster > 1 ? k_attend<NH, true, kTree> : k_attend<NH, false, kTree>, p.blocks, kThreads, Shared<NH>::bytes, p.cluster, st, p);
 }
 
-}  // namespace
-
-extern "C" uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads,
-                                              uint32_t k, int own) {
-  Plan pl;
-  return make_plan(n_req, n_q, heads, k, own != 0, &pl) ? pl.workspace : 0;
-}
-
-extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
-  if (!args) return ULA_ERR_INVALID_ARG;
-  ula_attend_args a = *args;
-  if (a.n_req == 1) a.q_req_stride = a.own_req_stride = 0;  // (no steps: whatever they are)
-  if (a.n_q == 1) a.q_tok_stride = a.own_tok_stride = 0;
-  if (a.heads == 1) a.q_head_stride = 0;
-  if (a.n_req == 0 || a.n_q == 0 || a.heads == 0) return ULA_OK;
-  if (!a.q || !a.out || (a.k && (!a.entry_row || (!a.rows && a.n_rows)))) return ULA_ERR_INVALID_ARG;
-  if (!aligned(a.q, 16) || !aligned(a.rows, 16) || !aligned(a.own_rows, 16) || !aligned(a.out, 16) ||
-      !aligned(a.entry_row, 4) || !aligned(a.lse, 4) || !aligned(a.workspace, 16))
-    return ULA_ERR_INVALID_ARG;
-  if (a.q_req_stride % 8 || a.q_tok_stride % 8 || a.q_head_stride % 8 || a.own_req_stride % 16 ||
-      a.own_tok_stride % 16 || a.n_rows > 0x7fffffffu)
-    return ULA_ERR_INVALID_ARG;
-  Plan pl;
-  if (!make_plan(a.n_req, a.n_q, a.heads, a.k, a.own_rows != nullptr, &pl)) return ULA_ERR_INVALID_ARG;
-  if (pl.workspace && (!a.workspace || a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
-  AttendParams p{};
-  p.a = a;
+template <bool kTree>
+cudaError_t launch_plan(const Plan &pl, AttendParams &p, cudaStream_t st) {
   p.rest = pl.rest, p.blocks = pl.blocks, p.rounds = pl.rounds, p.sharers = pl.sharers, p.tiles = pl.tiles, p.head_tiles = pl.head_tiles, p.keys = pl.keys;
   p.cluster = pl.cluster;
   p.hold = g_hold.load(std::memory_order_relaxed);
-  p.c0 = a.softmax_scale * 1.44269504088896341f;
-  p.part_out = (float *)a.workspace;
+  p.c0 = p.a.softmax_scale * 1.44269504088896341f;
+  p.part_out = (float *)p.a.workspace;
   p.part_lse = p.part_out + (uint64_t)2 * pl.blocks * pl.nh * ULA_ROW_LATENT;
-  cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = pl.nh == 16 ? launch_attend<16>(p, st) : pl.nh == 32 ? launch_attend<32>(p, st) : launch_attend<64>(p, st);
-  if (e != cudaSuccess) return ULA_ERR_CUDA;
+  cudaError_t e = pl.nh == 16 ? launch_attend<16, kTree>(p, st) : pl.nh == 32 ? launch_attend<32, kTree>(p, st) : launch_attend<64, kTree>(p, st);
+  if (e != cudaSuccess) return e;
   if (pl.parts) {
     // Heads per block of the join: 4 share the work on a block's place once every SM has several
     // blocks (96 tokens x 2,051 rows, 64 heads, both kernels: 72.9 us; 73.9 with 2), and 2 keep the
@@ -1103,7 +995,76 @@ extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
     e = launch(pl.tiles <= 2 ? k_join_parts<2> : pl.tiles <= 4 || most <= 4 ? k_join_parts<4> : few ? k_join_parts<16> : k_join_parts<8>,
                dim3(items, pl.nh / join_heads), 256, 0, 1, st, p, pl.nh, join_heads);
   }
-  return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+  return e;
+}
+
+// What both calls ask of their arguments, whose strides along a single request, token or head count for
+// nothing and become 0.
+bool arguments_hold(ula_attend_args &a) {
+  if (a.n_req == 1) a.q_req_stride = a.own_req_stride = 0;
+  if (a.n_q == 1) a.q_tok_stride = a.own_tok_stride = 0;
+  if (a.heads == 1) a.q_head_stride = 0;
+  if (a.n_req == 0 || a.n_q == 0 || a.heads == 0) return true;
+  if (!a.q || !a.out || (a.k && (!a.entry_row || (!a.rows && a.n_rows)))) return false;
+  if (!aligned(a.q, 16) || !aligned(a.rows, 16) || !aligned(a.own_rows, 16) || !aligned(a.out, 16) ||
+      !aligned(a.entry_row, 4) || !aligned(a.lse, 4) || !aligned(a.workspace, 16))
+    return false;
+  return !(a.q_req_stride % 8 || a.q_tok_stride % 8 || a.q_head_stride % 8 || a.own_req_stride % 16 ||
+           a.own_tok_stride % 16 || a.n_rows > 0x7fffffffu);
+}
+
+}  // namespace
+
+extern "C" uint64_t ula_rows_attend_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads,
+                                              uint32_t k, int own) {
+  Plan pl;
+  return make_plan((uint64_t)n_req * n_q, heads, k, own ? n_q : 0, &pl) ? pl.workspace : 0;
+}
+
+extern "C" int ula_rows_attend(const ula_attend_args *args, void *stream) {
+  if (!args) return ULA_ERR_INVALID_ARG;
+  AttendParams p{};
+  p.a = *args;
+  if (!arguments_hold(p.a)) return ULA_ERR_INVALID_ARG;
+  if (p.a.n_req == 0 || p.a.n_q == 0 || p.a.heads == 0) return ULA_OK;
+  Plan pl;
+  if (!make_plan((uint64_t)p.a.n_req * p.a.n_q, p.a.heads, p.a.k, p.a.own_rows ? p.a.n_q : 0, &pl)) return ULA_ERR_INVALID_ARG;
+  if (pl.workspace && (!p.a.workspace || p.a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
+  return launch_plan<false>(pl, p, (cudaStream_t)stream) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+namespace {
+
+// The plan of a tree: lists of the nodes or, shared, of the requests.
+bool plan_tree(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k, uint32_t flags, Plan *pl) {
+  if (n_q > ULA_MAX_TREE || (flags & ~ULA_TREE_SHARED_LIST)) return false;
+  const bool shared = flags & ULA_TREE_SHARED_LIST;
+  if (shared && heads > 0x7fffffffu / ULA_MAX_TREE) return false;
+  return make_plan(shared ? n_req : (uint64_t)n_req * n_q, shared ? n_q * heads : heads, k, n_q, pl);
+}
+
+}  // namespace
+
+extern "C" uint64_t ula_rows_attend_tree_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t k,
+                                                   uint32_t flags) {
+  Plan pl;
+  return plan_tree(n_req, n_q, heads, k, flags, &pl) ? pl.workspace : 0;
+}
+
+extern "C" int ula_rows_attend_tree(const ula_attend_args *args, const int32_t *parent, uint32_t flags,
+                                    void *stream) {
+  if (!args) return ULA_ERR_INVALID_ARG;
+  AttendParams p{};
+  p.a = *args;
+  if (!arguments_hold(p.a)) return ULA_ERR_INVALID_ARG;
+  Plan pl;
+  if (!plan_tree(p.a.n_req, p.a.n_q, p.a.heads, p.a.k, flags, &pl)) return ULA_ERR_INVALID_ARG;
+  if (p.a.n_req == 0 || p.a.n_q == 0 || p.a.heads == 0) return ULA_OK;
+  if (!p.a.own_rows || !parent || !aligned(parent, 4)) return ULA_ERR_INVALID_ARG;
+  if (pl.workspace && (!p.a.workspace || p.a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
+  p.parent = parent, p.nodes = p.a.n_q, p.node_heads = p.a.heads;
+  if (flags & ULA_TREE_SHARED_LIST) p.a.heads *= p.a.n_q, p.a.n_q = 1;
+  return launch_plan<true>(pl, p, (cudaStream_t)stream) == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 
 extern "C" int ula_rows_debug_hold(int barrier) {

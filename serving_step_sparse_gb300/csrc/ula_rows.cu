@@ -1,5 +1,6 @@
-// Operators on the cache's FP8 rows: rotary positions with several axes, row packing and
-// the join of partial attention results (the attention itself: ula_attend.cu).
+// Operators on the cache's FP8 rows: rotary positions with several axes, row packing, both with a
+// norm in the same pass, and the join of partial attention results (the attention itself:
+// ula_attend.cu).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cmath>
@@ -189,6 +190,63 @@ __global__ void __launch_bounds__(256) k_rotate_any(const __grid_constant__ Rota
   o[ib] = from_f<T>(ob);
 }
 
+// ---------------------------------------------------------------- norm and rotate
+
+struct NormParams {
+  RotaryDev rot;
+  const int32_t *pos;
+  uint64_t pos_axis_stride;
+  uint32_t n, heads, width, at;  // channels of a head; the first of its 64 rope channels
+  const void *x;
+  uint64_t xt, xh;
+  const void *weight;
+  bool weight_f32, halves;
+  void *out;
+  uint64_t ot, oh;
+  float eps;
+};
+
+// Element i of a weight that has its operand's type T, or fp32.
+template <typename T>
+__device__ __forceinline__ float weight_at(const void *w, bool f32, uint32_t i) {
+  return f32 ? ((const float *)w)[i] : to_f(((const T *)w)[i]);
+}
+
+// 1 / rms of `width` channels with the sum of squares ss.
+__device__ __forceinline__ float inverse_rms(float ss, float width, float eps) {
+  return __frsqrt_rn(__fdiv_rn(ss, width) + eps);
+}
+
+// Any alignment, strides and widths: one warp per token and head, which reads its channels twice; a lane turns
+// a pair.  (In place: a lane writes the channels that it alone reads in the second pass.)
+template <typename T>
+__global__ void __launch_bounds__(256) k_norm_any(const __grid_constant__ NormParams p) {
+  const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t j = threadIdx.x & 31;
+  after_previous();
+  if (w >= (uint64_t)p.n * p.heads) return;
+  const uint32_t t = (uint32_t)(w / p.heads), h = (uint32_t)(w % p.heads);
+  const T *x = (const T *)p.x + t * p.xt + h * p.xh;
+  T *o = (T *)p.out + t * p.ot + h * p.oh;
+  float ss = 0.f;
+  for (uint32_t c = j; c < p.width; c += 32) {
+    const float v = to_f(x[c]);
+    ss = fmaf(v, v, ss);
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+  const float r = inverse_rms(ss, (float)p.width, p.eps);
+  auto normed = [&](uint32_t c) { return to_f(x[c]) * r * weight_at<T>(p.weight, p.weight_f32, c); };
+  for (uint32_t c = j; c < p.width; c += 32)
+    if (c - p.at >= ULA_ROW_ROPE) o[c] = from_f<T>(normed(c));
+  const float2 cs = turn_of(p.rot.step[j], p.pos[p.rot.axis[j] * p.pos_axis_stride + t]);
+  const uint32_t ia = p.at + (p.halves ? j : 2 * j), ib = p.at + (p.halves ? j + kPairs : 2 * j + 1);
+  float oa, ob;
+  turn(normed(ia), normed(ib), cs.x, cs.y, oa, ob);
+  o[ia] = from_f<T>(oa);
+  o[ib] = from_f<T>(ob);
+}
+
 // ---------------------------------------------------------------- pack
 
 struct PackParams {
@@ -202,6 +260,9 @@ struct PackParams {
   uint64_t rope_stride;
   uint8_t *rows;
   uint64_t row_stride;
+  const void *latent_weight, *rope_weight;  // (with a norm; the rope's may be null: not normed)
+  bool latent_weight_f32, rope_weight_f32;
+  float eps;
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -226,7 +287,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // value near the middle of two codes goes to the nearer one.  (In blocks whose
 // largest value is below about 2^-105 the remainder's last bits fall under the smallest number,
 // and up to one quotient in 800 is off in its last bit.)
-template <typename T, bool kHalves, bool kVec>
+// kNorm: latents (and the rope channels, with a weight) divided by their root mean square and
+// multiplied by a weight first; a lane's 16 weights stay in registers.
+template <typename T, bool kHalves, bool kVec, bool kNorm>
 __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams p) {
   constexpr int V = Vec<T>::n, N = 16 / V;
   const uint32_t l = threadIdx.x & 31, warps = gridDim.x * 8;
@@ -255,13 +318,38 @@ __global__ void __launch_bounds__(256) k_pack(const __grid_constant__ PackParams
   uint64_t t = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   after_previous();
   if (t < p.n) fetch((uint32_t)t);
+  float weight[kNorm ? 16 : 1], weight_a = 1.f, weight_b = 1.f;
+  if (kNorm) {
+#pragma unroll
+    for (uint32_t i = 0; i < 16; ++i) weight[i] = weight_at<T>(p.latent_weight, p.latent_weight_f32, 16 * l + i);
+    if (p.rope_weight) {
+      weight_a = weight_at<T>(p.rope_weight, p.rope_weight_f32, ia);
+      weight_b = weight_at<T>(p.rope_weight, p.rope_weight_f32, ib);
+    }
+  }
   for (; t < p.n; t += warps) {
     float v[16], amax = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) Vec<T>::open(next[i], reinterpret_cast<float (&)[V]>(v[i * V]));
-    const float a = to_f(next_a), b = to_f(next_b);
+    float a = to_f(next_a), b = to_f(next_b);
     const int32_t pos = next_pos;
     if (t + warps < p.n) fetch((uint32_t)(t + warps));
+    if (kNorm) {
+      float ss = 0.f, rs = fmaf(a, a, b * b);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      const float r = inverse_rms(ss, (float)ULA_ROW_LATENT, p.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = v[i] * r * weight[i];
+      if (p.rope_weight) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, d);
+        const float rr = inverse_rms(rs, (float)ULA_ROW_ROPE, p.eps);
+        a = a * rr * weight_a, b = b * rr * weight_b;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(v[i]));
 #pragma unroll
@@ -367,9 +455,8 @@ uint32_t sm_count() {
              ? (uint32_t)n : 1u;
 }
 
-// Whether two of the rows of 64 channels at i * si + j * sj (i < ni, j < nj) share elements.
-bool overlap(uint64_t ni, uint64_t si, uint64_t nj, uint64_t sj) {
-  constexpr uint64_t kRow = ULA_ROW_ROPE;
+// Whether two of the rows of kRow channels at i * si + j * sj (i < ni, j < nj) share elements.
+bool overlap(uint64_t ni, uint64_t si, uint64_t nj, uint64_t sj, const uint64_t kRow = ULA_ROW_ROPE) {
   if ((ni > 1 && si < kRow) || (nj > 1 && sj < kRow)) return true;
   if (ni < 2 || nj < 2) return false;
   if (si > sj) std::swap(si, sj), std::swap(ni, nj);
@@ -407,9 +494,14 @@ cudaError_t launch_rotate(const RotateParams &p, bool halves, bool vec, cudaStre
 }
 
 template <typename T>
+cudaError_t launch_norm(const NormParams &p, cudaStream_t st) {
+  return launch(k_norm_any<T>, ((uint64_t)p.n * p.heads + 7) / 8, 0, st, p);
+}
+
+template <typename T, bool kNorm>
 cudaError_t launch_pack(const PackParams &p, bool halves, bool vec, cudaStream_t st) {
-  auto k = halves ? (vec ? k_pack<T, true, true> : k_pack<T, true, false>)
-                  : (vec ? k_pack<T, false, true> : k_pack<T, false, false>);
+  auto k = halves ? (vec ? k_pack<T, true, true, kNorm> : k_pack<T, true, false, kNorm>)
+                  : (vec ? k_pack<T, false, true, kNorm> : k_pack<T, false, false, kNorm>);
   // a warp takes more than one token once every SM has its 4 resident blocks (131,072 tokens
   // of bf16: 42.6 us, 5.6 TB/s, with 4; 53.6 / 46.3 / 47.5 / 43.5 with 2 / 3 / 6 / 8)
   const uint64_t blocks = ((uint64_t)p.n + 7) / 8, most = 4ull * sm_count();
@@ -446,12 +538,40 @@ extern "C" int ula_rows_rotate(const ula_rotary *rotary, uint32_t flags, const i
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 
-extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
-                             uint64_t pos_axis_stride, uint32_t n, uint32_t dtype,
-                             const void *d_latent, uint64_t latent_stride, const void *d_rope,
-                             uint64_t rope_stride, void *d_rows, uint64_t row_stride,
-                             void *stream) {
-  PackParams p{};
+extern "C" int ula_rows_norm_rotate(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride,
+                                    uint32_t n, uint32_t heads, uint32_t width, uint32_t at, uint32_t dtype,
+                                    const void *d_x, uint64_t x_token_stride, uint64_t x_head_stride,
+                                    const void *d_weight, uint32_t weight_dtype, float eps, void *d_out,
+                                    uint64_t out_token_stride, uint64_t out_head_stride, void *stream) {
+  NormParams p{};
+  if (!rotary_to_dev(rotary, &p.rot) || dtype > ULA_TYPE_F32 || (weight_dtype != dtype && weight_dtype != ULA_TYPE_F32) ||
+      width < ULA_ROW_ROPE || width > ULA_MAX_WIDTH || at > width - ULA_ROW_ROPE || !(eps >= 0.f && std::isfinite(eps)))
+    return ULA_ERR_INVALID_ARG;
+  const uint64_t work = (uint64_t)n * heads;
+  if (work == 0) return ULA_OK;
+  if (!d_pos || !d_x || !d_weight || !d_out || (work + 7) / 8 > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
+  if (!aligned(d_pos, 4) || !aligned(d_x, type_size(dtype)) || !aligned(d_out, type_size(dtype)) ||
+      !aligned(d_weight, type_size(weight_dtype)))
+    return ULA_ERR_INVALID_ARG;
+  if (overlap(n, out_token_stride, heads, out_head_stride, width)) return ULA_ERR_INVALID_ARG;
+  p.pos = d_pos, p.pos_axis_stride = pos_axis_stride, p.n = n, p.heads = heads, p.width = width, p.at = at;
+  p.x = d_x, p.xt = x_token_stride, p.xh = x_head_stride;
+  p.out = d_out, p.ot = out_token_stride, p.oh = out_head_stride;
+  p.weight = d_weight, p.weight_f32 = weight_dtype == ULA_TYPE_F32, p.halves = rotary->pairing == ULA_PAIR_HALVES;
+  p.eps = eps;
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_norm<__nv_bfloat16>(p, st)
+                        : dtype == ULA_TYPE_F16 ? launch_norm<__half>(p, st)
+                                                : launch_norm<float>(p, st);
+  return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+namespace {
+
+template <bool kNorm>
+int pack_rows(PackParams &p, const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride, uint32_t n,
+              uint32_t dtype, const void *d_latent, uint64_t latent_stride, const void *d_rope, uint64_t rope_stride,
+              void *d_rows, uint64_t row_stride, void *stream) {
   if (!rotary_to_dev(rotary, &p.rot) || dtype > ULA_TYPE_F32) return ULA_ERR_INVALID_ARG;
   if (n == 0) return ULA_OK;
   if (!d_pos || !d_latent || !d_rope || !d_rows || row_stride < ULA_ROW_BYTES || row_stride % 16)
@@ -466,10 +586,42 @@ extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
   const bool halves = rotary->pairing == ULA_PAIR_HALVES;
   const bool vec = aligned(d_latent, 16) && latent_stride * type_size(dtype) % 16 == 0;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_pack<__nv_bfloat16>(p, halves, vec, st)
-                        : dtype == ULA_TYPE_F16 ? launch_pack<__half>(p, halves, vec, st)
-                                                : launch_pack<float>(p, halves, vec, st);
+  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_pack<__nv_bfloat16, kNorm>(p, halves, vec, st)
+                        : dtype == ULA_TYPE_F16 ? launch_pack<__half, kNorm>(p, halves, vec, st)
+                                                : launch_pack<float, kNorm>(p, halves, vec, st);
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos,
+                             uint64_t pos_axis_stride, uint32_t n, uint32_t dtype,
+                             const void *d_latent, uint64_t latent_stride, const void *d_rope,
+                             uint64_t rope_stride, void *d_rows, uint64_t row_stride,
+                             void *stream) {
+  PackParams p{};
+  return pack_rows<false>(p, rotary, d_pos, pos_axis_stride, n, dtype, d_latent, latent_stride, d_rope, rope_stride,
+                          d_rows, row_stride, stream);
+}
+
+extern "C" int ula_rows_pack_norm(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_axis_stride,
+                                  uint32_t n, uint32_t dtype, const void *d_latent, uint64_t latent_stride,
+                                  const void *d_rope, uint64_t rope_stride, const void *d_latent_weight,
+                                  uint32_t latent_weight_dtype, const void *d_rope_weight, uint32_t rope_weight_dtype,
+                                  float eps, void *d_rows, uint64_t row_stride, void *stream) {
+  PackParams p{};
+  if (dtype > ULA_TYPE_F32 || (latent_weight_dtype != dtype && latent_weight_dtype != ULA_TYPE_F32) ||
+      (d_rope_weight && rope_weight_dtype != dtype && rope_weight_dtype != ULA_TYPE_F32) ||
+      !(eps >= 0.f && std::isfinite(eps)))
+    return ULA_ERR_INVALID_ARG;
+  if (n && (!d_latent_weight || !aligned(d_latent_weight, type_size(latent_weight_dtype)) ||
+            (d_rope_weight && !aligned(d_rope_weight, type_size(rope_weight_dtype)))))
+    return ULA_ERR_INVALID_ARG;
+  p.latent_weight = d_latent_weight, p.latent_weight_f32 = latent_weight_dtype == ULA_TYPE_F32;
+  p.rope_weight = d_rope_weight, p.rope_weight_f32 = rope_weight_dtype == ULA_TYPE_F32;
+  p.eps = eps;
+  return pack_rows<true>(p, rotary, d_pos, pos_axis_stride, n, dtype, d_latent, latent_stride, d_rope, rope_stride,
+                         d_rows, row_stride, stream);
 }
 
 extern "C" int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t parts,

@@ -110,6 +110,33 @@ def pack(latent: torch.Tensor, rope: torch.Tensor, pos: torch.Tensor, rotary: Ro
     return _rows.pack(latent, rope, pos, rotary.config, rows)
 
 
+def norm_rotate(x: torch.Tensor, weight: torch.Tensor, pos: torch.Tensor, rotary: Rotary, *,
+                eps: float = 1e-6, at: int | None = None, out: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Norms the heads of x [tokens][heads][width] (or [tokens][width]; bf16, f16 or f32; width 64 to
+    1024) and turns their rope channels, in one pass: y = x / sqrt(mean(x^2) + eps) * weight over
+    a head's channels, then y's channels at..at + 63 (default: the last 64) as by ``rotate``.
+
+    weight: [width] of x's type or float32.  pos: int32 [axes][tokens] (or [tokens]).  out: x itself
+    (in place) or another tensor of x's shape and type, whose tokens and heads may not share memory.
+    """
+    if stream is not None:
+        return _on(stream, _rows.norm_rotate, x, weight, pos, rotary.config, eps, at, out)
+    return _rows.norm_rotate(x, weight, pos, rotary.config, eps, at, out)
+
+
+def pack_norm(latent: torch.Tensor, rope: torch.Tensor, latent_weight: torch.Tensor, pos: torch.Tensor,
+              rotary: Rotary, rows: torch.Tensor | None = None, *,
+              rope_weight: torch.Tensor | None = None, eps: float = 1e-6,
+              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """``pack`` with the key's norm in the same pass: the latents become x / sqrt(mean(x^2) + eps) *
+    latent_weight before they are quantised, and with rope_weight the rope channels as much before they
+    are turned.  Weights: [512] and [64], of the latent's type or float32."""
+    if stream is not None:
+        return _on(stream, _rows.pack_norm, latent, rope, latent_weight, pos, rotary.config, eps, rope_weight, rows)
+    return _rows.pack_norm(latent, rope, latent_weight, pos, rotary.config, eps, rope_weight, rows)
+
+
 def attend(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax_scale: float, *,
            own_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
            lse: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
@@ -128,6 +155,24 @@ def attend(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax
     return _rows.attend(q, rows, entry_row, softmax_scale, own_rows, out, lse)
 
 
+def attend_tree(q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor, softmax_scale: float,
+                own_rows: torch.Tensor, parent: torch.Tensor, *, out: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Attention of a tree of drafted tokens over the rows a step gathered; returns (out, lse).
+
+    As ``attend``, with query token i of a request as node i of its tree (at most 64 nodes): it sees
+    its entries' rows and the own rows of i, parent[r, i], that node's parent, and so on.
+    parent: int32 [R][Q]; a value that is not an earlier node's, such as -1, stands for none.
+    entry_row: int32 [R][Q][K], a list for each node, or [R][K], one that all nodes of a request's
+    tree share (its rows are then read once for all their query heads).
+    An own row with NaN codes or scales that are not finite gives NaN to the nodes that see it, and
+    counts for nothing for the others.
+    """
+    if stream is not None:
+        return _on(stream, _rows.attend_tree, q, rows, entry_row, softmax_scale, own_rows, parent, out, lse)
+    return _rows.attend_tree(q, rows, entry_row, softmax_scale, own_rows, parent, out, lse)
+
+
 def join(outs, lses, *, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
          stream: torch.cuda.Stream | None = None):
     """Joins partial results over disjoint rows (at most 8 parts): lists of ``attend``'s outs
@@ -136,6 +181,39 @@ def join(outs, lses, *, out: torch.Tensor | None = None, lse: torch.Tensor | Non
     if stream is not None:
         return _on(stream, _rows.join, outs, lses, out, lse)
     return _rows.join(outs, lses, out, lse)
+
+
+def score(scores: torch.Tensor, q: torch.Tensor, rows: torch.Tensor, entry_row: torch.Tensor,
+          address: torch.Tensor, lse: torch.Tensor, softmax_scale: float, *,
+          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Accumulates attention weights by logical address, in place: for every query token's entry e,
+    scores[address[e]] += sum over heads of exp(logit[e] - lse).  Returns scores.
+
+    scores: float32 [addresses].  q, rows, entry_row: ``attend``'s (or ``attend_tree``'s, [R][K] too).
+    address: int32 of entry_row's shape, the selection that ``step_group`` got.  lse: float32
+    [R][Q][H], the attention's (joined with other parts: weights of the whole).  Entries whose row or
+    address is out of range count for nothing, and so do query tokens whose lse is -inf.  The result does
+    not depend on the order in which an address's weights are added.
+    """
+    if stream is not None:
+        return _on(stream, _rows.score, scores, q, rows, entry_row, address, lse, softmax_scale)
+    return _rows.score(scores, q, rows, entry_row, address, lse, softmax_scale)
+
+
+def evict(scores: torch.Tensor, address: torch.Tensor, length: torch.Tensor, budget: int, *,
+          first: int = 0, last: int = 0, kept: torch.Tensor | None = None,
+          dropped: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Which of each request's logical addresses stay within a budget; returns (kept, dropped).
+
+    address: int32 [R][N], a request's addresses, oldest first, of which length [R] (int32) count.
+    The first ``first`` and the last ``last`` stay, and of the others those with the largest
+    scores (float32 [addresses]), min(length, budget) in all; where scores are equal the older ones
+    leave.  kept: int32 [R][budget], dropped: int32 [R][max(N - budget, 0)] (for
+    ``UlaCache.free``), in the list's order, -1 behind.
+    """
+    if stream is not None:
+        return _on(stream, _rows.evict, scores, address, length, budget, first, last, kept, dropped)
+    return _rows.evict(scores, address, length, budget, first, last, kept, dropped)
 
 
 def sync(stream: torch.cuda.Stream | None = None) -> None:

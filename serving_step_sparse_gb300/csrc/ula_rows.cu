@@ -217,8 +217,158 @@ __device__ __forceinline__ float inverse_rms(float ss, float width, float eps) {
   return __frsqrt_rn(__fdiv_rn(ss, width) + eps);
 }
 
-// Any alignment, strides and widths: one warp per token and head, which reads its channels twice; a lane turns
-// a pair.  (In place: a lane writes the channels that it alone reads in the second pass.)
+// The sum over a row's 8 lanes, in every one of them.
+__device__ __forceinline__ float sum8(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  return v + __shfl_xor_sync(0xffffffffu, v, 4);
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ uint4 load_chunk(const T *x) {
+  uint4 u;
+  if (kVec) return *reinterpret_cast<const uint4 *>(x);
+  T *e = reinterpret_cast<T *>(&u);
+#pragma unroll
+  for (int k = 0; k < Vec<T>::n; ++k) e[k] = x[k];
+  return u;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_chunk(T *o, const uint4 &u) {
+  if (kVec) {
+    *reinterpret_cast<uint4 *>(o) = u;
+    return;
+  }
+  const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+  for (int k = 0; k < Vec<T>::n; ++k) o[k] = e[k];
+}
+
+// Bound by its bytes: every channel is read and written once, in 16-byte chunks.  Eight lanes take a row
+// (a token's head): lane l holds the rope chunks l (and l + 8 in fp32), so that a pair's halves are in one
+// lane or in lanes l and l ^ 4, and the chunks l, l + 8, ... of the others; kSlots in all.  The block's
+// sines and weights stand in shared memory, once for all its rows; kItems rows per thread have their
+// loads in flight together.  kVec: 16-byte accesses; without it (bases or strides that do not allow
+// them) the same values by single elements, so that a result's bits do not depend on the alignment.
+template <typename T, int kSlots, int kItems, bool kVec>
+__global__ void __launch_bounds__(256) k_norm_vec(const __grid_constant__ NormParams p) {
+  constexpr int V = Vec<T>::n, kRope = ULA_ROW_ROPE / V / 8;  // slots of rope chunks
+  constexpr uint32_t kStep = 32, kRows = kStep * kItems;
+  extern __shared__ float4 table4[];                   // [tokens of the block][32] (cos, sin), then [width] weights
+  float2 *table = reinterpret_cast<float2 *>(table4);
+  const uint64_t all = (uint64_t)p.n * p.heads, row0 = (uint64_t)blockIdx.x * kRows;
+  const uint64_t last = row0 + kRows < all ? row0 + kRows - 1 : all - 1;
+  const uint32_t t0 = (uint32_t)(row0 / p.heads), t1 = (uint32_t)(last / p.heads);
+  const uint32_t h0 = (uint32_t)(row0 - (uint64_t)t0 * p.heads);
+  const uint32_t l = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+  const uint32_t others = p.width / V - ULA_ROW_ROPE / V, at = p.at / V;  // (chunks)
+  float *weight = reinterpret_cast<float *>(table + (t1 - t0 + 1) * kPairs);
+  after_previous();
+  auto chunk = [&](int s) -> uint32_t {  // slot s's chunk
+    if (s < kRope) return at + l + 8 * s;
+    const uint32_t n = l + 8 * (s - kRope);
+    return n < at ? n : n + ULA_ROW_ROPE / V;
+  };
+  auto there = [&](int s) { return s < kRope || l + 8 * (s - kRope) < others; };
+  uint4 raw[kItems][kSlots];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const uint32_t r = h0 + r0 + i * kStep, tok = r / p.heads;
+    const T *x = (const T *)p.x + (t0 + tok) * p.xt + (r - tok * p.heads) * p.xh;
+    const bool in = row0 + r0 + i * kStep < all;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      raw[i][s] = make_uint4(0, 0, 0, 0);
+      if (in && there(s)) raw[i][s] = load_chunk<T, kVec>(x + chunk(s) * V);
+    }
+  }
+  const int32_t *pos = p.pos + p.rot.axis[threadIdx.x & 31] * p.pos_axis_stride + t0;
+  const unsigned long long step = p.rot.step[threadIdx.x & 31];
+  for (uint32_t k = threadIdx.x; k < (t1 - t0 + 1) * kPairs; k += 256) table[k] = turn_of(step, pos[k >> 5]);
+  for (uint32_t k = threadIdx.x; k < p.width; k += 256) weight[k] = weight_at<T>(p.weight, p.weight_f32, k);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const uint32_t r = h0 + r0 + i * kStep, tok = r / p.heads;
+    const bool in = row0 + r0 + i * kStep < all;
+    float ss = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      float v[V];
+      Vec<T>::open(raw[i][s], v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) ss = fmaf(v[k], v[k], ss);
+    }
+    const float inv = inverse_rms(sum8(ss), (float)p.width, p.eps);
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)  // (opened again below, not kept in fp32 beside the chunks)
+      asm volatile("" : "+r"(raw[i][s].x), "+r"(raw[i][s].y), "+r"(raw[i][s].z), "+r"(raw[i][s].w));
+    T *o = (T *)p.out + (t0 + tok) * p.ot + (r - tok * p.heads) * p.oh;
+    auto normed = [&](int s, float (&v)[V]) {
+      Vec<T>::open(raw[i][s], v);
+      const float *w = weight + chunk(s) * V;
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 w4 = *reinterpret_cast<const float4 *>(w + k);
+        v[k] = v[k] * inv * w4.x, v[k + 1] = v[k + 1] * inv * w4.y;
+        v[k + 2] = v[k + 2] * inv * w4.z, v[k + 3] = v[k + 3] * inv * w4.w;
+      }
+    };
+    const float4 *tb = table4 + (in ? tok : 0) * (kPairs / 2);
+    float a[V], b[V], oa[V], ob[V];
+    normed(0, a);
+    if (kRope == 2) normed(1, b);
+    if (p.halves) {
+      if (kRope == 2) {  // chunks l and l + 8: the halves of V pairs
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float4 cs = tb[(l * V + k) / 2];
+          turn(a[k], b[k], cs.x, cs.y, oa[k], ob[k]);
+          turn(a[k + 1], b[k + 1], cs.z, cs.w, oa[k + 1], ob[k + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float4 cs = tb[((l & 3) * V + k) / 2];
+          const float o0 = __shfl_xor_sync(0xffffffffu, a[k], 4), o1 = __shfl_xor_sync(0xffffffffu, a[k + 1], 4);
+          float x, y;  // (the other lane's)
+          if (l < 4) {
+            turn(a[k], o0, cs.x, cs.y, oa[k], x);
+            turn(a[k + 1], o1, cs.z, cs.w, oa[k + 1], y);
+          } else {
+            turn(o0, a[k], cs.x, cs.y, x, oa[k]);
+            turn(o1, a[k + 1], cs.z, cs.w, y, oa[k + 1]);
+          }
+        }
+      }
+    } else {
+      auto turn_pairs = [&](const float (&v)[V], float (&w)[V], uint32_t pair0) {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+          const float4 cs = tb[(pair0 + k / 2) / 2];
+          turn(v[k], v[k + 1], cs.x, cs.y, w[k], w[k + 1]);
+          turn(v[k + 2], v[k + 3], cs.z, cs.w, w[k + 2], w[k + 3]);
+        }
+      };
+      turn_pairs(a, oa, l * (V / 2));
+      if (kRope == 2) turn_pairs(b, ob, kPairs / 2 + l * (V / 2));
+    }
+    if (in) {
+      store_chunk<T, kVec>(o + chunk(0) * V, Vec<T>::close(oa));
+      if (kRope == 2) store_chunk<T, kVec>(o + chunk(1) * V, Vec<T>::close(ob));
+    }
+#pragma unroll
+    for (int s = kRope; s < kSlots; ++s) {
+      if (!(in && there(s))) continue;
+      normed(s, a);
+      store_chunk<T, kVec>(o + chunk(s) * V, Vec<T>::close(a));
+    }
+  }
+}
+
+// Widths or places of the rope channels that do not divide into 16-byte chunks, and rows of more than 16
+// slots (fp32 heads wider than 512): one warp per token and head, which reads its channels twice; a lane
+// turns a pair.  (In place: a lane writes the channels that it alone reads in the second pass.)
 template <typename T>
 __global__ void __launch_bounds__(256) k_norm_any(const __grid_constant__ NormParams p) {
   const uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -493,8 +643,30 @@ cudaError_t launch_rotate(const RotateParams &p, bool halves, bool vec, cudaStre
   return launch(halves ? k_rotate_any<T, true> : k_rotate_any<T, false>, blocks, 0, st, p);
 }
 
+template <typename T, int kSlots>
+cudaError_t launch_norm_slots(const NormParams &p, bool vec, cudaStream_t st) {
+  const uint64_t all = (uint64_t)p.n * p.heads;
+  constexpr int most = kSlots <= 4 ? 2 : 1;
+  const bool many = vec && p.heads >= 8 && all >= 2ull * 32 * 4 * sm_count();
+  const uint32_t rows = 32 * (many ? most : 1);
+  const uint32_t tokens = (rows - 1) / p.heads + 2;  // at most, whatever the first row
+  return launch(!vec ? k_norm_vec<T, kSlots, 1, false> : many ? k_norm_vec<T, kSlots, most, true> : k_norm_vec<T, kSlots, 1, true>,
+                (all + rows - 1) / rows, tokens * kPairs * 8 + p.width * 4, st, p);
+}
+
+// Slots: the fewest that hold a row's 16-byte chunks by eights.
 template <typename T>
-cudaError_t launch_norm(const NormParams &p, cudaStream_t st) {
+cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t st) {
+  constexpr uint32_t V = Vec<T>::n;
+  const uint32_t rope = ULA_ROW_ROPE / V / 8, slots = rope + (p.width / V - ULA_ROW_ROPE / V + 7) / 8;
+  if (p.width % V == 0 && p.at % V == 0 && slots <= 16)
+    return slots <= 1   ? launch_norm_slots<T, V == 8 ? 1 : 2>(p, vec, st)
+           : slots <= 2 ? launch_norm_slots<T, 2>(p, vec, st)
+           : slots <= 3 ? launch_norm_slots<T, 3>(p, vec, st)
+           : slots <= 4 ? launch_norm_slots<T, 4>(p, vec, st)
+           : slots <= 6 ? launch_norm_slots<T, 6>(p, vec, st)
+           : slots <= 9 ? launch_norm_slots<T, 9>(p, vec, st)
+                        : launch_norm_slots<T, 16>(p, vec, st);
   return launch(k_norm_any<T>, ((uint64_t)p.n * p.heads + 7) / 8, 0, st, p);
 }
 
@@ -559,10 +731,12 @@ extern "C" int ula_rows_norm_rotate(const ula_rotary *rotary, const int32_t *d_p
   p.out = d_out, p.ot = out_token_stride, p.oh = out_head_stride;
   p.weight = d_weight, p.weight_f32 = weight_dtype == ULA_TYPE_F32, p.halves = rotary->pairing == ULA_PAIR_HALVES;
   p.eps = eps;
+  const uint64_t strides = x_token_stride | x_head_stride | out_token_stride | out_head_stride;
+  const bool vec = aligned(d_x, 16) && aligned(d_out, 16) && strides * type_size(dtype) % 16 == 0;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_norm<__nv_bfloat16>(p, st)
-                        : dtype == ULA_TYPE_F16 ? launch_norm<__half>(p, st)
-                                                : launch_norm<float>(p, st);
+  const cudaError_t e = dtype == ULA_TYPE_BF16  ? launch_norm<__nv_bfloat16>(p, vec, st)
+                        : dtype == ULA_TYPE_F16 ? launch_norm<__half>(p, vec, st)
+                                                : launch_norm<float>(p, vec, st);
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }
 

@@ -640,8 +640,9 @@ int ula_rows_join(const void *const *outs, const float *const *lses, uint32_t pa
 
 /*
  * ula_rows_sync -- wait for `stream` (of the current device), then return ULA_OK, or
- * ULA_ERR_TIMEOUT if a bounded wait of an ula_rows_attend call has expired since the
- * stream's last ula_rows_sync: the outputs of some call are not valid.  The error is the
+ * ULA_ERR_TIMEOUT if a bounded wait of an ula_rows_attend, ula_rows_attend_tree or
+ * ula_rows_score call has expired since the stream's last ula_rows_sync: the outputs of some call
+ * are not valid.  The error is the
  * device's: every stream's next sync returns it once, whichever stream the call was on
  * (a stream that waits for another's results, or replays a graph, gets it as well).
  */
@@ -652,6 +653,9 @@ int ula_rows_sync(void *stream);
  * run out (after about a second) on a working GPU and the kernel's way out is taken. */
 #define ULA_DEBUG_BARRIERS 23
 int ula_rows_debug_hold(int barrier);
+/* The same for ula_rows_score and its barriers. */
+#define ULA_DEBUG_SCORE_BARRIERS 26
+int ula_rows_debug_hold_score(int barrier);
 
 /*
  * TP mode, emulated on one GPU (§2 "Unified logical addresses", TP paragraph): the

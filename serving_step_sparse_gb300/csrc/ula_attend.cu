@@ -1079,12 +1079,13 @@ extern "C" int ula_rows_sync(void *stream) {
   static std::mutex lock;
   static std::map<std::pair<int, unsigned long long>, uint32_t> seen;
   cudaStream_t st = (cudaStream_t)stream;
-  uint32_t late = 0;
+  uint32_t late = 0, late_scores = 0;
   int device = 0;
   unsigned long long id = 0;
   if (cudaMemcpyFromSymbolAsync(&late, g_late, sizeof late, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
+      score_late(&late_scores, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
     return ULA_ERR_CUDA;
+  late += late_scores;
   if (late == 0) return ULA_OK;
   if (cudaGetDevice(&device) != cudaSuccess || cudaStreamGetId(st, &id) != cudaSuccess) return ULA_ERR_CUDA;
   try {

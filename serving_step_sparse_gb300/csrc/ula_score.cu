@@ -7,6 +7,7 @@
 // at the addresses in question, the weights are added, and each sum is taken by the first entry that
 // finds it.
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cmath>
 
 #include "ula.h"
@@ -20,6 +21,9 @@ struct ScoreParams {
   ula_score_args a;
   uint32_t lists, nodes;        // lists, and the query tokens of each
   unsigned long long *sums;     // [n_scores]
+  unsigned long long total;     // tiles of all items
+  uint32_t tiles, column_tiles; // of an item; of a list
+  uint32_t hold;                // (test hook) an mbarrier whose phases never end; kBars: none
   float c0, unit;               // softmax_scale * log2(e); what 1.0 is in fixed point
 };
 
@@ -50,54 +54,336 @@ __global__ void __launch_bounds__(256) k_score_commit(const __grid_constant__ Sc
   }
 }
 
-// A warp per entry: lane l holds latents 16l..16l+15 and two rope channels.
-__global__ void __launch_bounds__(256) k_score(const __grid_constant__ ScoreParams p) {
+// ---------------------------------------------------------------- the weights
+
+constexpr uint32_t kTile = 128;                      // rows per tile
+constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
+constexpr uint32_t kPieces = 5;                      // of a tile: 4 blocks of latents, the rope channels
+constexpr uint32_t kStageBytes = 2 * kGroupBytes;
+constexpr uint32_t kBufs = 4;                        // accumulators in TMEM
+constexpr uint32_t kEnd = 8, kWiden = 8;             // warps that finish the logits, that widen rows (in two groups)
+constexpr uint32_t kIssue = 2;                       // and that issue products; then one that looks rows up
+constexpr uint32_t kThreads = (kEnd + kWiden + 4) * 32;  // (registers move between groups of 4 warps)
+// Launched with 96 registers a thread: 5 * 96 = 2 * 128 + 2 * 88 + 48.
+constexpr uint32_t kRegsEnd = 128, kRegsWiden = 88, kRegsIssue = 48;
+__device__ uint32_t g_late;                          // warps whose waits ran out, in all launches so far
+
+// mbarriers.  Full, Empty: a stage holds a piece, its products have ended; Done, Drained: an
+// accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
+// Free: both have been read; Query: the item's queries; Idle: the item's products have ended; End: an
+// issuing warp's have.  (A wait names its phase by its parity alone, so whoever waits for a phase has
+// waited for the one before it: pieces alternate between the groups, and the numbers of stages and
+// accumulators are even.)
+constexpr uint32_t kMostStages = 4;
+enum {
+  kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kBufs,
+  kBarPlace = kBarDrained + kBufs, kBarScale = kBarPlace + 2, kBarFree = kBarScale + 2, kBarQuery = kBarFree + 2,
+  kBarIdle = kBarQuery + 1, kBarEnd = kBarIdle + 1, kBars = kBarEnd + kIssue
+};
+static_assert(kBars == ULA_DEBUG_SCORE_BARRIERS, "as the header says");
+
+template <uint32_t NC>
+struct Shared {
+  static constexpr uint32_t stages = NC == 128 ? 2 : kMostStages;
+  static constexpr uint32_t q = 0;                                  // [9][NC][128 B]
+  static constexpr uint32_t ring = 9 * NC * 128;                    // [stages][2][128][128 B]
+  static constexpr uint32_t scale = ring + stages * kStageBytes;    // [2][128][4]
+  static constexpr uint32_t place = scale + 2 * kTile * 16;         // [2][128] the rows' addresses, 0: none
+  static constexpr uint32_t target = place + 2 * kTile * 8;         // [2][128] their places in scores
+  static constexpr uint32_t lse = target + 2 * kTile * 4;           // [2][NC] in units of log2
+  static constexpr uint32_t bars = lse + 2 * NC * 4;
+  static constexpr uint32_t words = bars + kBars * 8;
+  static constexpr uint32_t bytes = words + 16 + 1024;              // (+ alignment of the base)
+};
+
+// The tiles of a block: items (a list and a tile of its columns) in order, an even share of all tiles.
+struct Place {
+  uint32_t item, tile;
+};
+
+// S^T[128 rows][NC columns] = C_b Q_b^T for the four blocks of latents and the rope channels, as in the
+// attention (ula_attend.cu): codes widened to bf16, exact, and scaled in fp32 as the accumulators are
+// read.  Nothing but the sum over a row's columns of exp2(z - lse) leaves the block, so the pieces of a
+// tile stream: two groups of four warps widen every other piece into a ring of stages, two warps issue
+// its products into a ring of four accumulators, eight warps take them up, a row per thread and half of
+// the columns, and add a row's weights to its sum.
+template <uint32_t NC>
+__global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ ScoreParams p) {
+  extern __shared__ uint8_t raw_smem[];
+  using L = Shared<NC>;
+  constexpr uint32_t S = L::stages;
+  constexpr int HG = NC / 2;
+  const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+  uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < kMostStages; ++i) mbar_init(bar(kBarFull + i), kWiden / 2), mbar_init(bar(kBarEmpty + i), 1);
+    for (uint32_t i = 0; i < kBufs; ++i) mbar_init(bar(kBarDone + i), 1), mbar_init(bar(kBarDrained + i), kEnd);
+    for (uint32_t i = 0; i < 2; ++i)
+      mbar_init(bar(kBarPlace + i), 1), mbar_init(bar(kBarScale + i), 32), mbar_init(bar(kBarFree + i), kEnd + kWiden);
+    mbar_init(bar(kBarQuery), kWiden), mbar_init(bar(kBarIdle), kIssue);
+    for (uint32_t i = 0; i < kIssue; ++i) mbar_init(bar(kBarEnd + i), 1);
+    if (p.hold < kBars) {
+      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(p.hold)) : "memory");
+      mbar_init(bar(p.hold), 1u << 19);  // (more arrivals than a launch makes)
+    }
+    fence_async_smem();
+  }
+  // (what is read before its time, after a wait that ran out, is no address)
+  for (uint32_t i = threadIdx.x; i < 2 * kTile; i += kThreads) {
+    reinterpret_cast<uint64_t *>(sm + L::place)[i] = 0;
+    reinterpret_cast<uint32_t *>(sm + L::target)[i] = 0xffffffffu;
+  }
+  if (warp == kEnd + kWiden) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + L::words), "n"(kBufs * NC) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + L::words);
+  const unsigned long long from = p.total * blockIdx.x / gridDim.x;
+  const uint32_t count = (uint32_t)(p.total * (blockIdx.x + 1) / gridDim.x - from);
+  Place w;
+  w.item = (uint32_t)(from / p.tiles), w.tile = (uint32_t)(from - (unsigned long long)w.item * p.tiles);
+  auto step = [&]() {
+    if (++w.tile == p.tiles) w.tile = 0, ++w.item;
+  };
   after_previous();
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t n = (uint64_t)p.lists * p.a.k;
-  const uint64_t e = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (e >= n) return;
-  const uint32_t list = (uint32_t)(e / p.a.k);
-  const uint32_t u = (uint32_t)__ldg(p.a.entry_row + e), to = (uint32_t)__ldg(p.a.address + e);
-  if (u >= p.a.n_rows || to >= p.a.n_scores) return;
-  const uint8_t *row = (const uint8_t *)p.a.rows + (uint64_t)u * ULA_ROW_BYTES;
-  const uint4 codes = reinterpret_cast<const uint4 *>(row)[lane];
-  const float scale = reinterpret_cast<const float *>(row + ULA_ROW_LATENT)[lane >> 3];
-  const uint32_t rope = reinterpret_cast<const uint32_t *>(row + ULA_ROW_LATENT + 16)[lane];
-  float v[18];
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+
+  bool ok = true;  // false once a wait has run out
+  if (warp < kEnd) {
+    // ---- logits, weights, sums: this thread's row and HG columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEnd));
+    const uint32_t quad = warp & 3, grp = warp >> 2, mine = 32 * quad + lane;
+    const uint32_t lanes = tmem + (quad << 21) + grp * HG;
+    uint32_t items = 0;
+    for (uint32_t n = 0; n < count; ++n, step()) {
+      const uint32_t par = n & 1;
+      if (n == 0 || w.tile == 0) {
+        if (!(ok = warp_wait(bar(kBarQuery), items & 1))) break;
+        ++items;
+      }
+      ok = warp_wait(bar(kBarPlace + par), (n >> 1) & 1);
+      if (!(ok = ok && warp_wait(bar(kBarScale + par), (n >> 1) & 1))) break;
+      const float4 s4 = *reinterpret_cast<const float4 *>(sm + L::scale + (par * kTile + mine) * 16);
+      const uint32_t target = reinterpret_cast<const uint32_t *>(sm + L::target)[par * kTile + mine];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarFree + par));
+      float z[HG];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (uint32_t b = 0; b < kPieces; ++b) {
+        const uint32_t g = n * kPieces + b, buf = g % kBufs;
+        if (!(ok = warp_wait(bar(kBarDone + buf), (g / kBufs) & 1))) break;
+        tc_fence_after();
+        const float s = (b == 0 ? s4.x : b == 1 ? s4.y : b == 2 ? s4.z : b == 3 ? s4.w : 1.f) * p.c0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t two = codes_to_bf16(w[i] >> (16 * h));
-      v[4 * i + 2 * h] = __uint_as_float(two << 16), v[4 * i + 2 * h + 1] = __uint_as_float(two & 0xffff0000u);
+        for (int c = 0; c < HG; c += 16) {
+          float v[16];
+          tmem_ld<16>(lanes + buf * NC + c, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 16; h += 2) {
+            if (b == 0) mul2(z[c + h], z[c + h + 1], s, v[h], v[h + 1]);
+            else fma2(z[c + h], z[c + h + 1], s, v[h], v[h + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarDrained + buf));
+      }
+      if (!ok) break;
+      // a weight is between 0 and 1, and 0 where it is not a number (what .sat makes of one)
+      const float *lse = reinterpret_cast<const float *>(sm + L::lse) + ((items - 1) & 1) * NC + grp * HG;
+      float total = 0.f;
+#pragma unroll
+      for (int c = 0; c < HG; c += 4) {
+        const float4 l = *reinterpret_cast<const float4 *>(lse + c);
+        total += (__saturatef(ex2(z[c] - l.x)) + __saturatef(ex2(z[c + 1] - l.y))) +
+                 (__saturatef(ex2(z[c + 2] - l.z)) + __saturatef(ex2(z[c + 3] - l.w)));
+      }
+      if (target != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target, __float2ull_rn(total * p.unit));
     }
-  v[16] = __uint_as_float(rope << 16), v[17] = __uint_as_float(rope & 0xffff0000u);
-  const uint32_t req = list * p.nodes / p.a.n_q, first = list * p.nodes - req * p.a.n_q;
-  float total = 0.f;
-  for (uint32_t i = first; i < first + p.nodes; ++i)
-    for (uint32_t h = 0; h < p.a.heads; ++h) {
-      const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + req * p.a.q_req_stride + i * p.a.q_tok_stride + h * p.a.q_head_stride;
-      float x = 0.f;
+  } else if (warp < kEnd + kWiden) {
+    // ---- widening: group `grp` takes pieces grp, grp + 2, ...; a warp 32 rows, a lane of it every
+    // fourth, 16 bytes of a row's 128.  The next piece's loads are issued once this one's registers are free.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    const uint32_t cw = warp - kEnd, grp = cw >> 2, r0 = 32 * (cw & 3) + (lane >> 3), ch = lane & 7;
+    const uint32_t pieces = count * kPieces;
+    uint4 raw[8];
+    auto fetch = [&](uint32_t g) -> bool {
+      const uint32_t n = g / kPieces, b = g - n * kPieces, par = n & 1;
+      if (!warp_wait(bar(kBarPlace + par), (n >> 1) & 1)) return false;
+      const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile;
+      const uint32_t at = (b < 4 ? b * 128 : ULA_ROW_LATENT + 16) + ch * 16;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) x = fmaf(__bfloat162float(q[16 * lane + c]), v[c], x);
-      x = x * scale + __bfloat162float(q[512 + 2 * lane]) * v[16] + __bfloat162float(q[513 + 2 * lane]) * v[17];
+      for (uint32_t j = 0; j < 8; ++j) {
+        const uint64_t row = place[r0 + 4 * j];
+        raw[j] = make_uint4(0, 0, 0, 0);
+        if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + at));
+      }
+      if ((g + 2) / kPieces != n) {  // (the group's last piece of the tile)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarFree + par));
+      }
+      return true;
+    };
+    uint32_t items = 0, tile = 0;  // `tile`: the tile whose item's queries stand
+    ok = grp >= pieces || fetch(grp);
+    for (uint32_t g = grp; g < pieces && ok; g += 2) {
+      const uint32_t n = g / kPieces, b = g - n * kPieces;
+      for (; tile < n; ++tile) step();
+      if (b < 2 && (n == 0 || w.tile == 0)) {
+        // the item's queries, once the products that read the last one's have ended
+        if (items && !(ok = warp_wait(bar(kBarIdle), (items - 1) & 1))) break;
+        const uint32_t list = w.item / p.column_tiles, c0 = (w.item - list * p.column_tiles) * NC;
+        const uint32_t req = list * p.nodes / p.a.n_q, first = list * p.nodes - req * p.a.n_q;
+        const uint32_t columns = p.nodes * p.a.heads;
+        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + req * p.a.q_req_stride;
+        for (uint32_t i = cw * 32 + lane; i < NC * 72; i += kWiden * 32) {
+          const uint32_t h = i / 72, c = i - h * 72;
+          const uint32_t dst = base + L::q + (c >> 3) * (NC * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
+          const bool in = c0 + h < columns;
+          const uint32_t node = (c0 + h) / p.a.heads, head = c0 + h - node * p.a.heads;
+          copy16(dst, q + (in ? (first + node) * p.a.q_tok_stride + head * p.a.q_head_stride + c * 8 : 0), in ? 16 : 0);
+        }
+        for (uint32_t h = cw * 32 + lane; h < NC; h += kWiden * 32) {
+          const float l = c0 + h < columns ? __ldg(p.a.lse + (uint64_t)list * columns + c0 + h) : -INFINITY;
+          // (a column without an lse: exp2(z - inf) is 0)
+          reinterpret_cast<float *>(sm + L::lse)[(items & 1) * NC + h] = l > -INFINITY ? l * 1.44269504088896341f : INFINITY;
+        }
+        ++items;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarQuery));
+      }
+      const uint32_t st = g % S;
+      if (g >= S && !(ok = warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1))) break;
+      uint8_t *stage = sm + L::ring + st * kStageBytes;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      const float lse = __ldg(p.a.lse + ((uint64_t)req * p.a.n_q + i) * p.a.heads + h);
-      const float w1 = ex2(x * p.c0 - lse * 1.44269504088896341f);
-      total += lse == -INFINITY || !(w1 > 0.f) ? 0.f : fminf(w1, 1.f);
+      for (uint32_t j = 0; j < 8; ++j) {
+        const uint32_t r = r0 + 4 * j, x = r & 7;
+        const uint4 v = raw[j];
+        if (b == 4) {
+          *reinterpret_cast<uint4 *>(stage + r * 128 + ((ch ^ x) << 4)) = v;
+        } else {
+          // (16-byte accesses are served by quarters of a warp, here one row's: the lanes of the second
+          // half store their second chunk first, so that all eight lie in different banks)
+          uint8_t *at = stage + (ch >> 2) * kGroupBytes + r * 128;
+          const bool up = ch & 4;
+          const uint32_t c = 2 * (ch & 3) + (up ? 1 : 0);
+          const uint32_t p0 = up ? v.z : v.x, p1 = up ? v.w : v.y, q0 = up ? v.x : v.z, q1 = up ? v.y : v.w;
+          *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
+              make_uint4(codes_to_bf16(p0), codes_to_bf16(p0 >> 16), codes_to_bf16(p1), codes_to_bf16(p1 >> 16));
+          *reinterpret_cast<uint4 *>(at + ((c ^ 1 ^ x) << 4)) =
+              make_uint4(codes_to_bf16(q0), codes_to_bf16(q0 >> 16), codes_to_bf16(q1), codes_to_bf16(q1 >> 16));
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarFull + st));
+      if (g + 2 < pieces) ok = fetch(g + 2);
     }
-  if (lane == 0 && total > 0.f) atomicAdd(p.sums + to, __float2ull_rn(total * p.unit));
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kEnd + kWiden + kIssue) {
+    // ---- products, every other piece.  (A wait that has run out does not leave the loop, so that the
+    // descriptors stay in uniform registers; it is reported at the end.)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    const uint32_t which = warp - kEnd - kWiden;
+    constexpr uint32_t kId = (1u << 4) | (1u << 7) | (1u << 10) | ((NC >> 3) << 17) | ((kTile >> 4) << 24);  // D fp32, A and B bf16
+    const uint64_t rows = operand(base + L::ring, 16), queries = operand(base + L::q, 16);
+    uint32_t items = 0, tile = 0;
+    const uint32_t pieces = count * kPieces;
+    for (uint32_t g = which; g < pieces; g += kIssue) {
+      const uint32_t n = g / kPieces, b = g - n * kPieces, st = g % S, buf = g % kBufs;
+      for (; tile < n; ++tile) step();
+      if (b < 2 && (n == 0 || w.tile == 0)) {
+        ok = ok && warp_wait(bar(kBarQuery), items & 1);
+        ++items;
+      }
+      ok = ok && warp_wait(bar(kBarFull + st), (g / S) & 1);
+      if (g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
+      tc_fence_after();
+      const uint64_t da = rows + st * (kStageBytes >> 4), db = queries + b * (2 * NC * 128 >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (uint32_t s = 0; s < 8; ++s)
+          if (s < 4 || b < 4)
+            mma_bf16(tmem + buf * NC, da + (s >> 2) * (kGroupBytes >> 4) + (s & 3) * 2, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, kId, s != 0);
+        mma_commit(bar(kBarEmpty + st));
+        mma_commit(bar(kBarDone + buf));
+        if (b >= 3 && w.tile + 1 == p.tiles) mma_commit(bar(kBarIdle));  // (this warp's last piece of the item)
+      }
+      __syncwarp();
+    }
+    bool ended = true;
+    if (elect_one()) {  // every product has ended before the block's TMEM goes
+      mma_commit(bar(kBarEnd + which));
+      ended = mbar_wait(bar(kBarEnd + which), 0);
+    }
+    ok = __all_sync(0xffffffffu, ended) && ok;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+  }
+  if (warp == kEnd + kWiden + kIssue) {
+    // ---- the rows' addresses and targets, a tile ahead (four a lane), their scales, and the rows into L2
+    int32_t u[4], to[4];
+    auto fetch = [&]() {
+      const uint32_t list = w.item / p.column_tiles;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t e = w.tile * kTile + lane + 32 * j;
+        u[j] = to[j] = -1;
+        if (e < p.a.k) {
+          u[j] = __ldg(p.a.entry_row + (uint64_t)list * p.a.k + e);
+          to[j] = __ldg(p.a.address + (uint64_t)list * p.a.k + e);
+        }
+      }
+    };
+    if (count) fetch();
+    for (uint32_t n = 0; n < count; ++n) {
+      const uint32_t par = n & 1;
+      if (n > 1 && !(ok = warp_wait(bar(kBarFree + par), (n >> 1 & 1) ^ 1))) break;
+      uint64_t row[4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t r = par * kTile + lane + 32 * j;
+        const bool in = (uint32_t)u[j] < p.a.n_rows && (uint32_t)to[j] < p.a.n_scores;
+        row[j] = in ? (uint64_t)p.a.rows + (uint64_t)(uint32_t)u[j] * ULA_ROW_BYTES : 0;
+        reinterpret_cast<uint64_t *>(sm + L::place)[r] = row[j];
+        reinterpret_cast<uint32_t *>(sm + L::target)[r] = in ? (uint32_t)to[j] : 0xffffffffu;
+        copy16(base + L::scale + r * 16, (const void *)(in ? row[j] + ULA_ROW_LATENT : (uint64_t)p.a.q), in ? 16 : 0);
+      }
+      copy_arrive(bar(kBarScale + par));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarPlace + par));
+      if (n) {
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+          if (row[j]) prefetch((const void *)row[j], ULA_ROW_BYTES);
+      }
+      step();
+      if (n + 1 < count) fetch();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (!ok && lane == 0) atomicAdd(&g_late, 1u);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kEnd + kWiden)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kBufs * NC) : "memory");
 }
 
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-cudaError_t launch(void (*kernel)(ScoreParams), uint64_t grid, cudaStream_t st, const ScoreParams &p) {
+cudaError_t launch(void (*kernel)(ScoreParams), uint64_t grid, uint32_t threads, uint32_t smem, cudaStream_t st, const ScoreParams &p) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -107,7 +393,38 @@ cudaError_t launch(void (*kernel)(ScoreParams), uint64_t grid, cudaStream_t st, 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+std::atomic<uint32_t> g_hold{kBars};
+
+int sm_count() {
+  int dev = 0, n = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+}
+
+template <uint32_t NC>
+cudaError_t launch_score(ScoreParams &p, cudaStream_t st) {
+  const uint32_t columns = p.nodes * p.a.heads;
+  const int sms = sm_count();
+  p.column_tiles = (columns + NC - 1) / NC;
+  p.tiles = (p.a.k + kTile - 1) / kTile;
+  p.total = (unsigned long long)p.lists * p.column_tiles * p.tiles;
+  if (sms < 1) return cudaErrorInvalidDevice;
+  // (idempotent and cheap; a per-device flag would have to know about device resets)
+  const cudaError_t e = cudaFuncSetAttribute(k_score<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NC>::bytes);
+  if (e != cudaSuccess) return e;
+  return launch(k_score<NC>, p.total < (unsigned)sms ? p.total : (unsigned)sms, kThreads, Shared<NC>::bytes, st, p);
+}
+
 }  // namespace
+
+cudaError_t ula_tc::score_late(uint32_t *late, cudaStream_t st) {
+  return cudaMemcpyFromSymbolAsync(late, g_late, sizeof *late, 0, cudaMemcpyDeviceToHost, st);
+}
+
+extern "C" int ula_rows_debug_hold_score(int barrier) {
+  if (barrier >= (int)kBars) return ULA_ERR_INVALID_ARG;
+  g_hold.store(barrier < 0 ? (uint32_t)kBars : (uint32_t)barrier, std::memory_order_relaxed);
+  return ULA_OK;
+}
 
 extern "C" uint64_t ula_rows_score_workspace(uint32_t n_scores) { return (uint64_t)n_scores * 8; }
 
@@ -132,7 +449,7 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
   const uint64_t tokens = (uint64_t)a.n_req * a.n_q;
   p.nodes = shared ? a.n_q : 1;
   if (tokens > 0x7fffffffull || a.heads > 0x7fffffffu || tokens * a.heads > 0x7fffffffull || a.k > 0x7fffffffu ||
-      tokens * a.k > (1ull << 33))
+      (tokens * a.heads / 16 + tokens) * (a.k / 128 + 1ull) > (1ull << 36))
     return ULA_ERR_INVALID_ARG;
   p.lists = shared ? a.n_req : (uint32_t)tokens;
   p.sums = (unsigned long long *)a.workspace;
@@ -141,11 +458,12 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
   int bits = 0;
   while (bits < 62 && (double)tokens * a.heads * a.k > std::ldexp(1.0, bits)) ++bits;
   p.unit = std::ldexp(1.f, bits < 3 ? 60 : 63 - bits);
-  const uint64_t n = (uint64_t)p.lists * a.k;
+  p.hold = g_hold.load(std::memory_order_relaxed);
+  const uint64_t n = (uint64_t)p.lists * a.k, columns = (uint64_t)p.nodes * a.heads;
   cudaStream_t st = (cudaStream_t)stream;
   const uint64_t blocks = (n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024;
-  cudaError_t e = launch(k_score_clear, blocks, st, p);
-  if (e == cudaSuccess) e = launch(k_score, (n + 7) / 8, st, p);
-  if (e == cudaSuccess) e = launch(k_score_commit, blocks, st, p);
+  cudaError_t e = launch(k_score_clear, blocks, 256, 0, st, p);
+  if (e == cudaSuccess) e = columns <= 32 ? launch_score<32>(p, st) : columns <= 64 ? launch_score<64>(p, st) : launch_score<128>(p, st);
+  if (e == cudaSuccess) e = launch(k_score_commit, blocks, 256, 0, st, p);
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }

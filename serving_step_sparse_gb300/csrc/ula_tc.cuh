@@ -8,6 +8,9 @@
 
 namespace ula_tc {
 
+// Copies the count of ula_rows_score's warps whose waits ran out, in all launches so far (ula_score.cu).
+__attribute__((visibility("hidden"))) cudaError_t score_late(uint32_t *late, cudaStream_t st);
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

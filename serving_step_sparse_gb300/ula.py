@@ -151,6 +151,8 @@ def _load():
     lib.ula_rows_sync.restype = i32
     lib.ula_rows_debug_hold.argtypes = [i32]
     lib.ula_rows_debug_hold.restype = i32
+    lib.ula_rows_debug_hold_score.argtypes = [i32]
+    lib.ula_rows_debug_hold_score.restype = i32
     return lib
 
 
@@ -351,3 +353,8 @@ def ula_rows_sync(stream) -> None:
 def ula_rows_debug_hold(barrier: int) -> None:
     """Test hook: one of the attention kernel's barriers never opens (negative: none)."""
     _check(lib.ula_rows_debug_hold(barrier), "ula_rows_debug_hold")
+
+
+def ula_rows_debug_hold_score(barrier: int) -> None:
+    """Test hook: one of the weights kernel's barriers never opens (negative: none)."""
+    _check(lib.ula_rows_debug_hold_score(barrier), "ula_rows_debug_hold_score")

@@ -893,3 +893,31 @@ def test_other_streams():
     for i, g in enumerate(got):
         for x, y in zip(g, want[i % 3]):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("R,Q,H,K", [(90, 1, 20, 300), (3, 2, 64, 700), (60, 2, 100, 500)])
+@pytest.mark.parametrize("barrier", [0, 1, 4, 5, 8, 11, 12, 15, 16, 17, 18, 19, 20, 21, 22, 23, 24, 25])
+def test_score_gives_up(barrier, R, Q, H, K):
+    """A barrier that never opens: the call ends, its error is reported once, the next call is whole."""
+    from serving_step_sparse_gb300 import rows, ula
+    before, *case = score_case(R, Q, H, K, 500, barrier)
+    want = rows.score(before.clone(), *case, SCALE)
+    rows.sync()
+    ula.ula_rows_debug_hold_score(barrier)
+    try:
+        rows.score(before.clone(), *case, SCALE)
+    finally:
+        ula.ula_rows_debug_hold_score(-1)
+    # (with two tiles in a block nobody waits for a place to be free, with one for no second of anything)
+    if barrier in {20: (20, 21), 64: (4, 5, 12, 15, 17, 19, 20, 21, 23), 100: ()}[H]:
+        try:
+            rows.sync()
+        except ula.UlaError:
+            pass
+    else:
+        with pytest.raises(ula.UlaError) as e:
+            rows.sync()
+        assert e.value.code == ula.ERR_TIMEOUT
+    got = rows.score(before.clone(), *case, SCALE)
+    rows.sync()
+    assert torch.equal(got, want)

@@ -590,8 +590,8 @@ int ula_rows_attend_tree(const ula_attend_args *args, const int32_t *parent, uin
  *   address   : device int32, entry_row's shape: ula_step_group's d_sel.
  *   lse       : device fp32 [n_req][n_q][heads].
  *   scores    : device fp32 [n_scores], updated in place.
- *   workspace : device, 8-byte aligned, ula_rows_score_workspace(n_scores) bytes.  Calls that
- *               overlap on the GPU need workspaces of their own; they may share the scores.
+ *   workspace : device, 16-byte aligned, ula_rows_score_workspace(...) bytes.  Calls that overlap
+ *               on the GPU need workspaces of their own; they may share the scores.
  */
 typedef struct ula_score_args {
   const void *q;
@@ -607,7 +607,8 @@ typedef struct ula_score_args {
   float softmax_scale;
 } ula_score_args;
 
-uint64_t ula_rows_score_workspace(uint32_t n_scores);
+uint64_t ula_rows_score_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t flags,
+                                  uint32_t n_scores);
 int ula_rows_score(const ula_score_args *args, void *stream);
 
 /*

@@ -384,7 +384,8 @@ PyObject *score(PyObject *const *a) {
       reinterpret_cast<uintptr_t>(q.data_ptr()) % 16)
     q = q.clone(at::MemoryFormat::Contiguous);
   ula_score_args args{};
-  args.workspace_bytes = ula_rows_score_workspace(scores.size(0));
+  args.flags = entry.dim() == 2 ? ULA_TREE_SHARED_LIST : 0;
+  args.workspace_bytes = ula_rows_score_workspace(R, Q, H, args.flags, scores.size(0));
   const at::Tensor space = on.empty({(int64_t)args.workspace_bytes}, at::kByte);
   args.workspace = space.data_ptr();
   args.q = q.data_ptr();
@@ -394,7 +395,6 @@ PyObject *score(PyObject *const *a) {
   args.lse = lse.data_ptr<float>();
   args.scores = scores.data_ptr<float>(), args.n_scores = scores.size(0);
   args.n_req = R, args.n_q = Q, args.heads = H, args.k = K, args.softmax_scale = (float)scale;
-  args.flags = entry.dim() == 2 ? ULA_TREE_SHARED_LIST : 0;
   check(ula_rows_score(&args, on.stream()), "ula_rows_score");
   return wrap(a[0], scores);
 }

@@ -3,9 +3,9 @@
 //
 // An address may be selected by several query tokens, so its weights are summed as 64-bit whole numbers
 // (a fixed point that no sum of this call's weights can pass), whose sum does not depend on their
-// order; one addition in fp32 per address then updates its score.  Three launches: the sums are cleared
-// at the addresses in question, the weights are added, and each sum is taken by the first entry that
-// finds it.
+// order; one addition in fp32 per address then updates its score.  Three launches: the first clears the
+// sums at the addresses in question and lays the queries out as the second reads them; the second adds
+// the weights up; in the third each sum is taken by the first entry that finds it.
 #include <cuda_bf16.h>
 #include <atomic>
 #include <cmath>
@@ -23,6 +23,7 @@ struct ScoreParams {
   unsigned long long *sums;     // [n_scores]
   unsigned long long total;     // tiles of all items
   uint32_t tiles, column_tiles; // of an item; of a list
+  uint8_t *images;              // [lists][column_tiles] the queries as they stand in shared memory
   uint32_t hold;                // (test hook) an mbarrier whose phases never end; kBars: none
   float c0, unit;               // softmax_scale * log2(e); what 1.0 is in fixed point
 };
@@ -32,12 +33,63 @@ __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(256) k_score_clear(const __grid_constant__ ScoreParams p) {
+// The queries of an item (a list's tile of NC columns): nine groups of 64 channels, [NC][128 B] each with
+// the products' swizzle, then each column's -lse in units of log2 and the factor of its latents.
+template <uint32_t NC>
+struct Image {
+  static constexpr uint32_t lse = 9 * NC * 128, factor = lse + NC * 4, bytes = factor + NC * 4;
+};
+
+// Clears the sums, and makes the images, a warp a column.  Bound by its bytes (a query is read and
+// written once).  The latents become f16: exact once they are multiplied by a power of two that brings
+// the column's largest near 2^15 (bf16 has 8 significant bits, and f16 keeps them down to 2^-31 of the
+// largest; below, an error of 2^-39 of it is far under what fp32 sums lose).  The rope channels stay bf16.
+template <uint32_t NC>
+__global__ void __launch_bounds__(256) k_score_prepare(const __grid_constant__ ScoreParams p) {
   after_previous();
   const uint64_t n = (uint64_t)p.lists * p.a.k;
   for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (uint64_t)gridDim.x * 256) {
     const uint32_t a = (uint32_t)__ldg(p.a.address + e);
     if (a < p.a.n_scores) p.sums[a] = 0;
+  }
+  const uint32_t lane = threadIdx.x & 31, columns = p.nodes * p.a.heads, per_list = p.column_tiles * NC;
+  const uint64_t all = (uint64_t)p.lists * per_list;
+  for (uint64_t i = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < all; i += (uint64_t)gridDim.x * 8) {
+    const uint32_t list = (uint32_t)(i / per_list), c = (uint32_t)(i - (uint64_t)list * per_list), h = c % NC;
+    uint8_t *image = p.images + (i / NC) * Image<NC>::bytes;
+    uint8_t *dst = image + (lane >> 3) * (NC * 128) + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+    uint4 v[2] = {}, rope = {};
+    float l = -INFINITY;
+    int up = 0;
+    if (c < columns) {
+      const uint32_t token = list * p.nodes + c / p.a.heads, head = c % p.a.heads, req = token / p.a.n_q;
+      const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + req * p.a.q_req_stride + (token - req * p.a.n_q) * p.a.q_tok_stride + head * p.a.q_head_stride;
+      v[0] = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
+      v[1] = __ldg(reinterpret_cast<const uint4 *>(q) + 32 + lane);
+      if (lane < 8) rope = __ldg(reinterpret_cast<const uint4 *>(q) + 64 + lane);
+      l = __ldg(p.a.lse + (uint64_t)list * columns + c);
+      uint32_t *u = reinterpret_cast<uint32_t *>(v), most = 0;  // the largest finite value's exponent
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t lo = u[k] >> 7 & 0xff, hi = u[k] >> 23 & 0xff;
+        most = max(most, max(lo == 255 ? 0 : lo, hi == 255 ? 0 : hi));
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      up = min(14 + 127 - (int)most, 126);  // its exponent becomes 14; both factors are normal numbers of fp32
+      const float by = __int_as_float((127 + up) << 23);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __half2 t = __floats2half2_rn(__uint_as_float(u[k] << 16) * by, __uint_as_float(u[k] & 0xffff0000u) * by);
+        u[k] = *reinterpret_cast<const uint32_t *>(&t);
+      }
+    }
+    *reinterpret_cast<uint4 *>(dst) = v[0];
+    *reinterpret_cast<uint4 *>(dst + 4 * NC * 128) = v[1];
+    if (lane < 8) *reinterpret_cast<uint4 *>(dst + 8 * NC * 128) = rope;
+    if (lane == 0) {  // (a column without an lse, or none: exp2(z - inf) is 0)
+      reinterpret_cast<float *>(image + Image<NC>::lse)[h] = l > -INFINITY ? -l * 1.44269504088896341f : -INFINITY;
+      reinterpret_cast<float *>(image + Image<NC>::factor)[h] = __int_as_float((127 - up) << 23);
+    }
   }
 }
 
@@ -61,19 +113,19 @@ constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's 
 constexpr uint32_t kPieces = 5;                      // of a tile: 4 blocks of latents, the rope channels
 constexpr uint32_t kStageBytes = 2 * kGroupBytes;
 constexpr uint32_t kBufs = 4;                        // accumulators in TMEM
-constexpr uint32_t kEnd = 8, kWiden = 8;             // warps that finish the logits, that widen rows (in two groups)
-constexpr uint32_t kIssue = 2;                       // and that issue products; then one that looks rows up
+constexpr uint32_t kEnd = 16, kWiden = 8;            // warps that finish the logits, that widen rows
+constexpr uint32_t kIssue = 2;                       // and that issue products; then one that looks rows up, one for the queries
 constexpr uint32_t kThreads = (kEnd + kWiden + 4) * 32;  // (registers move between groups of 4 warps)
-// Launched with 96 registers a thread: 5 * 96 = 2 * 128 + 2 * 88 + 48.
-constexpr uint32_t kRegsEnd = 128, kRegsWiden = 88, kRegsIssue = 48;
+// Launched with 72 registers a thread: 7 * 72 = 4 * 72 + 2 * 80 + 56.
+constexpr uint32_t kRegsWiden = 80, kRegsIssue = 56;
 __device__ uint32_t g_late;                          // warps whose waits ran out, in all launches so far
 
 // mbarriers.  Full, Empty: a stage holds a piece, its products have ended; Done, Drained: an
 // accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
 // Free: both have been read; Query: the item's queries; Idle: the item's products have ended; End: an
 // issuing warp's have.  (A wait names its phase by its parity alone, so whoever waits for a phase has
-// waited for the one before it: pieces alternate between the groups, and the numbers of stages and
-// accumulators are even.)
+// waited for the one before it: pieces alternate between the issuing warps, and the numbers of stages
+// and accumulators are even.)
 constexpr uint32_t kMostStages = 4;
 enum {
   kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kBufs,
@@ -88,10 +140,10 @@ struct Shared {
   static constexpr uint32_t q = 0;                                  // [9][NC][128 B]
   static constexpr uint32_t ring = 9 * NC * 128;                    // [stages][2][128][128 B]
   static constexpr uint32_t scale = ring + stages * kStageBytes;    // [2][128][4]
-  static constexpr uint32_t place = scale + 2 * kTile * 16;         // [2][128] the rows' addresses, 0: none
+  static constexpr uint32_t place = scale + 2 * kTile * 16;         // [2][128] the rows' addresses (a query's: no row)
   static constexpr uint32_t target = place + 2 * kTile * 8;         // [2][128] their places in scores
-  static constexpr uint32_t lse = target + 2 * kTile * 4;           // [2][NC] in units of log2
-  static constexpr uint32_t bars = lse + 2 * NC * 4;
+  static constexpr uint32_t lse = target + 2 * kTile * 4;           // [2][2][NC] -lse in units of log2, factors
+  static constexpr uint32_t bars = lse + 4 * NC * 4;
   static constexpr uint32_t words = bars + kBars * 8;
   static constexpr uint32_t bytes = words + 16 + 1024;              // (+ alignment of the base)
 };
@@ -102,27 +154,28 @@ struct Place {
 };
 
 // S^T[128 rows][NC columns] = C_b Q_b^T for the four blocks of latents and the rope channels, as in the
-// attention (ula_attend.cu): codes widened to bf16, exact, and scaled in fp32 as the accumulators are
-// read.  Nothing but the sum over a row's columns of exp2(z - lse) leaves the block, so the pieces of a
-// tile stream: two groups of four warps widen every other piece into a ring of stages, two warps issue
-// its products into a ring of four accumulators, eight warps take them up, a row per thread and half of
-// the columns, and add a row's weights to its sum.
+// attention (ula_attend.cu), with the blocks' scales applied in fp32 as the accumulators are read.
+// Codes are exact in f16, by one conversion for two of them.
+// Nothing but the sum over a row's columns of exp2(z - lse) leaves the block, so the pieces of a
+// tile stream: eight warps widen them into a ring of stages, two warps issue their products in turn into
+// a ring of four accumulators, sixteen warps take them up, a row per thread and a quarter of the columns, and
+// add a row's weights to its sum.
 template <uint32_t NC>
 __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ ScoreParams p) {
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NC>;
   constexpr uint32_t S = L::stages;
-  constexpr int HG = NC / 2;
+  constexpr int HG = NC / 4, kRead = HG < 16 ? HG : 16;  // columns of a thread, and of one read
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
   if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < kMostStages; ++i) mbar_init(bar(kBarFull + i), kWiden / 2), mbar_init(bar(kBarEmpty + i), 1);
+    for (uint32_t i = 0; i < kMostStages; ++i) mbar_init(bar(kBarFull + i), kWiden), mbar_init(bar(kBarEmpty + i), 1);
     for (uint32_t i = 0; i < kBufs; ++i) mbar_init(bar(kBarDone + i), 1), mbar_init(bar(kBarDrained + i), kEnd);
     for (uint32_t i = 0; i < 2; ++i)
       mbar_init(bar(kBarPlace + i), 1), mbar_init(bar(kBarScale + i), 32), mbar_init(bar(kBarFree + i), kEnd + kWiden);
-    mbar_init(bar(kBarQuery), kWiden), mbar_init(bar(kBarIdle), kIssue);
+    mbar_init(bar(kBarQuery), 1), mbar_init(bar(kBarIdle), kIssue);
     for (uint32_t i = 0; i < kIssue; ++i) mbar_init(bar(kBarEnd + i), 1);
     if (p.hold < kBars) {
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(p.hold)) : "memory");
@@ -130,9 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     }
     fence_async_smem();
   }
-  // (what is read before its time, after a wait that ran out, is no address)
+  // (An entry without a row stands for 656 bytes of the queries, whose products nobody adds up.  So does what
+  // is read before its time, after a wait that ran out.)
   for (uint32_t i = threadIdx.x; i < 2 * kTile; i += kThreads) {
-    reinterpret_cast<uint64_t *>(sm + L::place)[i] = 0;
+    reinterpret_cast<uint64_t *>(sm + L::place)[i] = (uint64_t)p.a.q;
     reinterpret_cast<uint32_t *>(sm + L::target)[i] = 0xffffffffu;
   }
   if (warp == kEnd + kWiden) {
@@ -155,7 +209,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   bool ok = true;  // false once a wait has run out
   if (warp < kEnd) {
     // ---- logits, weights, sums: this thread's row and HG columns
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEnd));
     const uint32_t quad = warp & 3, grp = warp >> 2, mine = 32 * quad + lane;
     const uint32_t lanes = tmem + (quad << 21) + grp * HG;
     uint32_t items = 0;
@@ -178,15 +231,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
         if (!(ok = warp_wait(bar(kBarDone + buf), (g / kBufs) & 1))) break;
         tc_fence_after();
         const float s = (b == 0 ? s4.x : b == 1 ? s4.y : b == 2 ? s4.z : b == 3 ? s4.w : 1.f) * p.c0;
+        float x[kRead];
+        tmem_ld<kRead>(lanes + buf * NC, x);
+        if (b == 4) {  // the latents' part as it was before its column was scaled, less the lse
+          const float *l = reinterpret_cast<const float *>(sm + L::lse) + ((items - 1) & 1) * 2 * NC + grp * HG;
 #pragma unroll
-        for (int c = 0; c < HG; c += 16) {
-          float v[16];
-          tmem_ld<16>(lanes + buf * NC + c, v);
+          for (int c = 0; c < HG; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4 *>(l + c), f4 = *reinterpret_cast<const float4 *>(l + NC + c);
+            fma2(z[c], z[c + 1], f4.x, f4.y, l4.x, l4.y);
+            fma2(z[c + 2], z[c + 3], f4.z, f4.w, l4.z, l4.w);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < HG; c += kRead) {
+          if (c) tmem_ld<kRead>(lanes + buf * NC + c, x);
           tc_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 16; h += 2) {
-            if (b == 0) mul2(z[c + h], z[c + h + 1], s, v[h], v[h + 1]);
-            else fma2(z[c + h], z[c + h + 1], s, v[h], v[h + 1]);
+          for (int h = 0; h < kRead; h += 2) {
+            if (b == 0) mul2(z[c + h], z[c + h + 1], s, x[h], x[h + 1]);
+            else fma2(z[c + h], z[c + h + 1], s, x[h], x[h + 1]);
           }
         }
         tc_fence_before();
@@ -195,104 +258,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       }
       if (!ok) break;
       // a weight is between 0 and 1, and 0 where it is not a number (what .sat makes of one)
-      const float *lse = reinterpret_cast<const float *>(sm + L::lse) + ((items - 1) & 1) * NC + grp * HG;
       float total = 0.f;
 #pragma unroll
-      for (int c = 0; c < HG; c += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(lse + c);
-        total += (__saturatef(ex2(z[c] - l.x)) + __saturatef(ex2(z[c + 1] - l.y))) +
-                 (__saturatef(ex2(z[c + 2] - l.z)) + __saturatef(ex2(z[c + 3] - l.w)));
-      }
+      for (int c = 0; c < HG; c += 4)
+        total += (__saturatef(ex2(z[c])) + __saturatef(ex2(z[c + 1]))) + (__saturatef(ex2(z[c + 2])) + __saturatef(ex2(z[c + 3])));
       if (target != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target, __float2ull_rn(total * p.unit));
     }
   } else if (warp < kEnd + kWiden) {
-    // ---- widening: group `grp` takes pieces grp, grp + 2, ...; a warp 32 rows, a lane of it every
-    // fourth, 16 bytes of a row's 128.  The next piece's loads are issued once this one's registers are free.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
-    const uint32_t cw = warp - kEnd, grp = cw >> 2, r0 = 32 * (cw & 3) + (lane >> 3), ch = lane & 7;
+    // ---- widening: a warp 16 rows of every piece, a lane 4 of them in a row, 16 bytes of a row's 128.
+    // The loads of the next two pieces are in flight.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    const uint32_t cw = warp - kEnd, r0 = 16 * cw + 4 * (lane >> 3), ch = lane & 7;
     const uint32_t pieces = count * kPieces;
-    uint4 raw[8];
-    auto fetch = [&](uint32_t g) -> bool {
-      const uint32_t n = g / kPieces, b = g - n * kPieces, par = n & 1;
-      if (!warp_wait(bar(kBarPlace + par), (n >> 1) & 1)) return false;
-      const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + par * kTile;
-      const uint32_t at = (b < 4 ? b * 128 : ULA_ROW_LATENT + 16) + ch * 16;
-#pragma unroll
-      for (uint32_t j = 0; j < 8; ++j) {
-        const uint64_t row = place[r0 + 4 * j];
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (row) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row + at));
-      }
-      if ((g + 2) / kPieces != n) {  // (the group's last piece of the tile)
+    uint64_t row[4] = {};  // the rows of the tile whose pieces are being loaded
+    auto fetch = [&](uint4 (&raw)[4], uint32_t g) -> bool {
+      const uint32_t n = g / kPieces, b = g - n * kPieces;
+      if (b == 0) {
+        if (!warp_wait(bar(kBarPlace + (n & 1)), (n >> 1) & 1)) return false;
+        const ulonglong2 *place = reinterpret_cast<const ulonglong2 *>(sm + L::place + ((n & 1) * kTile + r0) * 8);
+        const ulonglong2 a = place[0], c = place[1];
+        row[0] = a.x + ch * 16, row[1] = a.y + ch * 16, row[2] = c.x + ch * 16, row[3] = c.y + ch * 16;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarFree + par));
+        if (lane == 0) mbar_arrive(bar(kBarFree + (n & 1)));
       }
+      const uint32_t at = b < 4 ? b * 128 : ULA_ROW_LATENT + 16;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row[j] + at));
       return true;
     };
-    uint32_t items = 0, tile = 0;  // `tile`: the tile whose item's queries stand
-    ok = grp >= pieces || fetch(grp);
-    for (uint32_t g = grp; g < pieces && ok; g += 2) {
-      const uint32_t n = g / kPieces, b = g - n * kPieces;
-      for (; tile < n; ++tile) step();
-      if (b < 2 && (n == 0 || w.tile == 0)) {
-        // the item's queries, once the products that read the last one's have ended
-        if (items && !(ok = warp_wait(bar(kBarIdle), (items - 1) & 1))) break;
-        const uint32_t list = w.item / p.column_tiles, c0 = (w.item - list * p.column_tiles) * NC;
-        const uint32_t req = list * p.nodes / p.a.n_q, first = list * p.nodes - req * p.a.n_q;
-        const uint32_t columns = p.nodes * p.a.heads;
-        const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + req * p.a.q_req_stride;
-        for (uint32_t i = cw * 32 + lane; i < NC * 72; i += kWiden * 32) {
-          const uint32_t h = i / 72, c = i - h * 72;
-          const uint32_t dst = base + L::q + (c >> 3) * (NC * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
-          const bool in = c0 + h < columns;
-          const uint32_t node = (c0 + h) / p.a.heads, head = c0 + h - node * p.a.heads;
-          copy16(dst, q + (in ? (first + node) * p.a.q_tok_stride + head * p.a.q_head_stride + c * 8 : 0), in ? 16 : 0);
-        }
-        for (uint32_t h = cw * 32 + lane; h < NC; h += kWiden * 32) {
-          const float l = c0 + h < columns ? __ldg(p.a.lse + (uint64_t)list * columns + c0 + h) : -INFINITY;
-          // (a column without an lse: exp2(z - inf) is 0)
-          reinterpret_cast<float *>(sm + L::lse)[(items & 1) * NC + h] = l > -INFINITY ? l * 1.44269504088896341f : INFINITY;
-        }
-        ++items;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQuery));
-      }
-      const uint32_t st = g % S;
-      if (g >= S && !(ok = warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1))) break;
-      uint8_t *stage = sm + L::ring + st * kStageBytes;
+    auto piece = [&](uint4 (&raw)[4], uint32_t g) -> bool {
+      const uint32_t b = g % kPieces, st = g % S;
+      if (g >= S && !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1)) return false;
+      uint8_t *stage = sm + L::ring + st * kStageBytes + r0 * 128;
+      // (16-byte accesses are served by quarters of a warp, here one row's: the lanes of the second
+      // half store their second chunk first, so that all eight lie in different banks)
+      const bool up = ch & 4;
+      const uint32_t c = 2 * (ch & 3) + (up ? 1 : 0);
 #pragma unroll
-      for (uint32_t j = 0; j < 8; ++j) {
-        const uint32_t r = r0 + 4 * j, x = r & 7;
+      for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t x = (r0 + j) & 7;
         const uint4 v = raw[j];
         if (b == 4) {
-          *reinterpret_cast<uint4 *>(stage + r * 128 + ((ch ^ x) << 4)) = v;
+          *reinterpret_cast<uint4 *>(stage + j * 128 + ((ch ^ x) << 4)) = v;
         } else {
-          // (16-byte accesses are served by quarters of a warp, here one row's: the lanes of the second
-          // half store their second chunk first, so that all eight lie in different banks)
-          uint8_t *at = stage + (ch >> 2) * kGroupBytes + r * 128;
-          const bool up = ch & 4;
-          const uint32_t c = 2 * (ch & 3) + (up ? 1 : 0);
+          uint8_t *at = stage + (ch >> 2) * kGroupBytes + j * 128;
           const uint32_t p0 = up ? v.z : v.x, p1 = up ? v.w : v.y, q0 = up ? v.x : v.z, q1 = up ? v.y : v.w;
           *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
-              make_uint4(codes_to_bf16(p0), codes_to_bf16(p0 >> 16), codes_to_bf16(p1), codes_to_bf16(p1 >> 16));
+              make_uint4(codes_to_f16(p0), codes_to_f16(p0 >> 16), codes_to_f16(p1), codes_to_f16(p1 >> 16));
           *reinterpret_cast<uint4 *>(at + ((c ^ 1 ^ x) << 4)) =
-              make_uint4(codes_to_bf16(q0), codes_to_bf16(q0 >> 16), codes_to_bf16(q1), codes_to_bf16(q1 >> 16));
+              make_uint4(codes_to_f16(q0), codes_to_f16(q0 >> 16), codes_to_f16(q1), codes_to_f16(q1 >> 16));
         }
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarFull + st));
-      if (g + 2 < pieces) ok = fetch(g + 2);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+      return g + 2 >= pieces || fetch(raw, g + 2);
+    };
+    uint4 raw0[4], raw1[4];
+    ok = pieces == 0 || (fetch(raw0, 0) && fetch(raw1, 1));  // (a tile has five)
+    for (uint32_t g = 0; g < pieces && ok; g += 2) ok = piece(raw0, g) && (g + 1 >= pieces || piece(raw1, g + 1));
   } else if (warp < kEnd + kWiden + kIssue) {
     // ---- products, every other piece.  (A wait that has run out does not leave the loop, so that the
     // descriptors stay in uniform registers; it is reported at the end.)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     const uint32_t which = warp - kEnd - kWiden;
-    constexpr uint32_t kId = (1u << 4) | (1u << 7) | (1u << 10) | ((NC >> 3) << 17) | ((kTile >> 4) << 24);  // D fp32, A and B bf16
+    // D fp32; A and B f16, the rope channels bf16
+    constexpr uint32_t kId = (1u << 4) | ((NC >> 3) << 17) | ((kTile >> 4) << 24), kIdRope = kId | (1u << 7) | (1u << 10);
     const uint64_t rows = operand(base + L::ring, 16), queries = operand(base + L::q, 16);
     uint32_t items = 0, tile = 0;
     const uint32_t pieces = count * kPieces;
@@ -311,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
 #pragma unroll
         for (uint32_t s = 0; s < 8; ++s)
           if (s < 4 || b < 4)
-            mma_bf16(tmem + buf * NC, da + (s >> 2) * (kGroupBytes >> 4) + (s & 3) * 2, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, kId, s != 0);
+            mma_bf16(tmem + buf * NC, da + (s >> 2) * (kGroupBytes >> 4) + (s & 3) * 2, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, b < 4 ? kId : kIdRope, s != 0);
         mma_commit(bar(kBarEmpty + st));
         mma_commit(bar(kBarDone + buf));
         if (b >= 3 && w.tile + 1 == p.tiles) mma_commit(bar(kBarIdle));  // (this warp's last piece of the item)
@@ -351,23 +382,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       for (uint32_t j = 0; j < 4; ++j) {
         const uint32_t r = par * kTile + lane + 32 * j;
         const bool in = (uint32_t)u[j] < p.a.n_rows && (uint32_t)to[j] < p.a.n_scores;
-        row[j] = in ? (uint64_t)p.a.rows + (uint64_t)(uint32_t)u[j] * ULA_ROW_BYTES : 0;
+        row[j] = in ? (uint64_t)p.a.rows + (uint64_t)(uint32_t)u[j] * ULA_ROW_BYTES : (uint64_t)p.a.q;
         reinterpret_cast<uint64_t *>(sm + L::place)[r] = row[j];
         reinterpret_cast<uint32_t *>(sm + L::target)[r] = in ? (uint32_t)to[j] : 0xffffffffu;
-        copy16(base + L::scale + r * 16, (const void *)(in ? row[j] + ULA_ROW_LATENT : (uint64_t)p.a.q), in ? 16 : 0);
+        copy16(base + L::scale + r * 16, (const void *)(row[j] + ULA_ROW_LATENT), 16);
       }
       copy_arrive(bar(kBarScale + par));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarPlace + par));
-      if (n) {
+      if (n) {  // into L2 ahead of the loads, by lines: a bulk prefetch of a row takes its engine 64 clocks
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j)
-          if (row[j]) prefetch((const void *)row[j], ULA_ROW_BYTES);
+#pragma unroll
+          for (uint32_t i = 0; i < ULA_ROW_BYTES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + i));
       }
       step();
       if (n + 1 < count) fetch();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (warp == kEnd + kWiden + kIssue + 1) {
+    // ---- an item's queries, once the products that read the last one's have ended
+    const uint32_t items = count ? (uint32_t)((from + count - 1) / p.tiles) - w.item + 1 : 0;
+    uint32_t i = 0;
+    for (; i < items; ++i) {
+      if (i && !(ok = warp_wait(bar(kBarIdle), (i - 1) & 1))) break;
+      if (elect_one()) {
+        const uint8_t *image = p.images + (uint64_t)(w.item + i) * Image<NC>::bytes;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(kBarQuery)), "r"(Image<NC>::bytes) : "memory");
+        for (uint32_t k = 0; k < 9; ++k) copy_bulk(base + L::q + k * NC * 128, image + k * NC * 128, NC * 128, bar(kBarQuery));
+        copy_bulk(base + L::lse + (i & 1) * 2 * NC * 4, image + Image<NC>::lse, 2 * NC * 4, bar(kBarQuery));
+      }
+      __syncwarp();
+    }
+    if (i) ok = warp_wait(bar(kBarQuery), (i - 1) & 1) && ok;  // (no copy is in flight when the block ends)
   }
   if (!ok && lane == 0) atomicAdd(&g_late, 1u);
   tc_fence_before();
@@ -409,7 +457,11 @@ cudaError_t launch_score(ScoreParams &p, cudaStream_t st) {
   p.total = (unsigned long long)p.lists * p.column_tiles * p.tiles;
   if (sms < 1) return cudaErrorInvalidDevice;
   // (idempotent and cheap; a per-device flag would have to know about device resets)
-  const cudaError_t e = cudaFuncSetAttribute(k_score<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NC>::bytes);
+  cudaError_t e = cudaFuncSetAttribute(k_score<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shared<NC>::bytes);
+  if (e != cudaSuccess) return e;
+  const uint64_t warps = (uint64_t)p.lists * p.column_tiles * NC, entries = (uint64_t)p.lists * p.a.k;
+  const uint64_t blocks = (warps + 7) / 8 > (entries + 255) / 256 ? (warps + 7) / 8 : (entries + 255) / 256;
+  e = launch(k_score_prepare<NC>, blocks < 2048 ? blocks : 2048, 256, 0, st, p);
   if (e != cudaSuccess) return e;
   return launch(k_score<NC>, p.total < (unsigned)sms ? p.total : (unsigned)sms, kThreads, Shared<NC>::bytes, st, p);
 }
@@ -426,7 +478,21 @@ extern "C" int ula_rows_debug_hold_score(int barrier) {
   return ULA_OK;
 }
 
-extern "C" uint64_t ula_rows_score_workspace(uint32_t n_scores) { return (uint64_t)n_scores * 8; }
+namespace {
+
+// Columns of an item: the fewest that hold a list's, up to 128 (TMEM's four accumulators).
+uint32_t item_columns(uint64_t columns) { return columns <= 32 ? 32 : columns <= 64 ? 64 : 128; }
+uint32_t image_bytes(uint32_t nc) { return nc == 32 ? Image<32>::bytes : nc == 64 ? Image<64>::bytes : Image<128>::bytes; }
+uint64_t sums_bytes(uint32_t n_scores) { return ((uint64_t)n_scores * 8 + 127) & ~127ull; }
+
+}  // namespace
+
+extern "C" uint64_t ula_rows_score_workspace(uint32_t n_req, uint32_t n_q, uint32_t heads, uint32_t flags, uint32_t n_scores) {
+  const bool shared = flags & ULA_TREE_SHARED_LIST;
+  const uint64_t lists = shared ? n_req : (uint64_t)n_req * n_q, columns = shared ? (uint64_t)n_q * heads : heads;
+  const uint32_t nc = item_columns(columns);
+  return sums_bytes(n_scores) + lists * ((columns + nc - 1) / nc) * image_bytes(nc);
+}
 
 extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
   if (!args) return ULA_ERR_INVALID_ARG;
@@ -441,9 +507,9 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
   if (!a.q || !a.entry_row || !a.address || !a.lse || !a.scores || !a.workspace || (!a.rows && a.n_rows))
     return ULA_ERR_INVALID_ARG;
   if (!aligned(a.q, 16) || !aligned(a.rows, 16) || !aligned(a.entry_row, 4) || !aligned(a.address, 4) ||
-      !aligned(a.lse, 4) || !aligned(a.scores, 4) || !aligned(a.workspace, 8) || a.q_req_stride % 8 ||
+      !aligned(a.lse, 4) || !aligned(a.scores, 4) || !aligned(a.workspace, 16) || a.q_req_stride % 8 ||
       a.q_tok_stride % 8 || a.q_head_stride % 8 || a.n_rows > 0x7fffffffu || a.n_scores > 0x7fffffffu ||
-      a.workspace_bytes < ula_rows_score_workspace(a.n_scores))
+      a.workspace_bytes < ula_rows_score_workspace(a.n_req, a.n_q, a.heads, a.flags, a.n_scores))
     return ULA_ERR_INVALID_ARG;
   const bool shared = a.flags & ULA_TREE_SHARED_LIST;
   const uint64_t tokens = (uint64_t)a.n_req * a.n_q;
@@ -453,6 +519,7 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
     return ULA_ERR_INVALID_ARG;
   p.lists = shared ? a.n_req : (uint32_t)tokens;
   p.sums = (unsigned long long *)a.workspace;
+  p.images = (uint8_t *)a.workspace + sums_bytes(a.n_scores);
   p.c0 = a.softmax_scale * 1.44269504088896341f;
   // a weight is at most 1, and an address gets at most one of every entry of every query head
   int bits = 0;
@@ -462,8 +529,7 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
   const uint64_t n = (uint64_t)p.lists * a.k, columns = (uint64_t)p.nodes * a.heads;
   cudaStream_t st = (cudaStream_t)stream;
   const uint64_t blocks = (n + 255) / 256 < 1024 ? (n + 255) / 256 : 1024;
-  cudaError_t e = launch(k_score_clear, blocks, 256, 0, st, p);
-  if (e == cudaSuccess) e = columns <= 32 ? launch_score<32>(p, st) : columns <= 64 ? launch_score<64>(p, st) : launch_score<128>(p, st);
+  cudaError_t e = item_columns(columns) == 32 ? launch_score<32>(p, st) : item_columns(columns) == 64 ? launch_score<64>(p, st) : launch_score<128>(p, st);
   if (e == cudaSuccess) e = launch(k_score_commit, blocks, 256, 0, st, p);
   return e == cudaSuccess ? ULA_OK : ULA_ERR_CUDA;
 }

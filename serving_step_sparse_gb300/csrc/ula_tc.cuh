@@ -56,7 +56,7 @@ __device__ __forceinline__ bool elect_one() {
   return p;
 }
 
-// One MMA of K = 16: D[128][N] (+)= A B, all operands in shared memory.
+// One MMA of K = 16: D[128][N] (+)= A B, all operands in shared memory (bf16, or f16 as idesc says).
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
@@ -77,6 +77,12 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
 // Brings bytes (a multiple of 16, as the address is) into L2.
 __device__ __forceinline__ void prefetch(const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// Bytes to shared memory (a multiple of 16, as both addresses are), counted by an mbarrier.
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -128,6 +134,11 @@ __device__ __forceinline__ void mul2(float &x0, float &x1, float s, float v0, fl
       " mov.b64 {%0, %1}, b;\n}\n"
       : "=f"(x0), "=f"(x1) : "f"(s), "f"(v0), "f"(v1));
 }
+__device__ __forceinline__ void fma2(float &x0, float &x1, float s0, float s1, float a0, float a1) {  // x = x * s + a
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 c, {%4, %5};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(s0), "f"(s1), "f"(a0), "f"(a1));
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&b);
@@ -167,11 +178,15 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// e4m3 codes (two in the low half of `two`) to bf16, exactly.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
+// e4m3 codes (two in the low half of `two`) to f16 and to bf16, exactly.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-  const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
+  return h;
+}
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
+  const uint32_t h = codes_to_f16(two);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
   return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);  // (their low halves are 0)
 }
 

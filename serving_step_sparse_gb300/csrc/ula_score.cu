@@ -35,6 +35,10 @@ __device__ __forceinline__ void after_previous() {
 
 // The queries of an item (a list's tile of NC columns): nine groups of 64 channels, [NC][128 B] each with
 // the products' swizzle, then each column's -lse in units of log2 and the factor of its latents.
+// A product's sum runs over channels in any order, so long as both sides have the same: that in which
+// k_score's threads bring a row's 128 into TMEM.  Thread i of a row's four holds channels 16 i.. and 64 + 16 i..
+// (of the rope channels 8 i.. and 32 + 8 i..), and gives 4 of them to every 16: the 16-byte chunk m
+// holds the (m / 2)-th four channels of thread 2 (m % 2), then those of the next thread.
 template <uint32_t NC>
 struct Image {
   static constexpr uint32_t lse = 9 * NC * 128, factor = lse + NC * 4, bytes = factor + NC * 4;
@@ -58,15 +62,22 @@ __global__ void __launch_bounds__(256) k_score_prepare(const __grid_constant__ S
     const uint32_t list = (uint32_t)(i / per_list), c = (uint32_t)(i - (uint64_t)list * per_list), h = c % NC;
     uint8_t *image = p.images + (i / NC) * Image<NC>::bytes;
     uint8_t *dst = image + (lane >> 3) * (NC * 128) + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+    // this lane's chunks, `lane` and `lane` + 32 of 64: chunk m of a block of 16
+    const uint32_t m = lane & 15, j = m >> 1, at = (lane >> 4) * 128 + (j >> 2) * 64 + (m & 1) * 32 + (j & 3) * 4;
+    const uint32_t at_rope = 512 + (lane >> 2) * 32 + (lane & 1) * 16 + (lane >> 1 & 1) * 4;
     uint4 v[2] = {}, rope = {};
     float l = -INFINITY;
     int up = 0;
     if (c < columns) {
       const uint32_t token = list * p.nodes + c / p.a.heads, head = c % p.a.heads, req = token / p.a.n_q;
       const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + req * p.a.q_req_stride + (token - req * p.a.n_q) * p.a.q_tok_stride + head * p.a.q_head_stride;
-      v[0] = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
-      v[1] = __ldg(reinterpret_cast<const uint4 *>(q) + 32 + lane);
-      if (lane < 8) rope = __ldg(reinterpret_cast<const uint4 *>(q) + 64 + lane);
+      auto four = [&](uint32_t c4) { return __ldg(reinterpret_cast<const uint2 *>(q + c4)); };
+      auto both = [&](uint32_t c4, uint32_t next) {
+        const uint2 a = four(c4), b = four(c4 + next);
+        return make_uint4(a.x, a.y, b.x, b.y);
+      };
+      v[0] = both(at, 16), v[1] = both(at + 256, 16);
+      if (lane < 8) rope = both(at_rope, 8);
       l = __ldg(p.a.lse + (uint64_t)list * columns + c);
       uint32_t *u = reinterpret_cast<uint32_t *>(v), most = 0;  // the largest finite value's exponent
 #pragma unroll
@@ -109,10 +120,8 @@ __global__ void __launch_bounds__(256) k_score_commit(const __grid_constant__ Sc
 // ---------------------------------------------------------------- the weights
 
 constexpr uint32_t kTile = 128;                      // rows per tile
-constexpr uint32_t kGroupBytes = kTile * 128;        // 64 channels of a tile's rows, bf16
 constexpr uint32_t kPieces = 5;                      // of a tile: 4 blocks of latents, the rope channels
-constexpr uint32_t kStageBytes = 2 * kGroupBytes;
-constexpr uint32_t kBufs = 4;                        // accumulators in TMEM
+constexpr uint32_t kMostBufs = 4, kMostStages = 4;    // accumulators and pieces in TMEM
 constexpr uint32_t kEnd = 16, kWiden = 8;            // warps that finish the logits, that widen rows
 constexpr uint32_t kIssue = 2;                       // and that issue products; then one that looks rows up, one for the queries
 constexpr uint32_t kThreads = (kEnd + kWiden + 4) * 32;  // (registers move between groups of 4 warps)
@@ -124,22 +133,21 @@ __device__ uint32_t g_late;                          // warps whose waits ran ou
 // accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
 // Free: both have been read; Query: the item's queries; Idle: the item's products have ended; End: an
 // issuing warp's have.  (A wait names its phase by its parity alone, so whoever waits for a phase has
-// waited for the one before it: pieces alternate between the issuing warps, and the numbers of stages
-// and accumulators are even.)
-constexpr uint32_t kMostStages = 4;
+// waited for the one before it, or for a later one of those who opened that.)
 enum {
-  kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kBufs,
-  kBarPlace = kBarDrained + kBufs, kBarScale = kBarPlace + 2, kBarFree = kBarScale + 2, kBarQuery = kBarFree + 2,
+  kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kMostBufs,
+  kBarPlace = kBarDrained + kMostBufs, kBarScale = kBarPlace + 2, kBarFree = kBarScale + 2, kBarQuery = kBarFree + 2,
   kBarIdle = kBarQuery + 1, kBarEnd = kBarIdle + 1, kBars = kBarEnd + kIssue
 };
 static_assert(kBars == ULA_DEBUG_SCORE_BARRIERS, "as the header says");
 
 template <uint32_t NC>
 struct Shared {
-  static constexpr uint32_t stages = NC == 128 ? 2 : kMostStages;
+  // TMEM: accumulators of NC columns, then stages of 64 (a piece of 128 channels)
+  static constexpr uint32_t bufs = NC == 128 ? 3 : kMostBufs, stages = NC == 128 ? 2 : kMostStages;
+  static_assert(bufs * NC + stages * 64 <= 512, "columns of TMEM");
   static constexpr uint32_t q = 0;                                  // [9][NC][128 B]
-  static constexpr uint32_t ring = 9 * NC * 128;                    // [stages][2][128][128 B]
-  static constexpr uint32_t scale = ring + stages * kStageBytes;    // [2][128][4]
+  static constexpr uint32_t scale = 9 * NC * 128;                   // [2][128][4]
   static constexpr uint32_t place = scale + 2 * kTile * 16;         // [2][128] the rows' addresses (a query's: no row)
   static constexpr uint32_t target = place + 2 * kTile * 8;         // [2][128] their places in scores
   static constexpr uint32_t lse = target + 2 * kTile * 4;           // [2][2][NC] -lse in units of log2, factors
@@ -158,13 +166,16 @@ struct Place {
 // Codes are exact in f16, by one conversion for two of them.
 // Nothing but the sum over a row's columns of exp2(z - lse) leaves the block, so the pieces of a
 // tile stream: eight warps widen them into a ring of stages, two warps issue their products in turn into
-// a ring of four accumulators, sixteen warps take them up, a row per thread and a quarter of the columns, and
-// add a row's weights to its sum.
+// a ring of accumulators, sixteen warps take them up, a row per thread and a quarter of the columns,
+// and add a row's weights to its sum.
+// The widened rows stand in TMEM, as the products' A: through shared memory a product of K = 16 read 8 KB of
+// operands at what shared memory gives in all (118 B a clock), and every other access of the widening
+// waited for it; now it reads the queries' 4 KB.
 template <uint32_t NC>
 __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ ScoreParams p) {
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NC>;
-  constexpr uint32_t S = L::stages;
+  constexpr uint32_t S = L::stages, kBufs = L::bufs;
   constexpr int HG = NC / 4, kRead = HG < 16 ? HG : 16;  // columns of a thread, and of one read
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
@@ -172,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   auto bar = [&](uint32_t i) { return base + L::bars + 8 * i; };
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kMostStages; ++i) mbar_init(bar(kBarFull + i), kWiden), mbar_init(bar(kBarEmpty + i), 1);
-    for (uint32_t i = 0; i < kBufs; ++i) mbar_init(bar(kBarDone + i), 1), mbar_init(bar(kBarDrained + i), kEnd);
+    for (uint32_t i = 0; i < kMostBufs; ++i) mbar_init(bar(kBarDone + i), 1), mbar_init(bar(kBarDrained + i), kEnd);
     for (uint32_t i = 0; i < 2; ++i)
       mbar_init(bar(kBarPlace + i), 1), mbar_init(bar(kBarScale + i), 32), mbar_init(bar(kBarFree + i), kEnd + kWiden);
     mbar_init(bar(kBarQuery), 1), mbar_init(bar(kBarIdle), kIssue);
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     reinterpret_cast<uint32_t *>(sm + L::target)[i] = 0xffffffffu;
   }
   if (warp == kEnd + kWiden) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + L::words), "n"(kBufs * NC) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::words) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
@@ -265,51 +276,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       if (target != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target, __float2ull_rn(total * p.unit));
     }
   } else if (warp < kEnd + kWiden) {
-    // ---- widening: a warp 16 rows of every piece, a lane 4 of them in a row, 16 bytes of a row's 128.
-    // The loads of the next two pieces are in flight.
+    // ---- widening: a warp 16 rows of every piece (half of its 32 lanes of TMEM); four lanes share a row
+    // and hold another one 8 rows on, 32 bytes of each row's 128.  The loads of the next two pieces are in flight.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
-    const uint32_t cw = warp - kEnd, r0 = 16 * cw + 4 * (lane >> 3), ch = lane & 7;
+    const uint32_t cw = warp - kEnd, first = 32 * (cw & 3) + 16 * (cw >> 2), r0 = first + (lane >> 2), ch = lane & 3;
+    const uint32_t mine = tmem + kBufs * NC + (first << 16);
     const uint32_t pieces = count * kPieces;
-    uint64_t row[4] = {};  // the rows of the tile whose pieces are being loaded
+    uint64_t row[2] = {};  // the rows of the tile whose pieces are being loaded
     auto fetch = [&](uint4 (&raw)[4], uint32_t g) -> bool {
       const uint32_t n = g / kPieces, b = g - n * kPieces;
       if (b == 0) {
         if (!warp_wait(bar(kBarPlace + (n & 1)), (n >> 1) & 1)) return false;
-        const ulonglong2 *place = reinterpret_cast<const ulonglong2 *>(sm + L::place + ((n & 1) * kTile + r0) * 8);
-        const ulonglong2 a = place[0], c = place[1];
-        row[0] = a.x + ch * 16, row[1] = a.y + ch * 16, row[2] = c.x + ch * 16, row[3] = c.y + ch * 16;
+        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile + r0;
+        row[0] = place[0] + ch * 16, row[1] = place[8] + ch * 16;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarFree + (n & 1)));
       }
       const uint32_t at = b < 4 ? b * 128 : ULA_ROW_LATENT + 16;
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row[j] + at));
+      for (uint32_t j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row[j >> 1] + at + (j & 1) * 64));
       return true;
     };
     auto piece = [&](uint4 (&raw)[4], uint32_t g) -> bool {
       const uint32_t b = g % kPieces, st = g % S;
       if (g >= S && !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1)) return false;
-      uint8_t *stage = sm + L::ring + st * kStageBytes + r0 * 128;
-      // (16-byte accesses are served by quarters of a warp, here one row's: the lanes of the second
-      // half store their second chunk first, so that all eight lie in different banks)
-      const bool up = ch & 4;
-      const uint32_t c = 2 * (ch & 3) + (up ? 1 : 0);
+      tc_fence_after();
+      const uint32_t stage = mine + st * 64;
+      if (b == 4) {
+        const uint32_t v[16] = {raw[0].x, raw[0].y, raw[2].x, raw[2].y, raw[0].z, raw[0].w, raw[2].z, raw[2].w,
+                                raw[1].x, raw[1].y, raw[3].x, raw[3].y, raw[1].z, raw[1].w, raw[3].z, raw[3].w};
+        tmem_st_16x32(stage, v);
+      } else {
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        const uint32_t x = (r0 + j) & 7;
-        const uint4 v = raw[j];
-        if (b == 4) {
-          *reinterpret_cast<uint4 *>(stage + j * 128 + ((ch ^ x) << 4)) = v;
-        } else {
-          uint8_t *at = stage + (ch >> 2) * kGroupBytes + j * 128;
-          const uint32_t p0 = up ? v.z : v.x, p1 = up ? v.w : v.y, q0 = up ? v.x : v.z, q1 = up ? v.y : v.w;
-          *reinterpret_cast<uint4 *>(at + ((c ^ x) << 4)) =
-              make_uint4(codes_to_f16(p0), codes_to_f16(p0 >> 16), codes_to_f16(p1), codes_to_f16(p1 >> 16));
-          *reinterpret_cast<uint4 *>(at + ((c ^ 1 ^ x) << 4)) =
-              make_uint4(codes_to_f16(q0), codes_to_f16(q0 >> 16), codes_to_f16(q1), codes_to_f16(q1 >> 16));
+        for (uint32_t i = 0; i < 2; ++i) {
+          const uint4 a = raw[i], c = raw[2 + i];  // 16 codes of the first row, of the second
+          const uint32_t v[16] = {codes_to_f16(a.x), codes_to_f16(a.x >> 16), codes_to_f16(c.x), codes_to_f16(c.x >> 16),
+                                  codes_to_f16(a.y), codes_to_f16(a.y >> 16), codes_to_f16(c.y), codes_to_f16(c.y >> 16),
+                                  codes_to_f16(a.z), codes_to_f16(a.z >> 16), codes_to_f16(c.z), codes_to_f16(c.z >> 16),
+                                  codes_to_f16(a.w), codes_to_f16(a.w >> 16), codes_to_f16(c.w), codes_to_f16(c.w >> 16)};
+          tmem_st_16x32(stage + 32 * i, v);
         }
       }
-      fence_async_smem();
+      tc_wait_st();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarFull + st));
       return g + 2 >= pieces || fetch(raw, g + 2);
@@ -324,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     const uint32_t which = warp - kEnd - kWiden;
     // D fp32; A and B f16, the rope channels bf16
     constexpr uint32_t kId = (1u << 4) | ((NC >> 3) << 17) | ((kTile >> 4) << 24), kIdRope = kId | (1u << 7) | (1u << 10);
-    const uint64_t rows = operand(base + L::ring, 16), queries = operand(base + L::q, 16);
+    const uint64_t queries = operand(base + L::q, 16);
     uint32_t items = 0, tile = 0;
     const uint32_t pieces = count * kPieces;
     for (uint32_t g = which; g < pieces; g += kIssue) {
@@ -337,12 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       ok = ok && warp_wait(bar(kBarFull + st), (g / S) & 1);
       if (g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
       tc_fence_after();
-      const uint64_t da = rows + st * (kStageBytes >> 4), db = queries + b * (2 * NC * 128 >> 4);
+      const uint64_t db = queries + b * (2 * NC * 128 >> 4);
+      const uint32_t a = tmem + kBufs * NC + st * 64;
       if (elect_one()) {
 #pragma unroll
         for (uint32_t s = 0; s < 8; ++s)
           if (s < 4 || b < 4)
-            mma_bf16(tmem + buf * NC, da + (s >> 2) * (kGroupBytes >> 4) + (s & 3) * 2, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, b < 4 ? kId : kIdRope, s != 0);
+            mma_tmem_a(tmem + buf * NC, a + 8 * s, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, b < 4 ? kId : kIdRope, s != 0);
         mma_commit(bar(kBarEmpty + st));
         mma_commit(bar(kBarDone + buf));
         if (b >= 3 && w.tile + 1 == p.tiles) mma_commit(bar(kBarIdle));  // (this warp's last piece of the item)
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   __syncthreads();
   tc_fence_after();
   if (warp == kEnd + kWiden)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kBufs * NC) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 bool aligned(const void *p, uint64_t a) { return ((uintptr_t)p & (a - 1)) == 0; }

@@ -655,7 +655,7 @@ int ula_rows_sync(void *stream);
 #define ULA_DEBUG_BARRIERS 23
 int ula_rows_debug_hold(int barrier);
 /* The same for ula_rows_score and its barriers. */
-#define ULA_DEBUG_SCORE_BARRIERS 26
+#define ULA_DEBUG_SCORE_BARRIERS 44
 int ula_rows_debug_hold_score(int barrier);
 
 /*

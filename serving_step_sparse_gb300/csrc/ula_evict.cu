@@ -59,6 +59,11 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Places of a warp's run, where `blocks` blocks share n: whole groups of 4 for every lane.
+__host__ __device__ __forceinline__ uint32_t run_of(uint32_t n, uint32_t blocks) {
+  return ((n + blocks * kWarps - 1) / (blocks * kWarps) + 127) & ~127u;
+}
+
 struct Smem {
   uint32_t hist[3][kBins];
   uint32_t warp[kWarps];        // a scan's sums
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
   const uint32_t leave = n > p.budget ? n - p.budget : 0;
   const int32_t *address = p.address + (uint64_t)req * p.longest;
   // a warp's run of places [run0, run1), the block's [begin, ...)
-  const uint32_t run = ((n + blocks * kWarps - 1) / (blocks * kWarps) + 31) & ~31u;
+  const uint32_t run = run_of(n, blocks);
   const uint64_t block0 = (uint64_t)rank * kWarps * run, at0 = block0 + (uint64_t)warp * run;
   const uint32_t begin = block0 < n ? (uint32_t)block0 : n;
   const uint32_t run0 = at0 < n ? (uint32_t)at0 : n, run1 = at0 + run < n ? (uint32_t)at0 + run : n;
@@ -104,6 +109,14 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     return key_of((uint32_t)a < p.n_scores ? __ldg(p.scores + a) : 0.f);
   };
   auto key = [&](uint32_t i) -> uint32_t { return p.cached ? keys[i - begin] : gather(i); };
+  auto four = [&](uint32_t i, uint32_t (&k)[4]) {  // places i.. (a multiple of 4) of the run
+    if (p.cached) {
+      *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<const uint4 *>(keys + (i - begin));
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) k[j] = i + j < run1 ? gather(i + j) : 0;
+    }
+  };
   auto middle = [&](uint32_t i) { return i >= mid0 && i < mid1; };
 
   uint32_t limit = 0, below = 0;  // T, and how many keys lie below it
@@ -127,27 +140,38 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
         }
       };
       if (pass == 0) {
-        for (uint32_t i0 = run0; i0 < run1; i0 += 256) {  // (eight gathers in flight)
-          int32_t a[8];
-          uint32_t k[8];
+        // eight gathers in flight, and the addresses of the next eight
+        int32_t a[8];
+        auto addresses = [&](uint32_t i0) {
 #pragma unroll
           for (uint32_t j = 0; j < 8; ++j) {
             const uint32_t i = i0 + 32 * j + lane;
             a[j] = i < run1 ? __ldg(address + i) : -1;
           }
+        };
+        addresses(run0);
+        for (uint32_t i0 = run0; i0 < run1; i0 += 256) {
+          float v[8];
 #pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) k[j] = key_of((uint32_t)a[j] < p.n_scores ? __ldg(p.scores + a[j]) : 0.f);
+          for (uint32_t j = 0; j < 8; ++j) v[j] = (uint32_t)a[j] < p.n_scores ? __ldg(p.scores + a[j]) : 0.f;
+          addresses(i0 + 256);
 #pragma unroll
           for (uint32_t j = 0; j < 8; ++j) {
-            const uint32_t i = i0 + 32 * j + lane;
-            if (p.cached && i < run1) keys[i - begin] = k[j];
-            count(k[j], i < run1 && middle(i));
+            const uint32_t i = i0 + 32 * j + lane, k = key_of(v[j]);
+            if (p.cached && i < run1) keys[i - begin] = k;
+            count(k, i < run1 && middle(i));
           }
         }
+        __syncwarp();  // (a warp's keys are its own)
       } else {
-        for (uint32_t i0 = run0; i0 < run1; i0 += 32) {
-          const uint32_t i = i0 + lane;
-          count(i < run1 ? key(i) : 0, i < run1 && middle(i));
+        for (uint32_t i0 = run0; i0 < run1; i0 += 128) {
+          uint32_t k[4];
+          four(i0 + 4 * lane, k);
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t i = i0 + 4 * lane + j;
+            count(k[j], i < run1 && middle(i));
+          }
         }
       }
       meet();
@@ -191,13 +215,17 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
   // what leaves of the runs before this warp's
   uint32_t less = 0, equal = 0;
   if (leave) {
-    for (uint32_t i0 = run0; i0 < run1; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool in = i < run1 && middle(i);
-      const uint32_t k = i < run1 ? key(i) : 0;
-      less += __popc(__ballot_sync(0xffffffffu, in && k < limit));
-      equal += __popc(__ballot_sync(0xffffffffu, in && k == limit));
+    for (uint32_t i0 = run0; i0 < run1; i0 += 128) {
+      uint32_t k[4];
+      four(i0 + 4 * lane, k);
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) {
+        const uint32_t i = i0 + 4 * lane + j;
+        const bool in = i < run1 && middle(i);
+        less += in && k[j] < limit, equal += in && k[j] == limit;
+      }
     }
+    less = __reduce_add_sync(0xffffffffu, less), equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) s.less[warp] = less, s.equal[warp] = equal;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -215,20 +243,33 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
   }
   const uint32_t ties = leave - below;  // equal keys that leave: the first ones
   int32_t *kept = p.kept + (uint64_t)req * p.budget, *dropped = p.dropped + (uint64_t)req * p.dropped_room;
-  for (uint32_t i0 = run0; i0 < run1; i0 += 32) {
-    const uint32_t i = i0 + lane, before = (1u << lane) - 1;
-    const bool in = leave && i < run1 && middle(i);
-    const uint32_t k = in ? key(i) : 0;
-    const uint32_t ls = __ballot_sync(0xffffffffu, in && k < limit), eq = __ballot_sync(0xffffffffu, in && k == limit);
-    const uint32_t le = less + __popc(ls & before), ee = equal + __popc(eq & before);
-    const bool goes = in && (k < limit || (k == limit && ee < ties));
-    const uint32_t gone = le + (ee < ties ? ee : ties);  // before this place
-    if (i < run1) {
-      const int32_t a = __ldg(address + i);
-      if (goes) dropped[gone] = a;
-      else kept[i - gone] = a;
+  const uint32_t before = (1u << lane) - 1;
+  int32_t a[8];  // (the next addresses are on their way while these are placed)
+  auto addresses = [&](uint32_t i0) {
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint32_t i = i0 + 32 * j + lane;
+      a[j] = i < run1 ? __ldg(address + i) : -1;
     }
-    less += __popc(ls), equal += __popc(eq);
+  };
+  addresses(run0);
+  for (uint32_t i0 = run0; i0 < run1; i0 += 256) {
+    int32_t now[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) now[j] = a[j];
+    addresses(i0 + 256);
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint32_t i = i0 + 32 * j + lane;
+      const bool in = leave && i < run1 && middle(i);
+      const uint32_t k = in ? key(i) : 0;
+      const uint32_t ls = __ballot_sync(0xffffffffu, in && k < limit), eq = __ballot_sync(0xffffffffu, in && k == limit);
+      const uint32_t le = less + __popc(ls & before), ee = equal + __popc(eq & before);
+      const bool goes = in && (k < limit || (k == limit && ee < ties));
+      const uint32_t gone = le + (ee < ties ? ee : ties);  // before this place
+      if (i < run1) (goes ? dropped + gone : kept + (i - gone))[0] = now[j];
+      less += __popc(ls), equal += __popc(eq);
+    }
   }
   for (uint32_t i = n - leave + rank * kThreads + threadIdx.x; i < p.budget; i += blocks * kThreads) kept[i] = -1;
   for (uint32_t i = leave + rank * kThreads + threadIdx.x; i < p.dropped_room; i += blocks * kThreads) dropped[i] = -1;
@@ -256,7 +297,7 @@ extern "C" int ula_rows_evict(const float *scores, uint32_t n_scores, const int3
   uint32_t cluster = 1;
   while (cluster < kMostCluster && longest > cluster * 2048) cluster *= 2;
   if ((uint64_t)n_req * cluster > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
-  const uint32_t run = (((longest + cluster * kWarps - 1) / (cluster * kWarps)) + 31) & ~31u;
+  const uint32_t run = run_of(longest, cluster);
   p.cached = (uint64_t)run * kWarps <= kMostKeys;
   const uint32_t smem = (uint32_t)sizeof(Smem) + (p.cached ? run * kWarps * 4 : 0);
   auto kernel = cluster > 1 ? k_evict<true> : k_evict<false>;

@@ -122,22 +122,25 @@ __global__ void __launch_bounds__(256) k_score_commit(const __grid_constant__ Sc
 constexpr uint32_t kTile = 128;                      // rows per tile
 constexpr uint32_t kPieces = 5;                      // of a tile: 4 blocks of latents, the rope channels
 constexpr uint32_t kMostBufs = 4, kMostStages = 4;    // accumulators and pieces in TMEM
-constexpr uint32_t kEnd = 16, kWiden = 8;            // warps that finish the logits, that widen rows
+constexpr uint32_t kEnd = 8, kWiden = 8;             // warps that finish the logits, that widen rows
 constexpr uint32_t kIssue = 2;                       // and that issue products; then one that looks rows up, one for the queries
 constexpr uint32_t kThreads = (kEnd + kWiden + 4) * 32;  // (registers move between groups of 4 warps)
-// Launched with 72 registers a thread: 7 * 72 = 4 * 72 + 2 * 80 + 56.
-constexpr uint32_t kRegsWiden = 80, kRegsIssue = 56;
+// Launched with 96 registers a thread: 5 * 96 = 2 * 128 + 2 * 80 + 64.
+constexpr uint32_t kRegsEnd = 128, kRegsWiden = 80, kRegsIssue = 64;
+constexpr uint32_t kParts = kEnd / 4;                // a row's columns are shared by so many threads
 __device__ uint32_t g_late;                          // warps whose waits ran out, in all launches so far
 
 // mbarriers.  Full, Empty: a stage holds a piece, its products have ended; Done, Drained: an
 // accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
-// Free: both have been read; Query: the item's queries; Idle: the item's products have ended; End: an
-// issuing warp's have.  (A wait names its phase by its parity alone, so whoever waits for a phase has
-// waited for the one before it, or for a later one of those who opened that.)
+// Free: all three have been read; Sum: the rows' sums stand; Query: the item's queries (of a piece's
+// channels); Idle: the item's products with them have ended; End: an issuing warp's have.  (A wait names its phase by its parity alone, so
+// whoever waits for a phase has waited for the one before it, or for a later one of those who opened that.)
+constexpr uint32_t kTiles = 4;                       // tiles whose addresses, scales and sums stand at once
 enum {
   kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kMostBufs,
-  kBarPlace = kBarDrained + kMostBufs, kBarScale = kBarPlace + 2, kBarFree = kBarScale + 2, kBarQuery = kBarFree + 2,
-  kBarIdle = kBarQuery + 1, kBarEnd = kBarIdle + 1, kBars = kBarEnd + kIssue
+  kBarPlace = kBarDrained + kMostBufs, kBarScale = kBarPlace + kTiles, kBarFree = kBarScale + kTiles,
+  kBarSum = kBarFree + kTiles, kBarQuery = kBarSum + kTiles, kBarIdle = kBarQuery + kPieces, kBarEnd = kBarIdle + kPieces,
+  kBars = kBarEnd + kIssue
 };
 static_assert(kBars == ULA_DEBUG_SCORE_BARRIERS, "as the header says");
 
@@ -147,10 +150,11 @@ struct Shared {
   static constexpr uint32_t bufs = NC == 128 ? 3 : kMostBufs, stages = NC == 128 ? 2 : kMostStages;
   static_assert(bufs * NC + stages * 64 <= 512, "columns of TMEM");
   static constexpr uint32_t q = 0;                                  // [9][NC][128 B]
-  static constexpr uint32_t scale = 9 * NC * 128;                   // [2][128][4]
-  static constexpr uint32_t place = scale + 2 * kTile * 16;         // [2][128] the rows' addresses (a query's: no row)
-  static constexpr uint32_t target = place + 2 * kTile * 8;         // [2][128] their places in scores
-  static constexpr uint32_t lse = target + 2 * kTile * 4;           // [2][2][NC] -lse in units of log2, factors
+  static constexpr uint32_t scale = 9 * NC * 128;                   // [kTiles][128][4]
+  static constexpr uint32_t place = scale + kTiles * kTile * 16;    // [kTiles][128] the rows' addresses (a query's: no row)
+  static constexpr uint32_t target = place + kTiles * kTile * 8;    // [kTiles][128] their places in scores
+  static constexpr uint32_t sum = target + kTiles * kTile * 4;      // [kTiles][kParts][128]
+  static constexpr uint32_t lse = sum + kTiles * kParts * kTile * 4;     // [2][2][NC] -lse in units of log2, factors
   static constexpr uint32_t bars = lse + 4 * NC * 4;
   static constexpr uint32_t words = bars + kBars * 8;
   static constexpr uint32_t bytes = words + 16 + 1024;              // (+ alignment of the base)
@@ -166,8 +170,8 @@ struct Place {
 // Codes are exact in f16, by one conversion for two of them.
 // Nothing but the sum over a row's columns of exp2(z - lse) leaves the block, so the pieces of a
 // tile stream: eight warps widen them into a ring of stages, two warps issue their products in turn into
-// a ring of accumulators, sixteen warps take them up, a row per thread and a quarter of the columns,
-// and add a row's weights to its sum.
+// a ring of accumulators, eight warps take them up, a row per thread and half of the columns,
+// and one adds the rows' sums to those in memory.
 // The widened rows stand in TMEM, as the products' A: through shared memory a product of K = 16 read 8 KB of
 // operands at what shared memory gives in all (118 B a clock), and every other access of the widening
 // waited for it; now it reads the queries' 4 KB.
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   extern __shared__ uint8_t raw_smem[];
   using L = Shared<NC>;
   constexpr uint32_t S = L::stages, kBufs = L::bufs;
-  constexpr int HG = NC / 4, kRead = HG < 16 ? HG : 16;  // columns of a thread, and of one read
+  constexpr int HG = NC / kParts, kRead = HG < 32 ? HG : 32;  // columns of a thread, and of one read
   const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
   uint8_t *sm = raw_smem + (base - smem_u32(raw_smem));
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,9 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < kMostStages; ++i) mbar_init(bar(kBarFull + i), kWiden), mbar_init(bar(kBarEmpty + i), 1);
     for (uint32_t i = 0; i < kMostBufs; ++i) mbar_init(bar(kBarDone + i), 1), mbar_init(bar(kBarDrained + i), kEnd);
-    for (uint32_t i = 0; i < 2; ++i)
-      mbar_init(bar(kBarPlace + i), 1), mbar_init(bar(kBarScale + i), 32), mbar_init(bar(kBarFree + i), kEnd + kWiden);
-    mbar_init(bar(kBarQuery), 1), mbar_init(bar(kBarIdle), kIssue);
+    for (uint32_t i = 0; i < kTiles; ++i) {
+      mbar_init(bar(kBarPlace + i), 1), mbar_init(bar(kBarScale + i), 1);
+      mbar_init(bar(kBarFree + i), kEnd + kWiden + 1), mbar_init(bar(kBarSum + i), kEnd);
+    }
+    for (uint32_t i = 0; i < kPieces; ++i) mbar_init(bar(kBarQuery + i), 1), mbar_init(bar(kBarIdle + i), 1);
     for (uint32_t i = 0; i < kIssue; ++i) mbar_init(bar(kBarEnd + i), 1);
     if (p.hold < kBars) {
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar(p.hold)) : "memory");
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   }
   // (An entry without a row stands for 656 bytes of the queries, whose products nobody adds up.  So does what
   // is read before its time, after a wait that ran out.)
-  for (uint32_t i = threadIdx.x; i < 2 * kTile; i += kThreads) {
+  for (uint32_t i = threadIdx.x; i < kTiles * kTile; i += kThreads) {
     reinterpret_cast<uint64_t *>(sm + L::place)[i] = (uint64_t)p.a.q;
     reinterpret_cast<uint32_t *>(sm + L::target)[i] = 0xffffffffu;
   }
@@ -219,31 +225,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
 
   bool ok = true;  // false once a wait has run out
   if (warp < kEnd) {
-    // ---- logits, weights, sums: this thread's row and HG columns
+    // ---- logits, weights, sums: this thread's row and HG columns.  Whether the next accumulator stands is
+    // asked before this one's numbers are added up.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEnd));
     const uint32_t quad = warp & 3, grp = warp >> 2, mine = 32 * quad + lane;
     const uint32_t lanes = tmem + (quad << 21) + grp * HG;
-    uint32_t items = 0;
+    uint32_t items = 0, stands = 0;
     for (uint32_t n = 0; n < count; ++n, step()) {
-      const uint32_t par = n & 1;
-      if (n == 0 || w.tile == 0) {
-        if (!(ok = warp_wait(bar(kBarQuery), items & 1))) break;
+      const uint32_t at = n % kTiles, par = n / kTiles & 1;
+      if (n == 0 || w.tile == 0) {  // (the lse come with the rope channels)
+        if (!(ok = warp_wait(bar(kBarQuery + 4), items & 1))) break;
         ++items;
       }
-      ok = warp_wait(bar(kBarPlace + par), (n >> 1) & 1);
-      if (!(ok = ok && warp_wait(bar(kBarScale + par), (n >> 1) & 1))) break;
-      const float4 s4 = *reinterpret_cast<const float4 *>(sm + L::scale + (par * kTile + mine) * 16);
-      const uint32_t target = reinterpret_cast<const uint32_t *>(sm + L::target)[par * kTile + mine];
+      if (!(ok = warp_wait(bar(kBarScale + at), par))) break;
+      const float4 s4 = *reinterpret_cast<const float4 *>(sm + L::scale + (at * kTile + mine) * 16);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarFree + par));
+      if (lane == 0) mbar_arrive(bar(kBarFree + at));
       float z[HG];
 #pragma unroll
       for (uint32_t b = 0; b < kPieces; ++b) {
         const uint32_t g = n * kPieces + b, buf = g % kBufs;
-        if (!(ok = warp_wait(bar(kBarDone + buf), (g / kBufs) & 1))) break;
+        if (!__all_sync(0xffffffffu, stands) && !(ok = warp_wait(bar(kBarDone + buf), (g / kBufs) & 1))) break;
         tc_fence_after();
-        const float s = (b == 0 ? s4.x : b == 1 ? s4.y : b == 2 ? s4.z : b == 3 ? s4.w : 1.f) * p.c0;
         float x[kRead];
         tmem_ld<kRead>(lanes + buf * NC, x);
+        stands = mbar_ended(bar(kBarDone + (g + 1) % kBufs), ((g + 1) / kBufs) & 1);
         if (b == 4) {  // the latents' part as it was before its column was scaled, less the lse
           const float *l = reinterpret_cast<const float *>(sm + L::lse) + ((items - 1) & 1) * 2 * NC + grp * HG;
 #pragma unroll
@@ -253,32 +259,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
             fma2(z[c + 2], z[c + 3], f4.z, f4.w, l4.z, l4.w);
           }
         }
+        const float s = (b == 0 ? s4.x : b == 1 ? s4.y : b == 2 ? s4.z : b == 3 ? s4.w : 1.f) * p.c0;
 #pragma unroll
         for (int c = 0; c < HG; c += kRead) {
           if (c) tmem_ld<kRead>(lanes + buf * NC + c, x);
           tc_wait_ld();
+          if (c + kRead == HG) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarDrained + buf));
+          }
 #pragma unroll
           for (int h = 0; h < kRead; h += 2) {
             if (b == 0) mul2(z[c + h], z[c + h + 1], s, x[h], x[h + 1]);
             else fma2(z[c + h], z[c + h + 1], s, x[h], x[h + 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarDrained + buf));
       }
       if (!ok) break;
       // a weight is between 0 and 1, and 0 where it is not a number (what .sat makes of one)
-      float total = 0.f;
+      float total[4] = {};
 #pragma unroll
       for (int c = 0; c < HG; c += 4)
-        total += (__saturatef(ex2(z[c])) + __saturatef(ex2(z[c + 1]))) + (__saturatef(ex2(z[c + 2])) + __saturatef(ex2(z[c + 3])));
-      if (target != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target, __float2ull_rn(total * p.unit));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[i] += __saturatef(ex2(z[c + i]));
+      reinterpret_cast<float *>(sm + L::sum)[(at * kParts + grp) * kTile + mine] = (total[0] + total[1]) + (total[2] + total[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarSum + at));
     }
   } else if (warp < kEnd + kWiden) {
     // ---- widening: a warp 16 rows of every piece (half of its 32 lanes of TMEM); four lanes share a row
     // and hold another one 8 rows on, 32 bytes of each row's 128.  The loads of the next two pieces are in flight.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
     const uint32_t cw = warp - kEnd, first = 32 * (cw & 3) + 16 * (cw >> 2), r0 = first + (lane >> 2), ch = lane & 3;
     const uint32_t mine = tmem + kBufs * NC + (first << 16);
     const uint32_t pieces = count * kPieces;
@@ -286,11 +298,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     auto fetch = [&](uint4 (&raw)[4], uint32_t g) -> bool {
       const uint32_t n = g / kPieces, b = g - n * kPieces;
       if (b == 0) {
-        if (!warp_wait(bar(kBarPlace + (n & 1)), (n >> 1) & 1)) return false;
-        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + (n & 1) * kTile + r0;
+        const uint32_t at = n % kTiles;
+        if (!warp_wait(bar(kBarPlace + at), n / kTiles & 1)) return false;
+        const uint64_t *place = reinterpret_cast<const uint64_t *>(sm + L::place) + at * kTile + r0;
         row[0] = place[0] + ch * 16, row[1] = place[8] + ch * 16;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarFree + (n & 1)));
+        if (lane == 0) mbar_arrive(bar(kBarFree + at));
       }
       const uint32_t at = b < 4 ? b * 128 : ULA_ROW_LATENT + 16;
 #pragma unroll
@@ -339,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     for (uint32_t g = which; g < pieces; g += kIssue) {
       const uint32_t n = g / kPieces, b = g - n * kPieces, st = g % S, buf = g % kBufs;
       for (; tile < n; ++tile) step();
-      if (b < 2 && (n == 0 || w.tile == 0)) {
-        ok = ok && warp_wait(bar(kBarQuery), items & 1);
-        ++items;
+      if (n == 0 || w.tile == 0) {
+        if (b < 2) ++items;
+        ok = ok && warp_wait(bar(kBarQuery + b), (items - 1) & 1);
       }
       ok = ok && warp_wait(bar(kBarFull + st), (g / S) & 1);
       if (g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
@@ -355,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
             mma_tmem_a(tmem + buf * NC, a + 8 * s, db + (s >> 2) * (NC * 128 >> 4) + (s & 3) * 2, b < 4 ? kId : kIdRope, s != 0);
         mma_commit(bar(kBarEmpty + st));
         mma_commit(bar(kBarDone + buf));
-        if (b >= 3 && w.tile + 1 == p.tiles) mma_commit(bar(kBarIdle));  // (this warp's last piece of the item)
+        if (w.tile + 1 == p.tiles) mma_commit(bar(kBarIdle + b));
       }
       __syncwarp();
     }
@@ -385,21 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     };
     if (count) fetch();
     for (uint32_t n = 0; n < count; ++n) {
-      const uint32_t par = n & 1;
-      if (n > 1 && !(ok = warp_wait(bar(kBarFree + par), (n >> 1 & 1) ^ 1))) break;
+      const uint32_t at = n % kTiles;
+      if (n >= kTiles && !(ok = warp_wait(bar(kBarFree + at), (n / kTiles & 1) ^ 1))) break;
       uint64_t row[4];
+      float4 scale[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
-        const uint32_t r = par * kTile + lane + 32 * j;
         const bool in = (uint32_t)u[j] < p.a.n_rows && (uint32_t)to[j] < p.a.n_scores;
         row[j] = in ? (uint64_t)p.a.rows + (uint64_t)(uint32_t)u[j] * ULA_ROW_BYTES : (uint64_t)p.a.q;
-        reinterpret_cast<uint64_t *>(sm + L::place)[r] = row[j];
-        reinterpret_cast<uint32_t *>(sm + L::target)[r] = in ? (uint32_t)to[j] : 0xffffffffu;
-        copy16(base + L::scale + r * 16, (const void *)(row[j] + ULA_ROW_LATENT), 16);
+        reinterpret_cast<uint64_t *>(sm + L::place)[at * kTile + lane + 32 * j] = row[j];
+        reinterpret_cast<uint32_t *>(sm + L::target)[at * kTile + lane + 32 * j] = in ? (uint32_t)to[j] : 0xffffffffu;
+        scale[j] = __ldg(reinterpret_cast<const float4 *>(row[j] + ULA_ROW_LATENT));
       }
-      copy_arrive(bar(kBarScale + par));
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarPlace + par));
+      if (lane == 0) mbar_arrive(bar(kBarPlace + at));
       if (n) {  // into L2 ahead of the loads, by lines: a bulk prefetch of a row takes its engine 64 clocks
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j)
@@ -408,24 +420,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       }
       step();
       if (n + 1 < count) fetch();
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) reinterpret_cast<float4 *>(sm + L::scale)[at * kTile + lane + 32 * j] = scale[j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarScale + at));
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   if (warp == kEnd + kWiden + kIssue + 1) {
-    // ---- an item's queries, once the products that read the last one's have ended
-    const uint32_t items = count ? (uint32_t)((from + count - 1) / p.tiles) - w.item + 1 : 0;
-    uint32_t i = 0;
-    for (; i < items; ++i) {
-      if (i && !(ok = warp_wait(bar(kBarIdle), (i - 1) & 1))) break;
-      if (elect_one()) {
-        const uint8_t *image = p.images + (uint64_t)(w.item + i) * Image<NC>::bytes;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(kBarQuery)), "r"(Image<NC>::bytes) : "memory");
-        for (uint32_t k = 0; k < 9; ++k) copy_bulk(base + L::q + k * NC * 128, image + k * NC * 128, NC * 128, bar(kBarQuery));
-        copy_bulk(base + L::lse + (i & 1) * 2 * NC * 4, image + Image<NC>::lse, 2 * NC * 4, bar(kBarQuery));
+    // ---- an item's queries, once the products that read the last one's have ended; a tile's sums, as whole
+    // numbers, to those in memory (four rows a lane)
+    uint32_t items = 0, begun = 0;  // items, and copies of pieces, begun
+    auto load_queries = [&](uint32_t item) -> bool {  // piece by piece, as the last item's are done with
+      for (uint32_t b = 0; b < kPieces; ++b, ++begun) {
+        if (items && !(warp_wait(bar(kBarIdle + b), (items - 1) & 1) && warp_wait(bar(kBarQuery + b), (items - 1) & 1))) return false;
+        if (elect_one()) {
+          const uint8_t *image = p.images + (uint64_t)item * Image<NC>::bytes + b * 2 * NC * 128;
+          const uint32_t bytes = b < 4 ? 2 * NC * 128 : NC * 128, more = b < 4 ? 0 : 2 * NC * 4, to = bar(kBarQuery + b);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(to), "r"(bytes + more) : "memory");
+          copy_bulk(base + L::q + b * 2 * NC * 128, image, bytes, to);
+          if (more) copy_bulk(base + L::lse + (items & 1) * 2 * NC * 4, image + bytes, more, to);
+        }
+        __syncwarp();
+      }
+      ++items;
+      return true;
+    };
+    if (count) ok = load_queries(w.item);
+    for (uint32_t n = 0; n < count; ++n) {
+      const uint32_t at = n % kTiles;
+      step();
+      if (w.tile == 0 && n + 1 < count && !(ok = load_queries(w.item))) break;
+      if (!(ok = warp_wait(bar(kBarSum + at), n / kTiles & 1))) break;
+      const float *sum = reinterpret_cast<const float *>(sm + L::sum) + at * kParts * kTile + lane;
+      const uint32_t *target = reinterpret_cast<const uint32_t *>(sm + L::target) + at * kTile + lane;
+#pragma unroll
+      for (uint32_t j = 0; j < kTile; j += 32) {
+        float total = 0.f;
+#pragma unroll
+        for (uint32_t i = 0; i < kParts; ++i) total += sum[i * kTile + j];
+        if (target[j] != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target[j], __float2ull_rn(total * p.unit));
       }
       __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarFree + at));
     }
-    if (i) ok = warp_wait(bar(kBarQuery), (i - 1) & 1) && ok;  // (no copy is in flight when the block ends)
+    for (uint32_t b = 0; b < kPieces; ++b) {  // (no copy is in flight when the block ends)
+      const uint32_t copies = begun / kPieces + (begun % kPieces > b ? 1 : 0);
+      if (copies) ok = warp_wait(bar(kBarQuery + b), (copies - 1) & 1) && ok;
+    }
   }
   if (!ok && lane == 0) atomicAdd(&g_late, 1u);
   tc_fence_before();

@@ -9,8 +9,8 @@
 //
 // Bound by its bytes (12 an address: the address, its score, one of the outputs) and, for short lists,
 // by the chain of a few passes.  A request's list is spread over a cluster of up to 8 blocks, so that
-// 32 requests fill the GPU; keys are gathered once and stay in shared memory; histograms are summed
-// through each other's shared memory.  The partition needs no barrier: a warp owns a run of places,
+// 32 requests fill the GPU; keys are gathered once and stay in shared memory; histograms are summed in
+// the first block's (each block reading all of them took 5,000 to 13,000 clocks a pass).  The partition needs no barrier: a warp owns a run of places,
 // knows how many of the runs before it leave, and goes on by ballots.
 #include <cstdint>
 
@@ -41,22 +41,20 @@ __device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   return at;
 }
-__device__ __forceinline__ uint32_t ld_remote(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void add_remote(uint32_t at, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint4 ld_remote4(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void st_remote2(uint32_t at, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
 }
 
-// A key per score, in the scores' order; -0 is 0, a NaN is larger than all numbers.
+// A key per score, in the scores' order; -0 is 0, a NaN is larger than all numbers.  kStays is larger than
+// every key: a place that may not leave, or lies behind the list.
+constexpr uint32_t kStays = 0xffffffffu, kZero = 0x80000000u;
 __device__ __forceinline__ uint32_t key_of(float s) {
-  if (s != s) return 0xffffffffu;
   const uint32_t u = __float_as_uint(s + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+  return s == s ? k : kStays - 1;
 }
 
 // Places of a warp's run, where `blocks` blocks share n: whole groups of 4 for every lane.
@@ -65,18 +63,19 @@ __host__ __device__ __forceinline__ uint32_t run_of(uint32_t n, uint32_t blocks)
 }
 
 struct Smem {
-  uint32_t hist[3][kBins];
+  uint32_t hist[2][kBins];      // the first pass's of this block; in the first block, the sum of a pass
   uint32_t warp[kWarps];        // a scan's sums
-  uint32_t found[2];            // the digit, and how many keys below it
-  uint32_t less[kWarps], equal[kWarps];
-  uint32_t sums[2];             // the block's (less, equal)
+  uint2 found[3];               // a pass's digit, and how many keys below it
+  uint2 sums[kWarps][kMostCluster];  // the runs' (less, equal)
+  uint2 pad;                    // (the keys start on 16 bytes)
 };
+static_assert(sizeof(Smem) % 16 == 0, "keys are read by fours");
 
 template <bool kCluster>
 __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t raw[];
+  extern __shared__ uint4 raw[];
   Smem &s = *reinterpret_cast<Smem *>(raw);
-  uint32_t *keys = raw + sizeof(Smem) / 4;
+  uint32_t *keys = reinterpret_cast<uint32_t *>(raw) + sizeof(Smem) / 4;
   uint32_t blocks = 1, rank = 0;
   if (kCluster) {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
@@ -91,127 +90,146 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     else
       __syncthreads();
   };
-  for (uint32_t i = threadIdx.x; i < 3 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+  for (uint32_t i = threadIdx.x; i < 2 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t given = __ldg(p.length + req);
   const uint32_t n = given < 0 ? 0 : (uint32_t)given < p.longest ? (uint32_t)given : p.longest;
   const uint32_t leave = n > p.budget ? n - p.budget : 0;
   const int32_t *address = p.address + (uint64_t)req * p.longest;
-  // a warp's run of places [run0, run1), the block's [begin, ...)
+  // A warp's run of places [run0, run1), and where its keys stand.  The blocks take the runs in turn: a
+  // list's last places were written one at a time, with other requests' between them, and their scores
+  // take a load each where a prompt's share one.
   const uint32_t run = run_of(n, blocks);
-  const uint64_t block0 = (uint64_t)rank * kWarps * run, at0 = block0 + (uint64_t)warp * run;
-  const uint32_t begin = block0 < n ? (uint32_t)block0 : n;
+  const uint64_t at0 = ((uint64_t)warp * blocks + rank) * run;
   const uint32_t run0 = at0 < n ? (uint32_t)at0 : n, run1 = at0 + run < n ? (uint32_t)at0 + run : n;
+  uint32_t *const mine = keys + warp * run;
   const uint32_t mid0 = p.first, mid1 = n - (p.last < n ? p.last : n);  // places that may leave
-  auto gather = [&](uint32_t i) -> uint32_t {
-    const int32_t a = __ldg(address + i);
-    return key_of((uint32_t)a < p.n_scores ? __ldg(p.scores + a) : 0.f);
-  };
-  auto key = [&](uint32_t i) -> uint32_t { return p.cached ? keys[i - begin] : gather(i); };
-  auto four = [&](uint32_t i, uint32_t (&k)[4]) {  // places i.. (a multiple of 4) of the run
-    if (p.cached) {
-      *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<const uint4 *>(keys + (i - begin));
-    } else {
+  // addresses of the places i0 + lane, i0 + 32 + lane, ... (-1 behind the run); scores; the key of place i
+  auto addresses = [&](uint32_t i0, auto &a) {
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) k[j] = i + j < run1 ? gather(i + j) : 0;
+    for (uint32_t j = 0; j < sizeof a / 4; ++j) {
+      const uint32_t i = i0 + 32 * j + lane;
+      a[j] = i < run1 ? __ldg(address + i) : -1;
     }
   };
-  auto middle = [&](uint32_t i) { return i >= mid0 && i < mid1; };
+  auto score = [&](int32_t a) { return (uint32_t)a < p.n_scores ? __ldg(p.scores + a) : 0.f; };
+  auto key_at = [&](uint32_t i, float v) { return i >= mid0 && i < mid1 && i < run1 ? key_of(v) : kStays; };
+  auto four = [&](uint32_t i, uint32_t (&k)[4]) {  // the keys of places i..
+    if (p.cached) {
+      *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<const uint4 *>(mine + (i - run0));
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) k[j] = key_at(i + j, i + j < run1 ? score(__ldg(address + i + j)) : 0.f);
+    }
+  };
 
   uint32_t limit = 0, below = 0;  // T, and how many keys lie below it
   if (leave) {
-    __syncthreads();  // (the histograms are clear)
-    uint32_t digits = 0;
+    meet();  // (the histograms are clear)
+    uint32_t digits = 0, zeros = 0;
 #pragma unroll
     for (uint32_t pass = 0; pass < 3; ++pass) {
       const uint32_t shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, mask = pass == 2 ? 1023 : 2047;
-      auto count = [&](uint32_t k, bool in) {
+      // Many scores may be equal (addresses that were never selected have 0), and adding to one place takes
+      // a lane after the other: zeros are counted in a register, and so is a run of equal digits.
+      uint32_t held = 0, times = 0;
+      const uint32_t sums = remote(smem_u32(&s.hist[1][0]), 0);
+      auto add = [&](uint32_t digit, uint32_t by) {  // few keys are left after the first pass: straight to the sums
+        if (pass == 0) atomicAdd(&s.hist[0][digit], by);
+        else if (kCluster) add_remote(sums + 4 * digit, by);
+        else atomicAdd(&s.hist[1][digit], by);
+      };
+      auto flush = [&] {
+        if (times) add(held, times);
+      };
+      auto count = [&](uint32_t k) {
         const uint32_t digit = (k >> shift) & mask;
-        in = in && (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == digits);
-        // Most scores may be equal (addresses that were never selected), and adding to one place takes
-        // a lane after the other: the digit of the first lane that has one is counted once for all of its lanes.
-        uint32_t todo = __ballot_sync(0xffffffffu, in);
-        if (todo) {
-          const uint32_t lead = __ffs(todo) - 1, d = __shfl_sync(0xffffffffu, digit, lead);
-          const uint32_t same = __ballot_sync(0xffffffffu, in && digit == d);
-          if (lane == lead) atomicAdd(&s.hist[pass][d], __popc(same));
-          if (in && digit != d) atomicAdd(&s.hist[pass][digit], 1u);
+        if (pass == 0 && k == kZero) {
+          ++zeros;
+        } else if (pass == 0 || ((k >> (pass == 1 ? 21 : 10)) == digits && k != kZero)) {
+          if (digit != held) flush(), held = digit, times = 0;
+          ++times;
         }
       };
       if (pass == 0) {
-        // eight gathers in flight, and the addresses of the next eight
-        int32_t a[8];
-        auto addresses = [&](uint32_t i0) {
+        // sixteen gathers in flight, and the addresses of the next sixteen
+        int32_t a[16];
+        addresses(run0, a);
+        for (uint32_t i0 = run0; i0 < run1; i0 += 512) {
+          float v[16];
 #pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) {
-            const uint32_t i = i0 + 32 * j + lane;
-            a[j] = i < run1 ? __ldg(address + i) : -1;
-          }
-        };
-        addresses(run0);
-        for (uint32_t i0 = run0; i0 < run1; i0 += 256) {
-          float v[8];
+          for (uint32_t j = 0; j < 16; ++j) v[j] = score(a[j]);
+          addresses(i0 + 512, a);
 #pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) v[j] = (uint32_t)a[j] < p.n_scores ? __ldg(p.scores + a[j]) : 0.f;
-          addresses(i0 + 256);
-#pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) {
-            const uint32_t i = i0 + 32 * j + lane, k = key_of(v[j]);
-            if (p.cached && i < run1) keys[i - begin] = k;
-            count(k, i < run1 && middle(i));
+          for (uint32_t j = 0; j < 16; ++j) {
+            const uint32_t i = i0 + 32 * j + lane, k = key_at(i, v[j]);
+            if (p.cached && i0 + (j & ~3u) * 32 < run1) mine[i - run0] = k;  // (a run is whole groups of 128 places)
+            count(k);
           }
         }
         __syncwarp();  // (a warp's keys are its own)
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
       } else {
         for (uint32_t i0 = run0; i0 < run1; i0 += 128) {
           uint32_t k[4];
           four(i0 + 4 * lane, k);
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t i = i0 + 4 * lane + j;
-            count(k[j], i < run1 && middle(i));
-          }
+          for (uint32_t j = 0; j < 4; ++j) count(k[j]);
+        }
+      }
+      flush();
+      if (lane == 0 && zeros && (pass == 0 || (kZero >> (pass == 1 ? 21 : 10)) == digits)) add((kZero >> shift) & mask, zeros);
+      if (pass == 0) {
+        __syncthreads();
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t d = threadIdx.x + i * kThreads, by = s.hist[0][d];
+          if (!kCluster) s.hist[1][d] = by;
+          else if (by) add_remote(sums + 4 * d, by);
         }
       }
       meet();
-      // the digit where the count of smaller keys passes what is still to leave
-      uint4 c = make_uint4(0, 0, 0, 0);
-      for (uint32_t r = 0; r < blocks; ++r) {
-        const uint32_t at = smem_u32(&s.hist[pass][4 * threadIdx.x]);
-        const uint4 v = kCluster ? ld_remote4(remote(at, r)) : *reinterpret_cast<const uint4 *>(&s.hist[pass][4 * threadIdx.x]);
-        c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
-      }
-      const uint32_t mine = c.x + c.y + c.z + c.w;
-      uint32_t sum = mine;
+      if (rank == 0) {  // the digit where the count of smaller keys passes what is still to leave
+        uint4 &bins = *reinterpret_cast<uint4 *>(&s.hist[1][4 * threadIdx.x]);
+        const uint4 c = bins;
+        bins = make_uint4(0, 0, 0, 0);  // (the others add to it again after the meeting below)
+        const uint32_t mine = c.x + c.y + c.z + c.w;
+        uint32_t sum = mine;
 #pragma unroll
-      for (uint32_t d = 1; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (lane == 31) s.warp[warp] = sum;
-      __syncthreads();
-      uint32_t before = sum - mine;
-      for (uint32_t w = 0; w < warp; ++w) before += s.warp[w];
-      const uint32_t want = leave - below;  // >= 1: the digit of the want-th smallest
-      if (before < want && want <= before + mine) {
-        uint32_t d = 4 * threadIdx.x;
-        if (want > before + c.x) {
-          before += c.x, ++d;
-          if (want > before + c.y) {
-            before += c.y, ++d;
-            if (want > before + c.z) before += c.z, ++d;
-          }
+        for (uint32_t d = 1; d < 32; d <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += o;
         }
-        s.found[0] = d, s.found[1] = before;
+        if (lane == 31) s.warp[warp] = sum;
+        __syncthreads();
+        uint32_t before = sum - mine;
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) before += w < warp ? s.warp[w] : 0;
+        const uint32_t want = leave - below;  // >= 1: the digit of the want-th smallest
+        if (before < want && want <= before + mine) {
+          uint32_t d = 4 * threadIdx.x;
+          if (want > before + c.x) {
+            before += c.x, ++d;
+            if (want > before + c.y) {
+              before += c.y, ++d;
+              if (want > before + c.z) before += c.z, ++d;
+            }
+          }
+          if (!kCluster) s.found[pass] = make_uint2(d, before);
+          else
+            for (uint32_t r = 0; r < blocks; ++r) st_remote2(remote(smem_u32(&s.found[pass]), r), d, before);
+        }
       }
-      __syncthreads();
-      digits = (digits << (pass == 2 ? 10 : 11)) | s.found[0];
-      below += s.found[1];
+      meet();
+      digits = (digits << (pass == 2 ? 10 : 11)) | s.found[pass].x;
+      below += s.found[pass].y;
     }
     limit = digits;
   }
 
+  int32_t a[8];  // addresses to be placed: the next are on their way while others are
+  addresses(run0, a);
   // what leaves of the runs before this warp's
   uint32_t less = 0, equal = 0;
   if (leave) {
@@ -219,61 +237,52 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
       uint32_t k[4];
       four(i0 + 4 * lane, k);
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        const uint32_t i = i0 + 4 * lane + j;
-        const bool in = i < run1 && middle(i);
-        less += in && k[j] < limit, equal += in && k[j] == limit;
-      }
+      for (uint32_t j = 0; j < 4; ++j) less += k[j] < limit, equal += k[j] == limit;
     }
     less = __reduce_add_sync(0xffffffffu, less), equal = __reduce_add_sync(0xffffffffu, equal);
-    if (lane == 0) s.less[warp] = less, s.equal[warp] = equal;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t a = 0, b = 0;
-      for (uint32_t w = 0; w < kWarps; ++w) a += s.less[w], b += s.equal[w];
-      s.sums[0] = a, s.sums[1] = b;
+    if (lane < blocks) {  // to every block
+      if (kCluster) st_remote2(remote(smem_u32(&s.sums[warp][rank]), lane), less, equal);
+      else s.sums[warp][0] = make_uint2(less, equal);
     }
     meet();
     less = equal = 0;
-    for (uint32_t r = 0; r < rank; ++r) {
-      less += ld_remote(remote(smem_u32(&s.sums[0]), r));
-      equal += ld_remote(remote(smem_u32(&s.sums[1]), r));
+    for (uint32_t i = lane; i < warp * blocks + rank; i += 32) {
+      const uint2 x = s.sums[i / blocks][i % blocks];
+      less += x.x, equal += x.y;
     }
-    for (uint32_t w = 0; w < warp; ++w) less += s.less[w], equal += s.equal[w];
+    less = __reduce_add_sync(0xffffffffu, less), equal = __reduce_add_sync(0xffffffffu, equal);
   }
   const uint32_t ties = leave - below;  // equal keys that leave: the first ones
   int32_t *kept = p.kept + (uint64_t)req * p.budget, *dropped = p.dropped + (uint64_t)req * p.dropped_room;
   const uint32_t before = (1u << lane) - 1;
-  int32_t a[8];  // (the next addresses are on their way while these are placed)
-  auto addresses = [&](uint32_t i0) {
-#pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) {
-      const uint32_t i = i0 + 32 * j + lane;
-      a[j] = i < run1 ? __ldg(address + i) : -1;
-    }
-  };
-  addresses(run0);
   for (uint32_t i0 = run0; i0 < run1; i0 += 256) {
     int32_t now[8];
+    uint32_t ls[8], eq[8];
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) now[j] = a[j];
-    addresses(i0 + 256);
+    addresses(i0 + 256, a);
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) {
       const uint32_t i = i0 + 32 * j + lane;
-      const bool in = leave && i < run1 && middle(i);
-      const uint32_t k = in ? key(i) : 0;
-      const uint32_t ls = __ballot_sync(0xffffffffu, in && k < limit), eq = __ballot_sync(0xffffffffu, in && k == limit);
-      const uint32_t le = less + __popc(ls & before), ee = equal + __popc(eq & before);
-      const bool goes = in && (k < limit || (k == limit && ee < ties));
-      const uint32_t gone = le + (ee < ties ? ee : ties);  // before this place
-      if (i < run1) (goes ? dropped + gone : kept + (i - gone))[0] = now[j];
-      less += __popc(ls), equal += __popc(eq);
+      uint32_t k = kStays;
+      if (leave && i < run1) k = p.cached ? mine[i - run0] : key_at(i, score(now[j]));
+      ls[j] = __ballot_sync(0xffffffffu, k < limit), eq[j] = __ballot_sync(0xffffffffu, k == limit);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint32_t i = i0 + 32 * j + lane;
+      const uint32_t ee = equal + __popc(eq[j] & before);
+      const uint32_t gone = less + __popc(ls[j] & before) + (ee < ties ? ee : ties);  // before this place
+      const bool goes = (ls[j] >> lane & 1) || ((eq[j] >> lane & 1) && ee < ties);
+      if (i < run1) {
+        if (goes) dropped[gone] = now[j];
+        else kept[i - gone] = now[j];
+      }
+      less += __popc(ls[j]), equal += __popc(eq[j]);
     }
   }
   for (uint32_t i = n - leave + rank * kThreads + threadIdx.x; i < p.budget; i += blocks * kThreads) kept[i] = -1;
   for (uint32_t i = leave + rank * kThreads + threadIdx.x; i < p.dropped_room; i += blocks * kThreads) dropped[i] = -1;
-  if (kCluster) meet();  // (a block's shared memory stays until the others have read it)
 }
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }

@@ -132,6 +132,16 @@ class UlaCache:
     def free(self, base: int, n: int) -> None:
         ula.ula_free(self.ctx, base, n)
 
+    def free_each(self, addresses: torch.Tensor) -> None:
+        """Frees single addresses (int32, on any device, in any order; negative ones, such as the pads of
+        ``rows.evict``'s dropped, stand for none), one ``free`` for each run of neighbours.  Reads them
+        on the host.  Not atomic: an address that is not live raises after earlier runs have gone."""
+        a = np.unique(addresses.detach().cpu().numpy())
+        a = a[a >= 0]
+        for run in np.split(a, np.flatnonzero(np.diff(a) != 1) + 1):
+            if len(run):
+                self.free(int(run[0]), len(run))
+
     def step_group(self, g: int, sel: torch.Tensor, out: torch.Tensor, entry_row: torch.Tensor,
                    req_off: torch.Tensor, layer_ready=None, stream: torch.cuda.Stream | None = None):
         """sel: device int32 view of uint32 [R][Q][k]; out: device uint8 [L][cap][W]."""

@@ -1056,11 +1056,11 @@ extern "C" int ula_rows_attend_tree(const ula_attend_args *args, const int32_t *
   if (!args) return ULA_ERR_INVALID_ARG;
   AttendParams p{};
   p.a = *args;
-  if (!arguments_hold(p.a)) return ULA_ERR_INVALID_ARG;
-  Plan pl;
-  if (!plan_tree(p.a.n_req, p.a.n_q, p.a.heads, p.a.k, flags, &pl)) return ULA_ERR_INVALID_ARG;
+  if (!arguments_hold(p.a) || p.a.n_q > ULA_MAX_TREE || (flags & ~ULA_TREE_SHARED_LIST)) return ULA_ERR_INVALID_ARG;
   if (p.a.n_req == 0 || p.a.n_q == 0 || p.a.heads == 0) return ULA_OK;
   if (!p.a.own_rows || !parent || !aligned(parent, 4)) return ULA_ERR_INVALID_ARG;
+  Plan pl;
+  if (!plan_tree(p.a.n_req, p.a.n_q, p.a.heads, p.a.k, flags, &pl)) return ULA_ERR_INVALID_ARG;
   if (pl.workspace && (!p.a.workspace || p.a.workspace_bytes < pl.workspace)) return ULA_ERR_INVALID_ARG;
   p.parent = parent, p.nodes = p.a.n_q, p.node_heads = p.a.heads;
   if (flags & ULA_TREE_SHARED_LIST) p.a.heads *= p.a.n_q, p.a.n_q = 1;

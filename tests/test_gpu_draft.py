@@ -926,3 +926,48 @@ def test_score_gives_up(R, Q, H, K, barrier):
     got = rows.score(before.clone(), *case, SCALE)
     rows.sync()
     assert torch.equal(got, want)
+
+
+def test_draft_tree_example():
+    """The operators with the cache, as drafted steps use them, against a dense computation in 64 bits.
+    Outputs are averages of normed latents (at most 6 * 1.5, a weight's spread included): rounded to bf16, with
+    the probabilities' 2^-8: off by at most 2 * 2^-8 * 9.  An address's score is a sum of at most
+    steps * nodes * layers * groups * heads weights of at most 1, each off by less than 2^-14 of itself (a
+    logit's error is below 2^-20 * 576 * 9 * 9 * scale), added up in 32 additions in fp32."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_tree.py")
+    spec = importlib.util.spec_from_file_location("draft_tree", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    steps = 3
+    err, off = example.run(steps=steps, seed=1, check=True)
+    most = steps * example.NODES * example.LAYERS * example.GROUPS * example.HEADS
+    assert err <= 2 * 2.0 ** -8 * 9
+    assert off <= most * 2.0 ** -10
+
+
+def test_free_each():
+    """What evict drops goes to the cache in any order; the rest stays."""
+    from serving_step_sparse_gb300 import ula
+    from serving_step_sparse_gb300.cache import UlaCache
+    cache = UlaCache(row_bytes=16, layers_per_group=[1], gpu_slots=40, host_slots=40, ring_buckets=2, max_logical=100, max_entries=80)
+    try:
+        data = torch.arange(60 * 16, dtype=torch.int32).to(torch.uint8).cuda()
+        assert cache.alloc(60, data) == 0
+        gone = [7, 3, 4, 5, 59, 0, 41]
+        cache.free_each(torch.tensor([[-1] + gone], dtype=torch.int32, device="cuda"))
+        cache.free_each(torch.tensor([], dtype=torch.int32))
+        stay = [a for a in range(60) if a not in gone]
+        out, entry = cache.out_buffer(0, 60), torch.empty(len(stay), dtype=torch.int32, device="cuda")
+        off = torch.empty(2, dtype=torch.int32, device="cuda")
+        cache.step_group(0, torch.tensor(stay[:38], dtype=torch.int32, device="cuda").view(1, 1, -1), out, entry, off)
+        cache.sync()
+        assert torch.equal(out[0, :38], data.view(60, 16)[stay[:38]])
+        for bad in (gone[0], 60):
+            with pytest.raises(ula.UlaError):
+                cache.free_each(torch.tensor([bad], dtype=torch.int32))
+        assert cache.alloc(7, data[:7 * 16].clone()) == 60
+        cache.sync()
+    finally:
+        cache.close()

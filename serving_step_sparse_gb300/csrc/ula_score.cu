@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       for (uint32_t j = 0; j < 4; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row[j >> 1] + at + (j & 1) * 64));
       return true;
     };
+    uint32_t empty = 0;  // whether the next piece's stage is
     auto piece = [&](uint4 (&raw)[4], uint32_t g) -> bool {
       const uint32_t b = g % kPieces, st = g % S;
-      if (g >= S && !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1)) return false;
+      if (g >= S && !__all_sync(0xffffffffu, empty) && !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1)) return false;
       tc_fence_after();
       const uint32_t stage = mine + st * 64;
       if (b == 4) {
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
           tmem_st_16x32(stage + 32 * i, v);
         }
       }
+      empty = mbar_ended(bar(kBarEmpty + (g + 1) % S), ((g + 1) / S & 1) ^ 1);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -356,8 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
         if (b < 2) ++items;
         ok = ok && warp_wait(bar(kBarQuery + b), (items - 1) & 1);
       }
-      ok = ok && warp_wait(bar(kBarFull + st), (g / S) & 1);
-      if (g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
+      const uint32_t ready = g >= kBufs ? mbar_ended(bar(kBarFull + st), (g / S) & 1, bar(kBarDrained + buf), (g / kBufs & 1) ^ 1) : 0;
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = ok && warp_wait(bar(kBarFull + st), (g / S) & 1);
+        if (g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
+      }
       tc_fence_after();
       const uint64_t db = queries + b * (2 * NC * 128 >> 4);
       const uint32_t a = tmem + kBufs * NC + st * 64;
@@ -396,35 +401,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
         }
       }
     };
+    // (a tile's scales are stored when the next one's rows are known: waiting for them here made this warp the
+    // slowest, 5,000 clocks a tile)
+    float4 scale[4];
+    auto store_scales = [&](uint32_t n) {
+      float4 *to4 = reinterpret_cast<float4 *>(sm + L::scale) + n % kTiles * kTile + lane;
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) to4[32 * j] = scale[j];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarScale + n % kTiles));
+    };
     if (count) fetch();
     for (uint32_t n = 0; n < count; ++n) {
       const uint32_t at = n % kTiles;
       if (n >= kTiles && !(ok = warp_wait(bar(kBarFree + at), (n / kTiles & 1) ^ 1))) break;
       uint64_t row[4];
-      float4 scale[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {
         const bool in = (uint32_t)u[j] < p.a.n_rows && (uint32_t)to[j] < p.a.n_scores;
         row[j] = in ? (uint64_t)p.a.rows + (uint64_t)(uint32_t)u[j] * ULA_ROW_BYTES : (uint64_t)p.a.q;
         reinterpret_cast<uint64_t *>(sm + L::place)[at * kTile + lane + 32 * j] = row[j];
         reinterpret_cast<uint32_t *>(sm + L::target)[at * kTile + lane + 32 * j] = in ? (uint32_t)to[j] : 0xffffffffu;
-        scale[j] = __ldg(reinterpret_cast<const float4 *>(row[j] + ULA_ROW_LATENT));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarPlace + at));
+      if (n) store_scales(n - 1);
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) scale[j] = __ldg(reinterpret_cast<const float4 *>(row[j] + ULA_ROW_LATENT));
+      step();
+      if (n + 1 < count) fetch();
       if (n) {  // into L2 ahead of the loads, by lines: a bulk prefetch of a row takes its engine 64 clocks
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j)
 #pragma unroll
           for (uint32_t i = 0; i < ULA_ROW_BYTES; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + i));
       }
-      step();
-      if (n + 1 < count) fetch();
-#pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) reinterpret_cast<float4 *>(sm + L::scale)[at * kTile + lane + 32 * j] = scale[j];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarScale + at));
     }
+    if (count && ok) store_scales(count - 1);
   }
   if (warp == kEnd + kWiden + kIssue + 1) {
     // ---- an item's queries, once the products that read the last one's have ended; a tile's sums, as whole

@@ -355,8 +355,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           const uint32_t par = n & 1;
           // (new to the compiler in every tile: it would keep 68 descriptors in registers otherwise)
           asm volatile("" : "+l"(k_rows), "+l"(k_channels), "+l"(q_rows));
-          ok = ok && warp_wait(bar(kBarFull + 1), par);
-          ok = ok && warp_wait(bar(kBarFull + 2), par);  // (every warp's queries)
+          ok = ok && warp_wait(bar(kBarFull + 1), par, bar(kBarFull + 2), par);  // (every warp's queries)
           issue_s(1);
           ok = ok && warp_wait(bar(kBarFull), par);
           issue_s(0);
@@ -384,13 +383,11 @@ k_attend(const __grid_constant__ AttendParams p) {
         for (uint32_t n = 0; n < count; ++n) {
           const uint32_t par = n & 1;
           asm volatile("" : "+l"(k_rows), "+l"(q_rows));
-          ok = ok && warp_wait(bar(kBarFull + 1), par);  // (every warp's queries)
-          ok = ok && warp_wait(bar(kBarFull + 2), par);
+          ok = ok && warp_wait(bar(kBarFull + 1), par, bar(kBarFull + 2), par);  // (every warp's queries)
           issue_s(2);
           ok = ok && warp_wait(bar(kBarFull + 3), par);
           issue_s(3);
-          ok = ok && warp_wait(bar(kBarFull + 4), par);
-          ok = ok && warp_wait(bar(kBarDrained), par);   // (block 1's columns have been read)
+          ok = ok && warp_wait(bar(kBarFull + 4), par, bar(kBarDrained), par);  // (block 1's columns have been read)
           issue_s(4);
         }
       }
@@ -567,18 +564,18 @@ k_attend(const __grid_constant__ AttendParams p) {
         for (uint32_t j = 0; j < kSlots; ++j) raw1[j] = raw2[j];
       }
       if (!ok) break;
-      // this row's scales, and whether there is a row
-      if (!(ok = warp_wait(bar(kBarScale), par))) break;
+      // this row's scales, and whether there is a row; block 1's product (and the next tile's rows)
+      const bool more = n + 1 < count;
+      ok = more ? warp_wait(bar(kBarScale), par, bar(kBarS + 1), par, bar(kBarPlace), par ^ 1) : warp_wait(bar(kBarScale), par, bar(kBarS + 1), par);
+      if (!ok) break;
       float4 scale = *reinterpret_cast<const float4 *>(sm + L::scale + mine * 16);
       const bool present = reinterpret_cast<const uint64_t *>(sm + L::place)[par * kTile + mine] != 0;
-      const bool more = n + 1 < count;
 
       // ---- logits in units of log2, this thread's row and HG heads: the scales carry c0.
       // Block 1's part comes first, so that the rope's product can take its columns.
       float z[HG];
       {
         float v[HG];
-        if (!(ok = warp_wait(bar(kBarS + 1), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, v);
         tc_wait_ld();
@@ -589,12 +586,10 @@ k_attend(const __grid_constant__ AttendParams p) {
 #pragma unroll
         for (int h = 0; h < HG; h += 2) mul2(z[h], z[h + 1], s, v[h], v[h + 1]);
       }
-      if (more && !(ok = warp_wait(bar(kBarPlace), par ^ 1))) break;
       if (more) fetch(raw1, n + 1, block1, 0);
       {
         float v[HG], x[HG];
-        ok = warp_wait(bar(kBarS + 2), par);
-        if (!(ok = ok && warp_wait(bar(kBarS), par))) break;
+        if (!(ok = warp_wait(bar(kBarS + 2), par, bar(kBarS), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + 2 * NH + grp * HG, v);
         tmem_ld<HG>(lanes + kColS + grp * HG, x);
@@ -605,8 +600,7 @@ k_attend(const __grid_constant__ AttendParams p) {
           fma2(z[h], z[h + 1], s, v[h], v[h + 1]);
           fma2(z[h], z[h + 1], t, x[h], x[h + 1]);
         }
-        ok = warp_wait(bar(kBarS + 3), par);
-        if (!(ok = ok && warp_wait(bar(kBarS + 4), par))) break;
+        if (!(ok = warp_wait(bar(kBarS + 3), par, bar(kBarS + 4), par))) break;
         tc_fence_after();
         tmem_ld<HG>(lanes + kColS + 3 * NH + grp * HG, v);
         tmem_ld<HG>(lanes + kColS + NH + grp * HG, x);

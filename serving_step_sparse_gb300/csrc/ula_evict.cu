@@ -63,7 +63,7 @@ __host__ __device__ __forceinline__ uint32_t run_of(uint32_t n, uint32_t blocks)
 }
 
 struct Smem {
-  uint32_t hist[2][kBins];      // the first pass's of this block; in the first block, the sum of a pass
+  uint32_t hist[2][kBins];      // a pass's of this block; in the first block, their sum
   uint32_t warp[kWarps];        // a scan's sums
   uint2 found[3];               // a pass's digit, and how many keys below it
   uint2 sums[kWarps][kMostCluster];  // the runs' (less, equal)
@@ -132,25 +132,10 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
     for (uint32_t pass = 0; pass < 3; ++pass) {
       const uint32_t shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, mask = pass == 2 ? 1023 : 2047;
       // Many scores may be equal (addresses that were never selected have 0), and adding to one place takes
-      // a lane after the other: zeros are counted in a register, and so is a run of equal digits.
-      uint32_t held = 0, times = 0;
-      const uint32_t sums = remote(smem_u32(&s.hist[1][0]), 0);
-      auto add = [&](uint32_t digit, uint32_t by) {  // few keys are left after the first pass: straight to the sums
-        if (pass == 0) atomicAdd(&s.hist[0][digit], by);
-        else if (kCluster) add_remote(sums + 4 * digit, by);
-        else atomicAdd(&s.hist[1][digit], by);
-      };
-      auto flush = [&] {
-        if (times) add(held, times);
-      };
+      // a lane after the other: zeros are counted in a register.
       auto count = [&](uint32_t k) {
-        const uint32_t digit = (k >> shift) & mask;
-        if (pass == 0 && k == kZero) {
-          ++zeros;
-        } else if (pass == 0 || ((k >> (pass == 1 ? 21 : 10)) == digits && k != kZero)) {
-          if (digit != held) flush(), held = digit, times = 0;
-          ++times;
-        }
+        if (pass == 0 && k == kZero) ++zeros;
+        else if (pass == 0 || ((k >> (pass == 1 ? 21 : 10)) == digits && k != kZero)) atomicAdd(&s.hist[0][(k >> shift) & mask], 1u);
       };
       if (pass == 0) {
         // sixteen gathers in flight, and the addresses of the next sixteen
@@ -178,16 +163,16 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
           for (uint32_t j = 0; j < 4; ++j) count(k[j]);
         }
       }
-      flush();
-      if (lane == 0 && zeros && (pass == 0 || (kZero >> (pass == 1 ? 21 : 10)) == digits)) add((kZero >> shift) & mask, zeros);
-      if (pass == 0) {
-        __syncthreads();
+      if (lane == 0 && zeros && (pass == 0 || (kZero >> (pass == 1 ? 21 : 10)) == digits))
+        atomicAdd(&s.hist[0][(kZero >> shift) & mask], zeros);
+      __syncthreads();
+      const uint32_t sums = remote(smem_u32(&s.hist[1][0]), 0);
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-          const uint32_t d = threadIdx.x + i * kThreads, by = s.hist[0][d];
-          if (!kCluster) s.hist[1][d] = by;
-          else if (by) add_remote(sums + 4 * d, by);
-        }
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t d = threadIdx.x + i * kThreads, by = s.hist[0][d];
+        s.hist[0][d] = 0;
+        if (!kCluster) s.hist[1][d] = by;
+        else if (by) add_remote(sums + 4 * d, by);
       }
       meet();
       if (rank == 0) {  // the digit where the count of smaller keys passes what is still to leave
@@ -255,9 +240,10 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
   const uint32_t ties = leave - below;  // equal keys that leave: the first ones
   int32_t *kept = p.kept + (uint64_t)req * p.budget, *dropped = p.dropped + (uint64_t)req * p.dropped_room;
   const uint32_t before = (1u << lane) - 1;
+  uint32_t gone = less + (equal < ties ? equal : ties);  // what leaves of the places before these
   for (uint32_t i0 = run0; i0 < run1; i0 += 256) {
     int32_t now[8];
-    uint32_t ls[8], eq[8];
+    uint32_t leaves[8];
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) now[j] = a[j];
     addresses(i0 + 256, a);
@@ -266,19 +252,22 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
       const uint32_t i = i0 + 32 * j + lane;
       uint32_t k = kStays;
       if (leave && i < run1) k = p.cached ? mine[i - run0] : key_at(i, score(now[j]));
-      ls[j] = __ballot_sync(0xffffffffu, k < limit), eq[j] = __ballot_sync(0xffffffffu, k == limit);
+      leaves[j] = __ballot_sync(0xffffffffu, k < limit);
+      const uint32_t same = __ballot_sync(0xffffffffu, k == limit);
+      if (same) {  // (the first of them, so many as may)
+        const uint32_t may = equal < ties ? ties - equal : 0;
+        leaves[j] |= __ballot_sync(0xffffffffu, k == limit && __popc(same & before) < may);
+        equal += __popc(same);
+      }
     }
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) {
-      const uint32_t i = i0 + 32 * j + lane;
-      const uint32_t ee = equal + __popc(eq[j] & before);
-      const uint32_t gone = less + __popc(ls[j] & before) + (ee < ties ? ee : ties);  // before this place
-      const bool goes = (ls[j] >> lane & 1) || ((eq[j] >> lane & 1) && ee < ties);
+      const uint32_t i = i0 + 32 * j + lane, at = gone + __popc(leaves[j] & before);
       if (i < run1) {
-        if (goes) dropped[gone] = now[j];
-        else kept[i - gone] = now[j];
+        if (leaves[j] >> lane & 1) dropped[at] = now[j];
+        else kept[i - at] = now[j];
       }
-      less += __popc(ls[j]), equal += __popc(eq[j]);
+      gone += __popc(leaves[j]);
     }
   }
   for (uint32_t i = n - leave + rank * kThreads + threadIdx.x; i < p.budget; i += blocks * kThreads) kept[i] = -1;

@@ -51,11 +51,9 @@ struct Image {
 template <uint32_t NC>
 __global__ void __launch_bounds__(256) k_score_prepare(const __grid_constant__ ScoreParams p) {
   after_previous();
-  const uint64_t n = (uint64_t)p.lists * p.a.k;
-  for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (uint64_t)gridDim.x * 256) {
-    const uint32_t a = (uint32_t)__ldg(p.a.address + e);
-    if (a < p.a.n_scores) p.sums[a] = 0;
-  }
+  const uint64_t n = (uint64_t)p.lists * p.a.k, stride = (uint64_t)gridDim.x * 256;
+  uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  uint32_t a = e < n ? (uint32_t)__ldg(p.a.address + e) : 0xffffffffu;  // (on its way beside the first queries)
   const uint32_t lane = threadIdx.x & 31, columns = p.nodes * p.a.heads, per_list = p.column_tiles * NC;
   const uint64_t all = (uint64_t)p.lists * per_list;
   for (uint64_t i = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < all; i += (uint64_t)gridDim.x * 8) {
@@ -102,18 +100,26 @@ __global__ void __launch_bounds__(256) k_score_prepare(const __grid_constant__ S
       reinterpret_cast<float *>(image + Image<NC>::factor)[h] = __int_as_float((127 - up) << 23);
     }
   }
+  for (; e < n; e += stride) {
+    if (a < p.a.n_scores) p.sums[a] = 0;
+    a = e + stride < n ? (uint32_t)__ldg(p.a.address + e + stride) : 0xffffffffu;
+  }
 }
 
-// (Two calls that update the same scores at once: each adds its own sums.)
+// (Two calls that update the same scores at once: each adds its own sums.)  The addresses are read before the
+// kernel before this one ends: it has waited for what came before it, so that nothing writes them any more.
 __global__ void __launch_bounds__(256) k_score_commit(const __grid_constant__ ScoreParams p) {
-  after_previous();
-  const uint64_t n = (uint64_t)p.lists * p.a.k;
+  const uint64_t n = (uint64_t)p.lists * p.a.k, stride = (uint64_t)gridDim.x * 256;
   const double scale = 1.0 / (double)p.unit;
-  for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (uint64_t)gridDim.x * 256) {
-    const uint32_t a = (uint32_t)__ldg(p.a.address + e);
-    if (a >= p.a.n_scores) continue;
-    const unsigned long long s = atomicExch(p.sums + a, 0ull);
-    if (s) atomicAdd(p.a.scores + a, (float)((double)s * scale));
+  uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  uint32_t a = e < n ? (uint32_t)__ldg(p.a.address + e) : 0xffffffffu;
+  after_previous();
+  for (; e < n; e += stride) {
+    if (a < p.a.n_scores) {
+      const unsigned long long s = atomicExch(p.sums + a, 0ull);
+      if (s) atomicAdd(p.a.scores + a, (float)((double)s * scale));
+    }
+    a = e + stride < n ? (uint32_t)__ldg(p.a.address + e + stride) : 0xffffffffu;
   }
 }
 
@@ -221,7 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
   auto step = [&]() {
     if (++w.tile == p.tiles) w.tile = 0, ++w.item;
   };
-  after_previous();
+  // The kernel before this one (k_score_prepare) has waited for all before it, so the rows, entries and
+  // addresses stand; who touches the sums and the images waits for it.
+  if (warp == kEnd + kWiden + kIssue + 1) after_previous();
 
   bool ok = true;  // false once a wait has run out
   if (warp < kEnd) {

@@ -403,7 +403,9 @@ int ula_dedup_noalloc(const uint32_t *d_sel, uint32_t n, uint32_t *d_uniq,
  * What a model does with the cache's FP8 rows, beside the residency calls above: it
  * packs a token's latents and rope channels into a row (the input of ula_alloc),
  * turns its queries' rope channels, attends over the rows that a step gathered, and
- * joins partial results over disjoint rows (TP mode's local and remote rows).  A row is
+ * joins partial results over disjoint rows (TP mode's local and remote rows); norms
+ * queries and keys on the way; attends for trees of drafted tokens; accumulates the
+ * attention's weights by logical address and evicts by them.  A row is
  * ULA_ROW_BYTES bytes, 16-byte aligned: 512 e4m3 codes (the latent), 4 fp32 scales (one
  * for each block of 128 channels: channel c stands for scale[c / 128] * code[c]), 64
  * bf16 rope channels.

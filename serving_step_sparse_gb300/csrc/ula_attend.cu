@@ -82,7 +82,8 @@ struct Shared {
   static constexpr uint32_t k = kGroups * NH * 128;           // [9][128][128 B]
   static constexpr uint32_t scale = k + kGroups * kGroupBytes;  // [128][4] the rows' scales
   static constexpr uint32_t place = scale + kTile * 16;       // [2][128] the rows' addresses, 0: no row
-  static constexpr uint32_t top = place + 2 * kTile * 8;      // [NH][4] tile maxima (then sums) by quadrant
+  static constexpr uint32_t sees = place + 2 * kTile * 8;     // [2][128] (a tree) which columns see them
+  static constexpr uint32_t top = sees + 2 * kTile * 8;       // [NH][4] tile maxima (then sums) by quadrant
   static constexpr uint32_t bars = top + NH * 16;
   static constexpr uint32_t words = bars + 24 * 8;            // TMEM address; first remaining item, its tile; tiles in all
   static constexpr uint32_t bytes = words + 16 + 1024;        // (+ alignment of the base)
@@ -187,43 +188,39 @@ __device__ __forceinline__ void ancestors(const int32_t *parent, uint32_t nodes,
   }
 }
 
-// Masks the logits of a tile with own rows of a tree: a column (node and head) sees the rows of its node
-// and of the node's ancestors.  `codes`: the tile's widened codes, `first` the thread's first column.
-// An own row is in the products of the columns that do not see it too, with a probability of 0, so
-// what it holds must be finite: one with a NaN among its codes (all its logits are NaN) or a scale
-// that is not finite gives NaN to the columns that see it here, and goes on with codes and scales that
-// are.  (Both threads of a row may write its codes: the same values.)
-template <int HG>
-__device__ __forceinline__ void see_tree(const AttendParams &p, const Place &w, uint32_t first, uint32_t mine,
-                                         uint8_t *codes, float (&z)[HG], float4 &scale) {
+// Which columns (nodes and heads, of the item's NH) see a tile's rows e and e + 32: a bit each, as their nodes
+// or ancestors of them; all for the list's rows.
+template <uint32_t NH>
+__device__ __forceinline__ void see_tree(const AttendParams &p, const Place &w, uint32_t e, uint64_t (&sees)[2]) {
   uint64_t seen[2];
   ancestors(p.parent + (uint64_t)w.req * p.nodes, p.nodes, threadIdx.x & 31, seen);
-  const uint32_t e = w.tile * kTile + mine, j = e - p.a.k;
-  const bool own = e >= p.a.k && j < p.nodes;
-  bool bad = own;
-#pragma unroll
-  for (int h = 0; h < HG; ++h) bad = bad && z[h] != z[h];
-  if (own && !(isfinite(scale.x) && isfinite(scale.y) && isfinite(scale.z) && isfinite(scale.w))) bad = true;
-  if (bad) {
-    scale = make_float4(1.f, 1.f, 1.f, 1.f);
-    for (uint32_t i = 0; i < 64; ++i) {  // (any order: the swizzle stays within a row's 128 bytes)
-      uint32_t *at = reinterpret_cast<uint32_t *>(codes + (i >> 3) * kGroupBytes + mine * 128 + (i & 7) * 16);
-      for (uint32_t k = 0; k < 4; ++k) {
-        uint32_t two = at[k];
-        if ((two & 0x7fff0000u) > 0x7f800000u) two &= 0xffffu;
-        if ((two & 0x7fffu) > 0x7f80u) two &= 0xffff0000u;
-        at[k] = two;
-      }
-    }
-  }
-  const uint32_t column = w.h0 + first;
-  uint32_t node = column / p.node_heads, head = column - node * p.node_heads;
+  uint32_t node = w.h0 / p.node_heads, left = (node + 1) * p.node_heads - w.h0;
   node += w.qi;
-#pragma unroll
-  for (int h = 0; h < HG; ++h) {
+  sees[0] = sees[1] = 0;
+#pragma unroll 1
+  for (uint32_t h = 0; h < NH; ++node, left = p.node_heads) {  // (by runs of a node's heads)
     const uint64_t s0 = __shfl_sync(0xffffffffu, seen[0], node & 31), s1 = __shfl_sync(0xffffffffu, seen[1], node & 31);
-    if (own) z[h] = ((node < 32 ? s0 : s1) >> j & 1) == 0 ? -INFINITY : bad ? __int_as_float(0x7fffffff) : z[h];
-    if (++head == p.node_heads) head = 0, ++node;
+    const uint64_t mask = node < 32 ? s0 : s1;
+    const uint32_t n = left < NH - h ? left : NH - h;
+    const uint64_t run = (n < 64 ? (1ull << n) - 1 : ~0ull) << h;
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t at = e + 32 * i, j = at - p.a.k;
+      if (at < p.a.k || j >= p.nodes || (mask >> j & 1)) sees[i] |= run;
+    }
+    h += n;
+  }
+}
+
+// A row's widened codes without their NaN.  (Any order: the swizzle stays within a row's 128 bytes.)
+__device__ __noinline__ void clean_codes(uint8_t *codes) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < 256; ++i) {
+    uint32_t *at = reinterpret_cast<uint32_t *>(codes + (i >> 5) * kGroupBytes) + (i & 31);
+    uint32_t two = *at;
+    if ((two & 0x7fff0000u) > 0x7f800000u) two &= 0xffffu;
+    if ((two & 0x7fffu) > 0x7f80u) two &= 0xffff0000u;
+    *at = two;
   }
 }
 
@@ -251,7 +248,7 @@ __device__ __forceinline__ void see_tree(const AttendParams &p, const Place &w, 
 //
 // kCluster: the tiles of one item spread over the blocks of a cluster, which join their
 // results through each other's shared memory (no second kernel, no trip through L2).
-// kTree: a column is a node and a head, and own rows are masked by the nodes' ancestors (see_tree).
+// kTree: a column is a node and a head, and own rows are masked by the nodes' ancestors.
 template <uint32_t NH, bool kCluster, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend(const __grid_constant__ AttendParams p) {
@@ -410,8 +407,16 @@ k_attend(const __grid_constant__ AttendParams p) {
       };
       auto place_rows = [&](uint32_t par) {
         uint64_t *place = reinterpret_cast<uint64_t *>(sm + L::place) + par * kTile + r0;
+        uint64_t *seen = reinterpret_cast<uint64_t *>(sm + L::sees) + par * kTile + r0;
+        const uint32_t e = w.tile * kTile + r0 + lane;
+        uint64_t sees[2] = {~0ull, ~0ull};
+        if (kTree && (w.tile + 1) * kTile > p.a.k) see_tree<NH>(p, w, e, sees);  // (the tile holds nodes' rows)
 #pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) place[lane + 32 * j] = row_of<kTree>(p, w, w.tile * kTile + r0 + lane + 32 * j, u[j]);
+        for (uint32_t j = 0; j < 2; ++j) {
+          const uint64_t row = row_of<kTree>(p, w, e + 32 * j, u[j]);
+          place[lane + 32 * j] = row;
+          if (kTree) seen[lane + 32 * j] = row ? sees[j] : 0;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPlace));
       };
@@ -615,12 +620,41 @@ k_attend(const __grid_constant__ AttendParams p) {
 
       // A row that is not there gets logits of -inf, whatever the products say: its zeros times a NaN
       // or an infinity of the query are NaN.
-      if (!__all_sync(0xffffffffu, present)) {
+      if (!kTree && !__all_sync(0xffffffffu, present)) {
 #pragma unroll
         for (int h = 0; h < HG; ++h) z[h] = present ? z[h] : -INFINITY;
       }
-      if (kTree && (w.tile + 1) * kTile > p.a.k)  // (the tile holds nodes' rows)
-        see_tree<HG>(p, w, grp * HG, mine, sm + L::k, z, scale);
+      // Of a tree's own rows a column (a node and a head) sees its node's and its ancestors'.  The loading warps
+      // have worked out which: here, unrolled over the columns, that took 11 % of the whole, as it runs once an
+      // item and its instructions are fetched each time.
+      if (kTree) {
+        const uint32_t sees = (uint32_t)(reinterpret_cast<const uint64_t *>(sm + L::sees)[par * kTile + mine] >> (grp * HG));
+        constexpr uint32_t kAll = HG < 32 ? (1u << (HG & 31)) - 1 : 0xffffffffu;
+        // A row that some see and others do not is in the products of both, with a probability of 0 for the
+        // latter, so what it holds must be finite: one with a NaN among its codes (all its logits are NaN) or a
+        // scale that is not finite gives NaN to those who see it here, and goes on with codes and scales that
+        // are.  (Both threads of a row may write its codes: the same values.)
+        if ((w.tile + 1) * kTile > p.a.k) {
+          const bool bad = present && w.tile * kTile + mine >= p.a.k &&
+                           (z[0] != z[0] || !(isfinite(scale.x) && isfinite(scale.y) && isfinite(scale.z) && isfinite(scale.w)));
+          if (__any_sync(0xffffffffu, bad)) {
+            bool all = bad;
+#pragma unroll
+            for (int h = 1; h < HG; ++h) all = all && z[h] != z[h];  // (not a NaN of the first column's query alone)
+            if (bad && !(isfinite(scale.x) && isfinite(scale.y) && isfinite(scale.z) && isfinite(scale.w))) all = true;
+            if (all) {
+              scale = make_float4(1.f, 1.f, 1.f, 1.f);
+              clean_codes(sm + L::k + mine * 128);
+            }
+#pragma unroll
+            for (int h = 0; h < HG; ++h) z[h] = all ? __int_as_float(0x7fffffff) : z[h];
+          }
+        }
+        if (!__all_sync(0xffffffffu, (sees & kAll) == kAll)) {
+#pragma unroll
+          for (int h = 0; h < HG; ++h) z[h] = sees >> h & 1 ? z[h] : -INFINITY;
+        }
+      }
 
       if (more) fetch(raw1, n + 1, block1, 1);
       // ---- running maximum: it moves only when a tile's is more than 8 (a factor of 256)

@@ -139,8 +139,9 @@ __device__ uint32_t g_late;                          // warps whose waits ran ou
 // mbarriers.  Full, Empty: a stage holds a piece, its products have ended; Done, Drained: an
 // accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
 // Free: all three have been read; Sum: the rows' sums stand; Query: the item's queries (of a piece's
-// channels); Idle: the item's products with them have ended; End: an issuing warp's have.  (A wait names its phase by its parity alone, so
-// whoever waits for a phase has waited for the one before it, or for a later one of those who opened that.)
+// channels); Idle: the item's products with them have ended; End: an issuing warp's have.  (A wait names
+// its phase by its parity alone, so whoever waits for a phase has waited for the one before it, or for a
+// later one of those who opened that.)
 constexpr uint32_t kTiles = 4;                       // tiles whose addresses, scales and sums stand at once
 enum {
   kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kMostBufs,
@@ -180,7 +181,14 @@ struct Place {
 // and one adds the rows' sums to those in memory.
 // The widened rows stand in TMEM, as the products' A: through shared memory a product of K = 16 read 8 KB of
 // operands at what shared memory gives in all (118 B a clock), and every other access of the widening
-// waited for it; now it reads the queries' 4 KB.
+// waited for it; now it reads the queries' 4 KB (96 tokens, 2,048 rows, 128 heads, the three kernels and
+// a copy of the scores: 77 us before, 61 after).
+//
+// What bounds it: hand-overs.  A tile takes some 6,800 clocks (the case above: 40 us of 57, 0.73 PFLOP/s),
+// its 36 products 2,300; the widening warps need 5,000 to 7,000 and the finishing ones 5,000, most of it in
+// barriers that answer after 150 to 250 clocks.  (57 us; 16 finishing warps of a quarter of the columns 62,
+// for want of registers; 4 stages with 2 accumulators, or 3 with 2, the same within 1 %.)  Item tiles of up
+// to 128 columns: the rows are widened once for all of them.
 template <uint32_t NC>
 __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ ScoreParams p) {
   extern __shared__ uint8_t raw_smem[];

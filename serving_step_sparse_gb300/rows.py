@@ -1,10 +1,14 @@
-"""Operators on the cache's FP8 rows: rotary positions, packing, attention, joining.
+"""Operators on the cache's FP8 rows: rotary positions, packing, attention, joining, eviction.
 
 A row is 656 bytes: 512 e4m3 codes (the latent), 4 fp32 scales (one for each block of
 128 channels), 64 bf16 rope channels.  A decode layer packs its new tokens into rows
 (``pack``, whose rows go to ``UlaCache.alloc``), turns its queries' rope channels
 (``rotate``), attends over the rows that ``UlaCache.step_group`` gathered (``attend``) and
-joins partial results over disjoint rows (``join``: ``UlaTP``'s local and remote rows).
+joins partial results over disjoint rows (``join``: ``UlaTP``'s local and remote rows).  Where
+queries and keys are normed first, ``norm_rotate`` and ``pack_norm`` do that in the same pass; where
+a step verifies a tree of drafted tokens, ``attend_tree`` is its attention; and where a request has a
+budget, ``score`` accumulates the attention's weights by logical address and ``evict`` picks those that
+leave (for ``UlaCache.free_each``).
 
 Every step runs in the CUDA library through the C ABI; ``_build/_rows.so`` checks and marshals
 the arguments (in C++: a decode step makes four of these calls per layer).  Calls run on
@@ -218,7 +222,7 @@ def evict(scores: torch.Tensor, address: torch.Tensor, length: torch.Tensor, bud
 
 def sync(stream: torch.cuda.Stream | None = None) -> None:
     """Waits for the stream (default: the current one).  Raises ``ula.UlaError`` if a bounded wait of
-    an ``attend`` on the stream's device, on this stream or another, has run out since this
+    an ``attend``, ``attend_tree`` or ``score`` on the stream's device, on this stream or another, has run out since this
     stream's last sync; the call's outputs are then not valid."""
     s = stream if stream is not None else torch.cuda.current_stream()
     with torch.cuda.device(s.device):

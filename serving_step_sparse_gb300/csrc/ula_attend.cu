@@ -530,16 +530,22 @@ k_attend(const __grid_constant__ AttendParams p) {
     // the queries of w's item
     auto load_queries = [&]() {
       const __nv_bfloat16 *q = (const __nv_bfloat16 *)p.a.q + w.req * p.a.q_req_stride + w.qi * p.a.q_tok_stride;
-      for (uint32_t i = threadIdx.x; i < NH * 72; i += kWarps * 32) {
+      if (kTree) {  // (a warp a column, whose node and head are worked out once)
+        for (uint32_t h = warp; h < NH; h += kWarps) {
+          const bool in = w.h0 + h < p.a.heads;
+          const uint32_t node = (w.h0 + h) / p.node_heads;
+          const __nv_bfloat16 *src = q + (in ? node * p.a.q_tok_stride + (w.h0 + h - node * p.node_heads) * p.a.q_head_stride : 0);
+          const uint32_t dst = base + L::q + (lane >> 3) * (NH * 128) + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+          copy16(dst, src + lane * 8, in ? 16 : 0);
+          copy16(dst + 4 * NH * 128, src + (32 + lane) * 8, in ? 16 : 0);
+          if (lane < 8) copy16(dst + 8 * NH * 128, src + (64 + lane) * 8, in ? 16 : 0);
+        }
+      }
+      for (uint32_t i = threadIdx.x; !kTree && i < NH * 72; i += kWarps * 32) {
         const uint32_t h = i / 72, c = i - h * 72;
         const uint32_t dst = base + L::q + (c >> 3) * (NH * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4);
         const bool in = w.h0 + h < p.a.heads;
-        uint64_t at = (w.h0 + h) * p.a.q_head_stride;
-        if (kTree) {
-          const uint32_t node = (w.h0 + h) / p.node_heads;
-          at = node * p.a.q_tok_stride + (w.h0 + h - node * p.node_heads) * p.a.q_head_stride;
-        }
-        const __nv_bfloat16 *src = q + (in ? at + c * 8 : 0);
+        const __nv_bfloat16 *src = q + (in ? (w.h0 + h) * p.a.q_head_stride + c * 8 : 0);
         copy16(dst, src, in ? 16 : 0);
       }
     };

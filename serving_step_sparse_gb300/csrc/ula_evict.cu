@@ -278,6 +278,11 @@ __global__ void __launch_bounds__(kThreads) k_evict(const __grid_constant__ Evic
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
 
+// Whether n 4-byte words at a and m at b share any.
+bool share(const void *a, uint64_t n, const void *b, uint64_t m) {
+  return n && m && (uintptr_t)a < (uintptr_t)b + 4 * m && (uintptr_t)b < (uintptr_t)a + 4 * n;
+}
+
 }  // namespace
 
 extern "C" int ula_rows_evict(const float *scores, uint32_t n_scores, const int32_t *address, const int32_t *length,
@@ -294,6 +299,12 @@ extern "C" int ula_rows_evict(const float *scores, uint32_t n_scores, const int3
   if (!length || (n_scores && !scores) || (longest && !address) || (budget && !kept) || (p.dropped_room && !dropped) ||
       !aligned4(scores) || !aligned4(address) || !aligned4(length) || !aligned4(kept) || !aligned4(dropped))
     return ULA_ERR_INVALID_ARG;
+  // (A list's blocks write their places while others still read theirs: no output lies in an input.)
+  const uint64_t n_kept = (uint64_t)n_req * budget, n_dropped = (uint64_t)n_req * p.dropped_room;
+  const struct { const void *at; uint64_t n; } inputs[] = {{address, (uint64_t)n_req * longest}, {length, n_req}, {scores, n_scores}};
+  for (const auto &in : inputs)
+    if (share(kept, n_kept, in.at, in.n) || share(dropped, n_dropped, in.at, in.n)) return ULA_ERR_INVALID_ARG;
+  if (share(kept, n_kept, dropped, n_dropped)) return ULA_ERR_INVALID_ARG;
   // 2,048 places a block, 4 a thread, before another joins: a block's passes over its keys then take less
   // than a meeting.  (The case at the top with clusters of 4: 40 us, with 8 39, when it was compared.)
   uint32_t cluster = 1;

@@ -213,7 +213,7 @@ def evict(scores: torch.Tensor, address: torch.Tensor, length: torch.Tensor, bud
     The first ``first`` and the last ``last`` stay, and of the others those with the largest
     scores (float32 [addresses]), min(length, budget) in all; where scores are equal the older ones
     leave.  kept: int32 [R][budget], dropped: int32 [R][max(N - budget, 0)] (for
-    ``UlaCache.free``), in the list's order, -1 behind.
+    ``UlaCache.free_each``), in the list's order, -1 behind; neither may share memory with an input or the other.
     """
     if stream is not None:
         return _on(stream, _rows.evict, scores, address, length, budget, first, last, kept, dropped)

@@ -140,3 +140,20 @@ def test_free_each_merges_runs(monkeypatch):
     cache.free_each(torch.tensor([[5, 4, -1], [9, 6, 20]], dtype=torch.int32))
     cache.free_each(torch.tensor([-1, -1], dtype=torch.int32))
     assert calls == [(4, 3), (9, 1), (20, 1)]
+
+
+def test_evict_refuses_shared_memory(ula):
+    """Outputs that lie in an input or in each other, by their last or first element."""
+    lib, none, bad = ula.lib, C.c_void_p(), ula.ERR_INVALID_ARG
+    at = dict(scores=1 << 20, address=2 << 20, length=3 << 20, kept=4 << 20, dropped=5 << 20)
+    size = dict(scores=5, address=2 * 10, length=2, kept=2 * 4, dropped=2 * 6)
+
+    def evict(**kw):
+        v = {k: C.c_void_p(x) for k, x in {**at, **kw}.items()}
+        return lib.ula_rows_evict(v["scores"], C.c_uint32(5), v["address"], v["length"], C.c_uint32(2), C.c_uint32(10), C.c_uint32(4),
+                                  C.c_uint32(1), C.c_uint32(1), v["kept"], v["dropped"], none)
+    for out in ("kept", "dropped"):
+        for other in at:
+            if other != out:
+                for place in (at[other], at[other] + 4 * (size[other] - 1), at[other] - 4 * (size[out] - 1)):
+                    assert evict(**{out: place}) == bad, (out, other, place)

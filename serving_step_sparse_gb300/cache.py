@@ -136,6 +136,8 @@ class UlaCache:
         """Frees single addresses (int32, on any device, in any order; negative ones, such as the pads of
         ``rows.evict``'s dropped, stand for none), one ``free`` for each run of neighbours.  Reads them
         on the host.  Not atomic: an address that is not live raises after earlier runs have gone."""
+        if addresses.dtype not in (torch.int32, torch.int64):
+            raise ValueError("addresses are int32")
         a = np.unique(addresses.detach().cpu().numpy())
         a = a[a >= 0]
         for run in np.split(a, np.flatnonzero(np.diff(a) != 1) + 1):

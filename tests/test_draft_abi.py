@@ -157,3 +157,10 @@ def test_evict_refuses_shared_memory(ula):
             if other != out:
                 for place in (at[other], at[other] + 4 * (size[other] - 1), at[other] - 4 * (size[out] - 1)):
                     assert evict(**{out: place}) == bad, (out, other, place)
+
+
+def test_free_each_refuses_other_types():
+    from serving_step_sparse_gb300.cache import UlaCache
+    for wrong in (torch.zeros(2), torch.zeros(2, dtype=torch.bool), torch.zeros(2, dtype=torch.int16)):
+        with pytest.raises(ValueError):
+            UlaCache.__new__(UlaCache).free_each(wrong)

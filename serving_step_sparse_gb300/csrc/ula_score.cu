@@ -140,8 +140,11 @@ __device__ uint32_t g_late;                          // warps whose waits ran ou
 // accumulator stands, has been read; Place: the rows' addresses and targets stand; Scale: their scales;
 // Free: all three have been read; Sum: the rows' sums stand; Query: the item's queries (of a piece's
 // channels); Idle: the item's products with them have ended; End: an issuing warp's have.  (A wait names
-// its phase by its parity alone, so whoever waits for a phase has waited for the one before it, or for a
-// later one of those who opened that.)
+// its phase by its parity alone, so whoever waits for a phase has to know that the one before it has ended: from
+// a wait of its own or, for an issuing warp, which sees every other piece, from an accumulator that it has
+// waited for, since those are read in the pieces' order and a product is issued after its queries stood.  The
+// queries' last phase may be that of piece g - 5, so an accumulator of piece g - 5 or a later one has to have
+// been read: the one that piece g - 2 waited for, where there are three, else the one that piece g waits for.)
 constexpr uint32_t kTiles = 4;                       // tiles whose addresses, scales and sums stand at once
 enum {
   kBarFull = 0, kBarEmpty = kBarFull + kMostStages, kBarDone = kBarEmpty + kMostStages, kBarDrained = kBarDone + kMostBufs,
@@ -371,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
       const uint32_t n = g / kPieces, b = g - n * kPieces, st = g % S, buf = g % kBufs;
       for (; tile < n; ++tile) step();
       if (n == 0 || w.tile == 0) {
+        static_assert(kBufs <= kPieces, "an accumulator's wait tells that an earlier item's queries stood");
+        if (kBufs + kIssue > kPieces && g >= kBufs) ok = ok && warp_wait(bar(kBarDrained + buf), (g / kBufs & 1) ^ 1);
         if (b < 2) ++items;
         ok = ok && warp_wait(bar(kBarQuery + b), (items - 1) & 1);
       }

@@ -971,3 +971,18 @@ def test_free_each():
         cache.sync()
     finally:
         cache.close()
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("R,Q,H,K", [(700, 1, 20, 100), (640, 1, 64, 128), (610, 1, 128, 40), (620, 2, 16, 5), (615, 2, 32, 77)])
+def test_score_items_of_one_tile(R, Q, H, K, shared):
+    """Four items of one tile or more in every block, for each number of columns: every repetition's bits are the first's."""
+    from serving_step_sparse_gb300 import rows
+    before, *case = score_case(R, Q, H, K, 500, R + K, pads=0.1, shared=shared)
+    want = rows.score(before.clone(), *case, SCALE)
+    check_score(want, score64(before, *case, SCALE))
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        differ += (rows.score(before.clone(), *case, SCALE) != want).sum()
+    rows.sync()
+    assert int(differ) == 0

@@ -986,3 +986,18 @@ def test_score_items_of_one_tile(R, Q, H, K, shared):
         differ += (rows.score(before.clone(), *case, SCALE) != want).sum()
     rows.sync()
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("R,Q,H,K", [(320, 2, 16, 60), (310, 2, 20, 100), (620, 1, 64, 40), (40, 4, 20, 700)])
+def test_tree_repeats_its_bits(R, Q, H, K, shared):
+    """Items of one tile, several in every block, and items that blocks share: every repetition's bits are the first's."""
+    from serving_step_sparse_gb300 import rows
+    q, kv, entry, own, parent = tree_case(R, Q, H, K, 500, R + K, "random", shared, pads=0.1)
+    want = rows.attend_tree(q, kv, entry, SCALE, own, parent)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(50):
+        out, lse = rows.attend_tree(q, kv, entry, SCALE, own, parent)
+        differ += (out != want[0]).sum() + (lse != want[1]).sum()
+    rows.sync()
+    assert int(differ) == 0

@@ -239,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     if (++w.tile == p.tiles) w.tile = 0, ++w.item;
   };
   // The kernel before this one (k_score_prepare) has waited for all before it, so the rows, entries and
-  // addresses stand; who touches the sums and the images waits for it.
+  // addresses stand; who touches the sums and the images waits for it, and so does every warp before it waits
+  // for what depends on them: the limit of those waits is this kernel's alone.
+  auto prepared = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   if (warp == kEnd + kWiden + kIssue + 1) after_previous();
 
   bool ok = true;  // false once a wait has run out
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     const uint32_t quad = warp & 3, grp = warp >> 2, mine = 32 * quad + lane;
     const uint32_t lanes = tmem + (quad << 21) + grp * HG;
     uint32_t items = 0, stands = 0;
+    prepared();
     for (uint32_t n = 0; n < count; ++n, step()) {
       const uint32_t at = n % kTiles, par = n / kTiles & 1;
       if (n == 0 || w.tile == 0) {  // (the lse come with the rope channels)
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     uint32_t empty = 0;  // whether the next piece's stage is
     auto piece = [&](uint4 (&raw)[4], uint32_t g) -> bool {
       const uint32_t b = g % kPieces, st = g % S;
-      if (g >= S && !__all_sync(0xffffffffu, empty) && !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1)) return false;
+      if (g >= S && !__all_sync(0xffffffffu, empty) && (prepared(), !warp_wait(bar(kBarEmpty + st), (g / S & 1) ^ 1))) return false;
       tc_fence_after();
       const uint32_t stage = mine + st * 64;
       if (b == 4) {
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     const uint64_t queries = operand(base + L::q, 16);
     uint32_t items = 0, tile = 0;
     const uint32_t pieces = count * kPieces;
+    prepared();
     for (uint32_t g = which; g < pieces; g += kIssue) {
       const uint32_t n = g / kPieces, b = g - n * kPieces, st = g % S, buf = g % kBufs;
       for (; tile < n; ++tile) step();
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
     if (count) fetch();
     for (uint32_t n = 0; n < count; ++n) {
       const uint32_t at = n % kTiles;
-      if (n >= kTiles && !(ok = warp_wait(bar(kBarFree + at), (n / kTiles & 1) ^ 1))) break;
+      if (n >= kTiles && (prepared(), !(ok = warp_wait(bar(kBarFree + at), (n / kTiles & 1) ^ 1)))) break;
       uint64_t row[4];
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) {

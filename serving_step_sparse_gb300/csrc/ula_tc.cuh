@@ -23,7 +23,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 
 // Bounded: false after 2^18 tries. A try that is not met comes back after 4.0 us on this GPU,
 // whatever time it is given, so a wait that is never met ends after 1.05 s, and any wait that these
-// kernels can meet is shorter than a tenth of a millisecond. The loop is written out because its
+// kernels can meet is shorter than a tenth of a millisecond.  (Waiting for the kernel before has no limit of
+// theirs and comes first.) The loop is written out because its
 // size matters: the compute warps pass through some 15 waits a tile, their code is longer than
 // the instruction caches nearest to them: with a clock read and two ways out in each wait the step
 // of 96 tokens, 128 heads, 2,051 rows took 6 % more when this form came in, and with a limit that is

@@ -583,9 +583,12 @@ int ula_rows_attend_tree(const ula_attend_args *args, const int32_t *parent, uin
  * with the logits z of ula_rows_attend (or its tree's) and the lse that it gave (with own rows, or
  * joined with other parts: the weights are then those of the whole).  Entries whose row is outside
  * [0, n_rows) or whose address is outside [0, n_scores) count for nothing, as do query heads whose
- * lse is -inf; a weight counts as 1 at most, one that is not a number as 0.  An address's weights
- * are summed as whole numbers (the sum does not depend on an order) and added to its score once, in
- * fp32.
+ * lse is -inf; a weight counts as 1 at most, one that is not a number as 0.  A row's weights (of up
+ * to 128 query heads) are summed in fp32.  An address's sums are added up as whole numbers of 2^(-2e),
+ * with 2^(62 - e) the smallest power of two, 4 at least, that is no less than n_req * n_q * heads * k: what
+ * lies below half of that (2^-75 for 96 query tokens of 128 heads and 2,048 entries) is lost, and the sum
+ * does not depend on an order.  It is added to the score once, in fp32.
+ * (n_req * n_q * heads / 16 + n_req * n_q) * (k / 128 + 1), rounded down, may not pass 2^36, nor n_req * n_q * heads 2^31 - 1.
  *   q         : as for ula_rows_attend.
  *   entry_row : device int32 [n_req][n_q][k], or [n_req][k] with ULA_TREE_SHARED_LIST: one list for
  *               a request's query tokens.

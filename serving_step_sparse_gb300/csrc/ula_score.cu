@@ -1,9 +1,11 @@
 // Accumulated attention weights (ula_rows_score): scores[address[e]] += sum over the query heads that
 // select e of exp(z[e] - lse), with the logits z of ula_rows_attend and the lse that it gave.
 //
-// An address may be selected by several query tokens, so its weights are summed as 64-bit whole numbers
-// (a fixed point that no sum of this call's weights can pass), whose sum does not depend on their
-// order; one addition in fp32 per address then updates its score.  Three launches: the first clears the
+// An address may be selected by several query tokens, so its weights are summed as whole numbers, whose sum
+// does not depend on their order; one addition in fp32 per address then updates its score.  A sum has two
+// 64-bit words: units of 2^-e, with e such that no sum of this call's weights passes 2^62, and under them units
+// of 2^-2e for what is left of a row's sum, which only a sum below 2^(24 - e) has (96 tokens, 2,048 rows, 128 heads:
+// e = 37).  The first word's top bit says that there is a second.  Three launches: the first clears the
 // sums at the addresses in question and lays the queries out as the second reads them; the second adds
 // the weights up; in the third each sum is taken by the first entry that finds it.
 #include <cuda_bf16.h>
@@ -17,15 +19,17 @@ using namespace ula_tc;
 
 namespace {
 
+constexpr unsigned long long kRest = 1ull << 63;  // (of a sum's first word)
+
 struct ScoreParams {
   ula_score_args a;
   uint32_t lists, nodes;        // lists, and the query tokens of each
-  unsigned long long *sums;     // [n_scores]
+  ulonglong2 *sums;             // [n_scores]
   unsigned long long total;     // tiles of all items
   uint32_t tiles, column_tiles; // of an item; of a list
   uint8_t *images;              // [lists][column_tiles] the queries as they stand in shared memory
   uint32_t hold;                // (test hook) an mbarrier whose phases never end; kBars: none
-  float c0, unit;               // softmax_scale * log2(e); what 1.0 is in fixed point
+  float c0, unit;               // softmax_scale * log2(e); 2^e
 };
 
 __device__ __forceinline__ void after_previous() {
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(256) k_score_prepare(const __grid_constant__ S
     }
   }
   for (; e < n; e += stride) {
-    if (a < p.a.n_scores) p.sums[a] = 0;
+    if (a < p.a.n_scores) p.sums[a] = make_ulonglong2(0, 0);
     a = e + stride < n ? (uint32_t)__ldg(p.a.address + e + stride) : 0xffffffffu;
   }
 }
@@ -116,8 +120,12 @@ __global__ void __launch_bounds__(256) k_score_commit(const __grid_constant__ Sc
   after_previous();
   for (; e < n; e += stride) {
     if (a < p.a.n_scores) {
-      const unsigned long long s = atomicExch(p.sums + a, 0ull);
-      if (s) atomicAdd(p.a.scores + a, (float)((double)s * scale));
+      const unsigned long long s = atomicExch(&p.sums[a].x, 0ull);
+      if (s) {
+        double v = (double)(s & ~kRest) * scale;
+        if (s & kRest) v += (double)__ldcg(&p.sums[a].y) * scale * scale;
+        atomicAdd(p.a.scores + a, (float)v);
+      }
     }
     a = e + stride < n ? (uint32_t)__ldg(p.a.address + e + stride) : 0xffffffffu;
   }
@@ -496,7 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ S
         float total = 0.f;
 #pragma unroll
         for (uint32_t i = 0; i < kParts; ++i) total += sum[i * kTile + j];
-        if (target[j] != 0xffffffffu && total > 0.f) atomicAdd(p.sums + target[j], __float2ull_rn(total * p.unit));
+        if (target[j] != 0xffffffffu && total > 0.f) {
+          ulonglong2 *to = p.sums + target[j];
+          const float t = total * p.unit, whole = floorf(t), rest = t - whole;  // (all exact)
+          atomicAdd(&to->x, __float2ull_rn(whole));
+          if (rest > 0.f) {
+            atomicAdd(&to->y, __float2ull_rn(rest * p.unit));
+            atomicOr(&to->x, kRest);
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarFree + at));
@@ -572,7 +588,7 @@ namespace {
 // Columns of an item: the fewest that hold a list's, up to 128 (TMEM's four accumulators).
 uint32_t item_columns(uint64_t columns) { return columns <= 32 ? 32 : columns <= 64 ? 64 : 128; }
 uint32_t image_bytes(uint32_t nc) { return nc == 32 ? Image<32>::bytes : nc == 64 ? Image<64>::bytes : Image<128>::bytes; }
-uint64_t sums_bytes(uint32_t n_scores) { return ((uint64_t)n_scores * 8 + 127) & ~127ull; }
+uint64_t sums_bytes(uint32_t n_scores) { return ((uint64_t)n_scores * sizeof(ulonglong2) + 127) & ~127ull; }
 
 }  // namespace
 
@@ -607,13 +623,14 @@ extern "C" int ula_rows_score(const ula_score_args *args, void *stream) {
       (tokens * a.heads / 16 + tokens) * (a.k / 128 + 1ull) > (1ull << 36))
     return ULA_ERR_INVALID_ARG;
   p.lists = shared ? a.n_req : (uint32_t)tokens;
-  p.sums = (unsigned long long *)a.workspace;
+  p.sums = (ulonglong2 *)a.workspace;
   p.images = (uint8_t *)a.workspace + sums_bytes(a.n_scores);
   p.c0 = a.softmax_scale * 1.44269504088896341f;
-  // a weight is at most 1, and an address gets at most one of every entry of every query head
-  int bits = 0;
-  while (bits < 62 && (double)tokens * a.heads * a.k > std::ldexp(1.0, bits)) ++bits;
-  p.unit = std::ldexp(1.f, bits < 3 ? 60 : 63 - bits);
+  // a weight is at most 1, and an address gets at most one of every entry of every query head (and, a row at a
+  // time, as many rests, each of 2^e at most)
+  int bits = 2;
+  while (tokens * a.heads * a.k > 1ull << bits) ++bits;
+  p.unit = std::ldexp(1.f, 62 - bits);
   p.hold = g_hold.load(std::memory_order_relaxed);
   const uint64_t n = (uint64_t)p.lists * a.k, columns = (uint64_t)p.nodes * a.heads;
   cudaStream_t st = (cudaStream_t)stream;

@@ -197,7 +197,8 @@ def score(scores: torch.Tensor, q: torch.Tensor, rows: torch.Tensor, entry_row: 
     address: int32 of entry_row's shape, the selection that ``step_group`` got.  lse: float32
     [R][Q][H], the attention's (joined with other parts: weights of the whole).  Entries whose row or
     address is out of range count for nothing, and so do query tokens whose lse is -inf.  The result does
-    not depend on the order in which an address's weights are added.
+    not depend on the order in which an address's weights are added: they are summed as whole numbers of
+    2^(-2e), with 2^(62 - e) the power of two at or above R * Q * H * K (4 at least), and added to the score once.
     """
     if stream is not None:
         return _on(stream, _rows.score, scores, q, rows, entry_row, address, lse, softmax_scale)

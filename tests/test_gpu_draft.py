@@ -1001,3 +1001,53 @@ def test_tree_repeats_its_bits(R, Q, H, K, shared):
         differ += (out != want[0]).sum() + (lse != want[1]).sum()
     rows.sync()
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("R,Q,H,K", [(1, 1, 1, 300), (2, 3, 40, 500), (8, 3, 64, 2048)])
+@pytest.mark.parametrize("below", [8.0, 20.0, 40.0])
+def test_score_small_weights(R, Q, H, K, below):
+    """Weights of e^-below of an attention's count as others do, beside those of a token whose weights are whole.
+    Each is off by what the head of this file says, without a fixed point's share but for its last unit: a call of n
+    weights, 4 at least, adds whole numbers of 2^-2e with e = 62 - ceil(log2 n), so a row's sum is off by half of one."""
+    from serving_step_sparse_gb300 import rows
+    before, q, kv, entry, address, lse = score_case(R, Q, H, K, K, R + K)
+    lse += below
+    entry[0, 0, : K // 2] = -1
+    lse[0, 0] -= below
+    first = address[0, 0].clone()
+    address[0, 0] = torch.where(first % 2 == 0, first, -1)
+    got = rows.score(torch.zeros_like(before), q, kv, entry, address, lse, SCALE).double().cpu().numpy()
+    rows.sync()
+    lat, rope = unpack(kv)
+    keys, qd, zd = np.concatenate([lat, rope], axis=1), q.double().cpu().numpy(), lse.double().cpu().numpy()
+    e, a = entry.cpu().numpy(), address.cpu().numpy()
+    want, slack = np.zeros(len(got)), np.zeros(len(got))
+    unit = 2.0 ** (-2 * (62 - max(2, math.ceil(math.log2(R * Q * H * K)))))
+    for r in range(R):
+        for i in range(Q):
+            ok = (e[r, i] >= 0) & (a[r, i] >= 0)
+            k, m = keys[e[r, i][ok]], zd[r, i][:, None]
+            z, err = qd[r, i] @ k.T * SCALE, 2.0 ** -20 * SCALE * (np.abs(qd[r, i]) @ np.abs(k).T)
+            p = np.exp(z - m)
+            np.add.at(want, a[r, i][ok], p.sum(0))
+            loss = p * (np.expm1(err + 2.0 ** -22 * (np.abs(z) + np.abs(m))) + 2.0 ** -21 + 2.0 ** -16)
+            np.add.at(slack, a[r, i][ok], loss.sum(0) + unit / 2 * math.ceil(H / 128) + 2.0 ** -126 * H)
+    assert (np.abs(got - want) <= slack + 2.0 ** -23 * want * 1.01).all()
+
+
+def test_score_orders_what_is_hardly_seen():
+    """Addresses whose weights are all small leave by them, not by age."""
+    from serving_step_sparse_gb300 import rows
+    n, heads = 64, 128
+    _, kv, _, _ = attend_case(1, 1, 1, 1, n, 5)
+    q = torch.zeros(16, 1, heads, 576, dtype=torch.bfloat16, device="cuda")
+    order = torch.randperm(n, device="cuda").to(torch.int32)
+    entry = order.expand(16, 1, n).contiguous()
+    # logits of 0: a weight is e^-lse, and the later an address stands in the order the fewer tokens list it
+    for i in range(16):
+        entry[i, 0, n - 4 * i:] = -1
+    lse = torch.full((16, 1, heads), 60.0, device="cuda")
+    scores = rows.score(torch.zeros(n, device="cuda"), q, kv, entry, entry, lse, SCALE)
+    assert (scores > 0).all()
+    kept, dropped = rows.evict(scores, torch.arange(n, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda"), n // 2)
+    assert torch.equal(dropped[0], order[n // 2:].sort().values) and torch.equal(kept[0], order[:n // 2].sort().values)

@@ -482,7 +482,9 @@ int ula_rows_pack(const ula_rotary *rotary, const int32_t *d_pos, uint64_t pos_a
 /*
  * ula_rows_norm_rotate -- query heads (or keys) normed and turned in one pass: for each of n
  * tokens' heads, y = x / sqrt(mean(x^2) + eps) * weight over its `width` channels, then the
- * 64 channels of y from `at` on turned as by ula_rows_rotate.  In fp32, rounded once.
+ * 64 channels of y from `at` on turned as by ula_rows_rotate.  In fp32, the squares' sum too,
+ * rounded once: channels of a head may reach 5e17 (a sum that passes fp32's range is infinite, and the
+ * head becomes zeros), and with an eps below 1e-30 the largest of them may not be under 1e-15.
  *   width    : 64..ULA_MAX_WIDTH; at: 0..width - 64.
  *   d_x      : channel c of head h of token t at d_x[t * x_token_stride + h * x_head_stride + c].
  *   d_weight : [width], of dtype or ULA_TYPE_F32 (weight_dtype).
@@ -500,7 +502,8 @@ int ula_rows_norm_rotate(const ula_rotary *rotary, const int32_t *d_pos, uint64_
 /*
  * ula_rows_pack_norm -- ula_rows_pack with the key's norm in the same pass: the 512 latents
  * become x / sqrt(mean(x^2) + eps) * latent_weight before they are quantised; with a rope
- * weight the 64 rope channels become as much before they are turned.
+ * weight the 64 rope channels become as much before they are turned.  The channels' range is
+ * ula_rows_norm_rotate's.
  *   d_latent_weight, d_rope_weight : [512] and [64], of dtype or ULA_TYPE_F32; the latter
  *                                    NULL: rope channels are not normed.
  */

@@ -119,7 +119,8 @@ def norm_rotate(x: torch.Tensor, weight: torch.Tensor, pos: torch.Tensor, rotary
                 stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Norms the heads of x [tokens][heads][width] (or [tokens][width]; bf16, f16 or f32; width 64 to
     1024) and turns their rope channels, in one pass: y = x / sqrt(mean(x^2) + eps) * weight over
-    a head's channels, then y's channels at..at + 63 (default: the last 64) as by ``rotate``.
+    a head's channels, then y's channels at..at + 63 (default: the last 64) as by ``rotate``.  In float32,
+    sums of squares too: channels up to 5e17 (from 1e-15, a head's largest, where eps is below 1e-30).
 
     weight: [width] of x's type or float32.  pos: int32 [axes][tokens] (or [tokens]).  out: x itself
     (in place) or another tensor of x's shape and type, whose tokens and heads may not share memory.
@@ -135,7 +136,7 @@ def pack_norm(latent: torch.Tensor, rope: torch.Tensor, latent_weight: torch.Ten
               stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """``pack`` with the key's norm in the same pass: the latents become x / sqrt(mean(x^2) + eps) *
     latent_weight before they are quantised, and with rope_weight the rope channels as much before they
-    are turned.  Weights: [512] and [64], of the latent's type or float32."""
+    are turned.  Weights: [512] and [64], of the latent's type or float32.  Channels may be as large as ``norm_rotate``'s."""
     if stream is not None:
         return _on(stream, _rows.pack_norm, latent, rope, latent_weight, pos, rotary.config, eps, rope_weight, rows)
     return _rows.pack_norm(latent, rope, latent_weight, pos, rotary.config, eps, rope_weight, rows)

@@ -1051,3 +1051,51 @@ def test_score_orders_what_is_hardly_seen():
     assert (scores > 0).all()
     kept, dropped = rows.evict(scores, torch.arange(n, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda"), n // 2)
     assert torch.equal(dropped[0], order[n // 2:].sort().values) and torch.equal(kept[0], order[:n // 2].sort().values)
+
+
+RANGE = {"bf16": (5e17, 1e15, 1e-12, 1e-15), "f32": (5e17, 1e15, 1e-12, 1e-15), "f16": (6e4, 1e-4, 6e-8)}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("width", [64, 128, 130, 576, 640, 1024])
+def test_norm_range(width, dtype):
+    """Heads at the ends of the range, and some channels there alone, beside heads of ordinary size.  (1,024 squares
+    of 5e17 are 2.6e38; a square of 1e-15 / 2 is 2^-102, so its least bit of 24 is a normal number's.)"""
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(width)
+    rot, freq, axis = make_rotary(rng, 2, "halves")
+    n, heads, at = 9, 8, width - 64
+    pos = positions(rng, 2, n)
+    pos_d = torch.from_numpy(pos).cuda()
+    x = rng.uniform(0.5, 1, (n, heads, width)) * rng.choice([-1, 1], (n, heads, width))
+    plain = torch.from_numpy(x).to(DT[dtype]).cuda()
+    for i, size in enumerate(RANGE[dtype]):
+        x[i, 1::2] *= size
+        x[i + 4, 2, :3] *= size
+    x = torch.from_numpy(x).to(DT[dtype]).cuda()
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(width)).float().cuda()
+    for eps in (0.0, 1e-30, 1e-6):
+        out = rows.norm_rotate(x, w, pos_d, rot, at=at, eps=eps)
+        check_norm(out, x, w, eps, at, pos, freq, axis, "halves", dtype)
+        assert torch.equal(out[:, 0], rows.norm_rotate(plain, w, pos_d, rot, at=at, eps=eps)[:, 0])
+    if dtype != "f16":
+        assert not rows.norm_rotate(torch.full_like(x, 1e20), w, pos_d, rot, at=at).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_pack_norm_range(dtype):
+    from serving_step_sparse_gb300 import rows
+    rng = np.random.default_rng(3)
+    rot, freq, axis = make_rotary(rng, 2, "adjacent")
+    n = 20
+    x, k = rng.uniform(0.5, 1, (n, 512)), rng.uniform(0.5, 1, (n, 64))
+    for i, size in enumerate(RANGE[dtype]):
+        x[2 * i] *= size
+        k[2 * i + 1] *= size
+        x[2 * i + 1, 100:102] *= size
+    latent, rope = torch.from_numpy(x).to(DT[dtype]).cuda(), torch.from_numpy(k).to(DT[dtype]).cuda()
+    w, rw = torch.from_numpy(1 + 0.3 * rng.standard_normal(512)).float().cuda(), torch.from_numpy(1 + 0.3 * rng.standard_normal(64)).float().cuda()
+    pos = positions(rng, 2, n)
+    for eps in (0.0, 1e-30, 1e-6):
+        got = rows.pack_norm(latent, rope, w, torch.from_numpy(pos).cuda(), rot, rope_weight=rw, eps=eps)
+        check_pack_norm(got, latent, rope, w, rw, eps, pos, freq, axis, "adjacent")

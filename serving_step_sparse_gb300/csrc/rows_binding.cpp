@@ -6,6 +6,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -36,12 +37,14 @@ void check(int code, const char *what) {
 }
 
 // What the objects hold (references, borrowed for the call).  The operators record nothing for
-// autograd: a gradient that is expected would be missing without a word.
+// autograd: a gradient that is expected, or a forward tangent, would be missing without a word.
 const at::Tensor &tensor(PyObject *o) {
   need(THPVariable_Check(o), "the arguments are tensors");
   const at::Tensor &t = THPVariable_Unpack(o);
   need(!t.requires_grad() || !at::GradMode::is_enabled(),
        "no gradient is recorded: detach the tensors that require one, or call under torch.no_grad()");
+  need(!t._fw_grad(/*level=*/0).defined() || !c10::AutogradState::get_tls_state().get_fw_grad_mode(),
+       "no tangent is computed: call on the primals of dual tensors");
   return t;
 }
 bool given(PyObject *o) { return o != Py_None; }

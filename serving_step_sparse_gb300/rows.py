@@ -14,7 +14,8 @@ Every step runs in the CUDA library through the C ABI; ``_build/_rows.so`` check
 the arguments (in C++: a decode step makes four of these calls per layer).  Calls run on
 ``stream`` (default: the current stream of the tensors' device) and return without waiting.
 Wrong shapes, types or devices raise ValueError, errors of the C ABI ``ula.UlaError``.  Nothing
-is recorded for autograd: tensors that require a gradient are refused outside ``torch.no_grad()``.
+is recorded for autograd: tensors that require a gradient are refused outside ``torch.no_grad()``, and so are
+dual tensors of forward-mode differentiation.
 """
 from __future__ import annotations
 

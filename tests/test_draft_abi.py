@@ -164,3 +164,27 @@ def test_free_each_refuses_other_types():
     for wrong in (torch.zeros(2), torch.zeros(2, dtype=torch.bool), torch.zeros(2, dtype=torch.int16)):
         with pytest.raises(ValueError):
             UlaCache.__new__(UlaCache).free_each(wrong)
+
+
+def test_tangents_are_refused(ula):
+    """A dual tensor's tangent would be lost without a word, whichever argument it is."""
+    import torch.autograd.forward_ad as fwd
+    from serving_step_sparse_gb300 import rows
+    rot = rows.Rotary([1.0 / (j + 1) for j in range(32)])
+    pos = torch.zeros(2, dtype=torch.int32)
+    x, latent, rope, w = torch.zeros(2, 64), torch.zeros(2, 512), torch.zeros(2, 64), torch.ones(512)
+    q, kv = torch.zeros(1, 2, 1, 576, dtype=torch.bfloat16), torch.zeros(4, 656, dtype=torch.uint8)
+    entry, own = torch.zeros(1, 2, 4, dtype=torch.int32), torch.zeros(1, 2, 656, dtype=torch.uint8)
+    parent, lse, scores = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, 2, 1), torch.zeros(9)
+    length, out = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 1, 512, dtype=torch.bfloat16)
+    with fwd.dual_level():
+        d = lambda t: fwd.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for f in (lambda: rows.rotate(d(x), pos, rot), lambda: rows.pack(d(latent), rope, pos, rot), lambda: rows.pack(latent, d(rope), pos, rot),
+                  lambda: rows.norm_rotate(d(x), w[:64], pos, rot), lambda: rows.pack_norm(d(latent), rope, w, pos, rot),
+                  lambda: rows.attend(d(q), kv, entry, 0.1), lambda: rows.attend_tree(d(q), kv, entry, 0.1, own, parent),
+                  lambda: rows.join([d(out)], [lse]), lambda: rows.score(d(scores), q, kv, entry, entry, lse, 0.1),
+                  lambda: rows.score(scores, d(q), kv, entry, entry, lse, 0.1), lambda: rows.evict(d(scores), entry[0], length, 2)):
+            with pytest.raises(ValueError, match="tangent"):
+                f()
+    with pytest.raises(ValueError, match="device"):  # (outside: tensors as any others)
+        rows.rotate(x, pos, rot)

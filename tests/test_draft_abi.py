@@ -188,3 +188,18 @@ def test_tangents_are_refused(ula):
                 f()
     with pytest.raises(ValueError, match="device"):  # (outside: tensors as any others)
         rows.rotate(x, pos, rot)
+
+
+def test_free_each_refuses_wide_addresses(monkeypatch):
+    """2^32 + 5 is not address 5; nothing is freed."""
+    from serving_step_sparse_gb300 import cache as module
+    from serving_step_sparse_gb300.cache import UlaCache
+    cache, calls = UlaCache.__new__(UlaCache), []
+    cache.ctx = None
+    monkeypatch.setattr(module.ula.lib, "ula_free", lambda ctx, base, n: calls.append((base, n)) or 0)
+    for wide in (2 ** 32 + 5, 2 ** 32, 2 ** 62):
+        with pytest.raises(ValueError):
+            cache.free_each(torch.tensor([3, wide]))
+    assert calls == []
+    cache.free_each(torch.tensor([-(2 ** 40), 2 ** 32 - 1, 7]))
+    assert calls == [(7, 1), (2 ** 32 - 1, 1)]

@@ -1099,3 +1099,18 @@ def test_pack_norm_range(dtype):
     for eps in (0.0, 1e-30, 1e-6):
         got = rows.pack_norm(latent, rope, w, torch.from_numpy(pos).cuda(), rot, rope_weight=rw, eps=eps)
         check_pack_norm(got, latent, rope, w, rw, eps, pos, freq, axis, "adjacent")
+
+
+def test_draft_tree_example_weights():
+    """Every address's accumulated weights, as a part of them.  Heads and rows are normed (weights below 1.5, codes
+    off by 2^-4), so |z| and sum |q k| * scale are at most 1.5^2 * 17 / 16 * 576 * 192^-0.5 < 100.  A logit is off by
+    2^-20 * 100, and so is the lse, which has 2^-23 * 105 of its own and 2^-16 of its sum; the difference in units of
+    log2 2^-22 * 205, the exponential 2^-21; 20 heads in fp32 are 20 * 2^-24, a score's 3 * 2 * 2 additions 12 * 2^-24:
+    2.9e-4 in all."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_tree.py")
+    spec = importlib.util.spec_from_file_location("draft_tree", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.run(steps=3, seed=1, check=True)[1] <= 2.9e-4

@@ -236,7 +236,7 @@ __device__ __noinline__ void clean_codes(uint8_t *codes) {
 // which its 68 products take 3,500 (their operands' bytes from shared memory, not their
 // arithmetic), its rows 2,700 (82 KB at the 30 B a clock that an SM exchanges with L2, in either
 // direction) and the conversions 1,600.  96 tokens, 2,048 + 3 rows, with the join: 128 heads
-// 120 us (0.46 PFLOP/s), 64 heads 73 us, and 15.5 us for 8 tokens of 64 heads.  (When they were
+// 119 us (0.46 PFLOP/s), 64 heads 72 us, and 15.5 us for 8 tokens of 64 heads.  (When they were
 // compared, before the loads were spread, 16 compute warps of half the registers took 12, 5 and
 // 0.4 us more than 8.)
 //

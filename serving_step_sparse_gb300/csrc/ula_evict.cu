@@ -311,6 +311,7 @@ extern "C" int ula_rows_evict(const float *scores, uint32_t n_scores, const int3
   while (cluster < kMostCluster && longest > cluster * 2048) cluster *= 2;
   if ((uint64_t)n_req * cluster > 0x7fffffffull) return ULA_ERR_INVALID_ARG;
   const uint32_t run = run_of(longest, cluster);
+  // (32 lists of up to 393,216 addresses: 124 us; of 400,000, whose scores are gathered again in every pass, 180)
   p.cached = (uint64_t)run * kWarps <= kMostKeys;
   const uint32_t smem = (uint32_t)sizeof(Smem) + (p.cached ? run * kWarps * 4 : 0);
   auto kernel = cluster > 1 ? k_evict<true> : k_evict<false>;

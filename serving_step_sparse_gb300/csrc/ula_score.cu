@@ -5,7 +5,8 @@
 // does not depend on their order; one addition in fp32 per address then updates its score.  A sum has two
 // 64-bit words: units of 2^-e, with e such that no sum of this call's weights passes 2^62, and under them units
 // of 2^-2e for what is left of a row's sum, which only a sum below 2^(24 - e) has (96 tokens, 2,048 rows, 128 heads:
-// e = 37).  The first word's top bit says that there is a second.  Three launches: the first clears the
+// e = 37).  The first word's top bit says that there is a second, so that few are read: reading it for
+// every entry took 66 us where this takes 55.5.  Three launches: the first clears the
 // sums at the addresses in question and lays the queries out as the second reads them; the second adds
 // the weights up; in the third each sum is taken by the first entry that finds it.
 #include <cuda_bf16.h>
@@ -195,10 +196,11 @@ struct Place {
 // waited for it; now it reads the queries' 4 KB (96 tokens, 2,048 rows, 128 heads, the three kernels and
 // a copy of the scores: 77 us before, 61 after).
 //
-// What bounds it: hand-overs.  A tile takes some 6,800 clocks (the case above: 40 us of 57, 0.73 PFLOP/s),
+// What bounds it: hand-overs.  A tile takes some 6,800 clocks (the case above: 40 us of 55, 0.73 PFLOP/s; 16
+// requests of 16 tokens that share a list of 2,048 rows, 128 heads: 101 us in all, 0.76),
 // its 36 products 2,300; the widening warps need 5,000 to 7,000 and the finishing ones 5,000, most of it in
-// barriers that answer after 150 to 250 clocks.  (57 us; 16 finishing warps of a quarter of the columns 62,
-// for want of registers; 4 stages with 2 accumulators, or 3 with 2, the same within 1 %.)  Item tiles of up
+// barriers that answer after 150 to 250 clocks.  (57 us when they were compared; 16 finishing warps of a quarter
+// of the columns 62, for want of registers; 4 stages with 2 accumulators, or 3 with 2, the same within 1 %.)  Item tiles of up
 // to 128 columns: the rows are widened once for all of them.
 template <uint32_t NC>
 __global__ void __launch_bounds__(kThreads, 1) k_score(const __grid_constant__ ScoreParams p) {
